@@ -383,6 +383,106 @@ int sd_gather_attend_noalloc(const sd_shape* shape, const void* q, const void* K
                              void* stream);
 
 /*
+ * The 4-bit K/V cache: K and V of every token held as 4-bit codes, 144 bytes per
+ * token and KV head where the bf16 rows take 512.  (4-bit uniform codes as in Fathom,
+ * "store as bit planes per channel"; here per token, so that a token's row is
+ * complete as soon as it is written and rows can be read in place by index,
+ * HashAttention 2.5.)  Device arrays owned by the caller:
+ *   k, v: uint8 [B][hkv][n_cap][64]; scale: bf16 [B][hkv][n_cap][8].
+ * A group is 64 consecutive channels of one token's K or V; with m the group's
+ * minimum and s = bf16((max - m) / 15) (fp32 difference and quotient, nearest even; 0
+ * where it is below 2^-100), channel x has the code c = clamp(rint((x - m) / s), 0,
+ * 15) (fp32, ties to even; 0 where s = 0) and stands for c s + m.  The error is at
+ * most s (1/2 + 15 * 2^-8): half a step, and what rounding s to bf16 cuts off at the
+ * top.  A group that holds a value that is not finite, or whose max - m overflows
+ * fp32, stands for NaN (s = m = NaN, codes 0).
+ * The 64 bytes of a row are 16 little-endian 32-bit words; word w holds channels
+ * 64 (w % 2) + 8 (w / 2) + i, i = 0..7, at bits 4i .. 4i + 3.  A token's scale record
+ * is {K: s0, m0, s1, m1, V: s0, m0, s1, m1}.
+ * k, v and scale are 16-byte aligned.
+ */
+typedef struct sd_kv4 {
+  uint8_t* k;
+  uint8_t* v;
+  uint16_t* scale;
+} sd_kv4;
+
+/* Strides in elements of a [B][hkv][m][d] array whose channels are consecutive;
+ * each a multiple of 8 and below 2^40 (that of a dimension of size 1 is ignored). */
+typedef struct sd_strides {
+  int64_t seq;
+  int64_t head;
+  int64_t token;
+} sd_strides;
+
+/*
+ * sd_kv4_write -- quantise tokens into the cache as they are written (a prompt, or
+ * one token per sequence and step).
+ *   K, V: bf16, token t of (sequence b, KV head h) at b * seq + h * head + t * token
+ *   (k_strides, v_strides; NULL: contiguous [B][hkv][m][d]).  Strides may be 0 (a
+ *   broadcast source).  K or V may be NULL (not both): that half of the cache is
+ *   left as it is.
+ *   Token t < min(m, length[b]) of sequence b goes to position first + pos[b] + t of
+ *   its cache; tokens whose position is outside [0, n) are dropped.  pos, length:
+ *   int32 [B] (device), NULL meaning 0 and m.  Positions not written keep what they
+ *   hold.  n is the shape's; hq is not used.
+ *   Errors: SD_ERR_INVALID_ARG for a NULL cache array, a misaligned pointer, bad
+ *   strides, m outside [0, 2^31) or first outside [0, n].  m = 0 does nothing.
+ */
+int sd_kv4_write(const sd_shape* shape, const sd_kv4* cache, const void* K,
+                 const sd_strides* k_strides, const void* V, const sd_strides* v_strides,
+                 int64_t m, int64_t first, const int32_t* pos, const int32_t* length,
+                 void* stream);
+
+/*
+ * sd_kv4_read -- read tokens back as bf16 (to build a key index over the cache, or to
+ * move a sequence): K, V receive bf16(c s + m) (one fp32 fused multiply-add, nearest
+ * even) of the positions that sd_kv4_write with the same arguments would have filled.
+ * Rows of tokens t >= length[b] and of positions outside [0, n) are not written.
+ * Arguments and errors as sd_kv4_write; the strides must not make two rows of an
+ * output overlap (SD_ERR_INVALID_ARG).
+ */
+int sd_kv4_read(const sd_shape* shape, const sd_kv4* cache, void* K, const sd_strides* k_strides,
+                void* V, const sd_strides* v_strides, int64_t m, int64_t first,
+                const int32_t* pos, const int32_t* length, void* stream);
+
+/*
+ * sd_kv4_attend -- decode attention over each sequence's 4-bit cache (the attention
+ * that HashAttention 2.1 starts from: every cached token): for query head g of
+ * sequence b, KV head h = g / G, over the tokens i of [max(begin[b], 0), min(end[b],
+ * n)): z_i = scale * <q_g, k_i>, out = sum_i e^{z_i - m} v_i / sum_i e^{z_i - m}, lse =
+ * m + log(sum_i e^{z_i - m}), k_i and v_i the values that the cache stands for (not
+ * rounded to bf16), sums and softmax in fp32.
+ *   q bf16 [B][hq][d]; begin, end: int32 [B] (device), NULL meaning 0 and n; out fp32
+ *   [B][hq][d]; lse fp32 [B][hq] or NULL.  An empty range gives out = 0, lse = -inf.
+ *   Cache contents outside the range reach no output.  q is finite.
+ *   Workspace: sd_kv4_attend_workspace_size() bytes (device, 16-byte aligned),
+ *   contents need not be initialised; calls sharing a workspace must not overlap.
+ *   Errors: SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED (shape), SD_ERR_WORKSPACE,
+ *   SD_ERR_CUDA.
+ */
+size_t sd_kv4_attend_workspace_size(const sd_shape* shape);
+int sd_kv4_attend(const sd_shape* shape, const void* q, const sd_kv4* cache,
+                  const int32_t* begin, const int32_t* end, float scale, float* out, float* lse,
+                  void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * sd_kv4_gather_attend -- sd_gather_attend over the 4-bit cache (HashAttention 2.1,
+ * GATHER-ATT; 2.5, page size 1): the attention of sd_kv4_attend over the rows I =
+ * idx[b*hkv + h][0 .. min(count, max_count)).
+ *   idx int32 [B*hkv][idx_stride], count int32 [B*hkv] as sd_topk writes them (any
+ *   order; entries outside [0, n) are skipped, an index listed twice counts twice; a
+ *   count below 1 is an empty row: out = 0, lse = -inf).  Other arguments and errors
+ *   as sd_kv4_attend; 0 <= max_count <= idx_stride, max_count < 2^31.
+ *   Workspace: sd_kv4_gather_attend_workspace_size() bytes (device).
+ */
+size_t sd_kv4_gather_attend_workspace_size(const sd_shape* shape, int64_t max_count);
+int sd_kv4_gather_attend(const sd_shape* shape, const void* q, const sd_kv4* cache,
+                         const int32_t* idx, int64_t idx_stride, const int32_t* count,
+                         int64_t max_count, float scale, float* out, float* lse,
+                         void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * sd_offload_gather -- copy each (sequence, KV head, channel j)'s planned
  * prefix (the first plan_j planes, contiguous in the channel-major layout)
  * and channel j's scales from pinned host memory into HBM, with device loads
@@ -589,7 +689,8 @@ const char* sd_last_error(void);
  * SD_IDX_LANDMARK, sd_delta_select and sd_resident_gather to 100; 102 adds
  * sd_device_status, sd_set_fallback_paths and sd_debug_set_device_error; 103 adds
  * SD_PLAN_SPLIT, sd_shard_candidates, sd_topk_merge, sd_shard_select and
- * sd_attend_combine; 104 adds sd_copy. */
+ * sd_attend_combine; 104 adds sd_copy.  The sd_kv4_* entry points came later under
+ * the same number (nothing else changed): look them up by name. */
 int sd_version(void);
 
 /*

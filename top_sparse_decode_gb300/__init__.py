@@ -34,7 +34,8 @@ __all__ = [
     "sd_topk_merge", "sd_shard_select", "sd_attend_combine",
     "sd_score_topk_workspace_size", "sd_score_topk", "sd_plan_score", "sd_topk_wmax", "sd_copy",
     "sd_select_attend_workspace_size", "sd_select_attend", "sd_hamming_topk_workspace_size",
-    "sd_hamming_topk",
+    "sd_hamming_topk", "Kv4Cache", "sd_kv4_write", "sd_kv4_read", "sd_kv4_attend_workspace_size",
+    "sd_kv4_attend", "sd_kv4_gather_attend_workspace_size", "sd_kv4_gather_attend",
 ]
 
 
@@ -227,6 +228,76 @@ def sd_gather_attend_noalloc(shape: SdShape, q, K, V, idx, idx_stride: int, coun
                                           _ptr(idx), idx_stride, _ptr(count), max_count,
                                           float(scale), _ptr(out), _ptr(lse), _stream(stream)),
            "sd_gather_attend_noalloc")
+
+
+class Kv4Cache:
+    """A 4-bit K/V cache on the device (sd_kv4): k, v uint8 [B][hkv][n_cap][64] and
+    scale bf16 [B][hkv][n_cap][8], given or allocated (zeros: every token stands for 0)."""
+
+    def __init__(self, batch: int, hkv: int, n_cap: int, device="cuda", k=None, v=None,
+                 scale=None):
+        dims = (batch, hkv, n_cap)
+        self.k = torch.zeros((*dims, 64), dtype=torch.uint8, device=device) if k is None else k
+        self.v = torch.zeros((*dims, 64), dtype=torch.uint8, device=device) if v is None else v
+        self.scale = (torch.zeros((*dims, 8), dtype=torch.bfloat16, device=device)
+                      if scale is None else scale)
+        for t, nbytes in ((self.k, 64), (self.v, 64), (self.scale, 16)):
+            if t.numel() * t.element_size() != batch * hkv * n_cap * nbytes:
+                raise ValueError("Kv4Cache: an array's size does not match batch, hkv, n_cap")
+        self.c = _abi.SdKv4(_ptr(self.k), _ptr(self.v), _ptr(self.scale))
+
+
+def _rows(t, shape: SdShape, m: int):
+    """(pointer, strides) of a [B][hkv][>= m][128] tensor of any strides with consecutive
+    channels; other contiguous tensors and addresses are taken as [B][hkv][m][128]."""
+    if isinstance(t, torch.Tensor) and t.dim() == 4:
+        if tuple(t.shape[:2]) != (shape.batch, shape.hkv) or t.shape[2] < m or t.shape[3] != shape.d:
+            raise ValueError(f"expected [{shape.batch}][{shape.hkv}][>= {m}][{shape.d}] rows, "
+                             f"got {tuple(t.shape)}")
+        if t.stride(3) != 1:
+            raise ValueError("libsd takes rows of consecutive channels")
+        return t.data_ptr(), ctypes.byref(_abi.SdStrides(*t.stride()[:3]))
+    return _ptr(t), None
+
+
+def sd_kv4_write(shape: SdShape, cache: Kv4Cache, K, V, m: int, pos=None, length=None,
+                 first: int = 0, stream=None) -> None:
+    (k, ks), (v, vs) = _rows(K, shape, m), _rows(V, shape, m)
+    _check(lib().sd_kv4_write(ctypes.byref(shape), ctypes.byref(cache.c), k, ks, v, vs, m, first,
+                              _ptr(pos), _ptr(length), _stream(stream)), "sd_kv4_write")
+
+
+def sd_kv4_read(shape: SdShape, cache: Kv4Cache, K, V, m: int, pos=None, length=None,
+                first: int = 0, stream=None) -> None:
+    (k, ks), (v, vs) = _rows(K, shape, m), _rows(V, shape, m)
+    _check(lib().sd_kv4_read(ctypes.byref(shape), ctypes.byref(cache.c), k, ks, v, vs, m, first,
+                             _ptr(pos), _ptr(length), _stream(stream)), "sd_kv4_read")
+
+
+def sd_kv4_attend_workspace_size(shape: SdShape) -> int:
+    return int(lib().sd_kv4_attend_workspace_size(ctypes.byref(shape)))
+
+
+def sd_kv4_attend(shape: SdShape, q, cache: Kv4Cache, scale: float, out, lse=None, workspace=None,
+                  begin=None, end=None, stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().sd_kv4_attend(ctypes.byref(shape), _ptr(q), ctypes.byref(cache.c), _ptr(begin),
+                               _ptr(end), float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+                               ws_bytes, _stream(stream)), "sd_kv4_attend")
+
+
+def sd_kv4_gather_attend_workspace_size(shape: SdShape, max_count: int) -> int:
+    return int(lib().sd_kv4_gather_attend_workspace_size(ctypes.byref(shape), max_count))
+
+
+def sd_kv4_gather_attend(shape: SdShape, q, cache: Kv4Cache, idx, idx_stride: int, count,
+                         max_count: int, scale: float, out, lse=None, workspace=None,
+                         stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().sd_kv4_gather_attend(ctypes.byref(shape), _ptr(q), ctypes.byref(cache.c),
+                                      _ptr(idx), idx_stride, _ptr(count), max_count,
+                                      float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+                                      ws_bytes, _stream(stream)), "sd_kv4_gather_attend")
 
 
 def sd_offload_gather(shape: SdShape, host_planes, host_scales, plan, dev_planes, dev_scales,

@@ -39,10 +39,19 @@ class SdSelect(ctypes.Structure):
                 ("block", ctypes.c_int32)]
 
 
+class SdKv4(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class SdStrides(ctypes.Structure):
+    _fields_ = [("seq", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
 # name -> (restype, argtypes); the same list as include/sd.h
 _p, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 _PS, _PE, _PL = ctypes.POINTER(SdShape), ctypes.POINTER(SdEncoder), ctypes.POINTER(SdSelect)
 _PR = ctypes.POINTER(SdResident)
+_PK, _PT = ctypes.POINTER(SdKv4), ctypes.POINTER(SdStrides)
 SIGNATURES = {
     "sd_build_index": (_i, [_i, _PS, _p, _PE, _p, _p, _p]),
     "sd_append_index": (_i, [_i, _PS, _i64, _p, _PE, _p, _p, _p]),
@@ -65,6 +74,13 @@ SIGNATURES = {
                               _sz, _p]),
     "sd_gather_attend_noalloc": (_i, [_PS, _p, _p, _p, _p, _i64, _p, _i64, ctypes.c_float, _p,
                                       _p, _p]),
+    "sd_kv4_write": (_i, [_PS, _PK, _p, _PT, _p, _PT, _i64, _i64, _p, _p, _p]),
+    "sd_kv4_read": (_i, [_PS, _PK, _p, _PT, _p, _PT, _i64, _i64, _p, _p, _p]),
+    "sd_kv4_attend_workspace_size": (_sz, [_PS]),
+    "sd_kv4_attend": (_i, [_PS, _p, _PK, _p, _p, ctypes.c_float, _p, _p, _p, _sz, _p]),
+    "sd_kv4_gather_attend_workspace_size": (_sz, [_PS, _i64]),
+    "sd_kv4_gather_attend": (_i, [_PS, _p, _PK, _p, _i64, _p, _i64, ctypes.c_float, _p, _p, _p,
+                                  _sz, _p]),
     "sd_offload_gather": (_i, [_PS, _p, _p, _p, _p, _p, _p]),
     "sd_delta_select": (_i, [_PS, _PL, _p, _p, _i64, _p, ctypes.c_int32, ctypes.c_int32, _PR,
                              _p, _p, _p, _p, _p, _i64, _p, _p]),

@@ -518,6 +518,143 @@ int sd_offload_gather(const sd_shape* shape, const uint32_t* host_planes,
                                dev_planes, dev_scales, (cudaStream_t)stream);
 }
 
+static int check_kv4(const char* fn, const sd_kv4* c) {
+  if (!c || !c->k || !c->v || !c->scale)
+    return fail(SD_ERR_INVALID_ARG, "%s: the cache or one of its arrays is NULL", fn);
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->scale))
+    return fail(SD_ERR_INVALID_ARG, "%s: the cache's arrays must be 16-byte aligned", fn);
+  return SD_OK;
+}
+
+// Resolves the strides of a [B][hkv][m][d] array (null: contiguous); with `apart`, two
+// rows must not overlap.
+static int resolve_strides(const char* fn, const Dims& s, int64_t m, const sd_strides* in,
+                           bool apart, sd_strides* out) {
+  *out = in ? *in : sd_strides{(int64_t)s.Hkv * m * kD, m * kD, kD};
+  int64_t* st[3] = {&out->seq, &out->head, &out->token};
+  int64_t ext[3] = {s.B, s.Hkv, m};
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] == 1) *st[i] = 0;
+    if (*st[i] < 0 || *st[i] >= (int64_t)1 << 40 || *st[i] % 8)
+      return fail(SD_ERR_INVALID_ARG, "%s: strides must be multiples of 8 in [0, 2^40)", fn);
+  }
+  if (!apart) return SD_OK;
+  int64_t span = kD;  // rows are apart if, by ascending stride, each clears the ones below
+  bool used[3] = {ext[0] == 1, ext[1] == 1, ext[2] == 1};
+  for (int k = 0; k < 3; ++k) {
+    int at = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!used[i] && (at < 0 || *st[i] < *st[at])) at = i;
+    if (at < 0) break;
+    used[at] = true;
+    if (*st[at] < span)
+      return fail(SD_ERR_INVALID_ARG, "%s: the strides make rows of an output overlap", fn);
+    if (ext[at] - 1 > ((int64_t)1 << 62) / *st[at])
+      return fail(SD_ERR_INVALID_ARG, "%s: strides too large", fn);
+    span += *st[at] * (ext[at] - 1);
+  }
+  return SD_OK;
+}
+
+static int kv4_move(const char* fn, bool write, const sd_shape* shape, const sd_kv4* cache,
+                    const void* K, const sd_strides* ks, const void* V, const sd_strides* vs,
+                    int64_t m, int64_t first, const int32_t* pos, const int32_t* length,
+                    void* stream) {
+  Dims s;
+  int rc = check_shape(shape, &s);
+  if (rc) return rc;
+  if ((rc = check_kv4(fn, cache))) return rc;
+  if (!K && !V) return fail(SD_ERR_INVALID_ARG, "%s: K and V are both NULL", fn);
+  if (!aligned16(K) || !aligned16(V))
+    return fail(SD_ERR_INVALID_ARG, "%s: K and V must be 16-byte aligned", fn);
+  if ((uintptr_t)pos % 4 || (uintptr_t)length % 4)
+    return fail(SD_ERR_INVALID_ARG, "%s: pos and length must be 4-byte aligned", fn);
+  if (m < 0 || m >= (int64_t)1 << 31 || first < 0 || first > s.n)
+    return fail(SD_ERR_INVALID_ARG, "%s: m = %lld or first = %lld out of range", fn,
+                (long long)m, (long long)first);
+  if (m == 0) return SD_OK;
+  sd_strides k, v;
+  if ((rc = resolve_strides(fn, s, m, K ? ks : nullptr, !write, &k))) return rc;
+  if ((rc = resolve_strides(fn, s, m, V ? vs : nullptr, !write, &v))) return rc;
+  return launch_kv4_move(write, s, *cache, const_cast<void*>(K), k, const_cast<void*>(V), v, m,
+                         first, pos, length, (cudaStream_t)stream);
+}
+
+int sd_kv4_write(const sd_shape* shape, const sd_kv4* cache, const void* K,
+                 const sd_strides* k_strides, const void* V, const sd_strides* v_strides,
+                 int64_t m, int64_t first, const int32_t* pos, const int32_t* length,
+                 void* stream) {
+  return kv4_move("sd_kv4_write", true, shape, cache, K, k_strides, V, v_strides, m, first, pos,
+                  length, stream);
+}
+
+int sd_kv4_read(const sd_shape* shape, const sd_kv4* cache, void* K, const sd_strides* k_strides,
+                void* V, const sd_strides* v_strides, int64_t m, int64_t first,
+                const int32_t* pos, const int32_t* length, void* stream) {
+  return kv4_move("sd_kv4_read", false, shape, cache, K, k_strides, V, v_strides, m, first, pos,
+                  length, stream);
+}
+
+// The checks that sd_kv4_attend and sd_kv4_gather_attend share.
+static int check_kv4_attend(const char* fn, const Dims& s, const void* q, const sd_kv4* cache,
+                            float* out, float* lse, void* ws, size_t ws_bytes, size_t need) {
+  if (int rc = check_kv4(fn, cache)) return rc;
+  if (!q || !out) return fail(SD_ERR_INVALID_ARG, "%s: NULL input", fn);
+  if (!aligned16(q) || !aligned16(out) || (uintptr_t)lse % 4)
+    return fail(SD_ERR_INVALID_ARG, "%s: q and out must be 16-byte, lse 4-byte aligned", fn);
+  if (need && (!ws || ws_bytes < need))
+    return fail(SD_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+  if (!aligned16(ws)) return fail(SD_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+  return SD_OK;
+}
+
+size_t sd_kv4_attend_workspace_size(const sd_shape* shape) {
+  Dims s;
+  if (check_shape(shape, &s)) return 0;
+  return kv4_attend_workspace_bytes(s, s.n);
+}
+
+int sd_kv4_attend(const sd_shape* shape, const void* q, const sd_kv4* cache,
+                  const int32_t* begin, const int32_t* end, float scale, float* out, float* lse,
+                  void* workspace, size_t ws_bytes, void* stream) {
+  Dims s;
+  int rc = check_shape(shape, &s);
+  if (rc) return rc;
+  if ((rc = check_kv4_attend("sd_kv4_attend", s, q, cache, out, lse, workspace, ws_bytes,
+                             kv4_attend_workspace_bytes(s, s.n))))
+    return rc;
+  if ((uintptr_t)begin % 4 || (uintptr_t)end % 4)
+    return fail(SD_ERR_INVALID_ARG, "sd_kv4_attend: begin and end must be 4-byte aligned");
+  return launch_kv4_attend(s, (const uint16_t*)q, *cache, nullptr, 0, nullptr, 0, begin, end,
+                           scale, out, lse, workspace, (cudaStream_t)stream);
+}
+
+size_t sd_kv4_gather_attend_workspace_size(const sd_shape* shape, int64_t max_count) {
+  Dims s;
+  if (check_shape(shape, &s) || max_count < 0) return 0;
+  return kv4_attend_workspace_bytes(s, max_count);
+}
+
+int sd_kv4_gather_attend(const sd_shape* shape, const void* q, const sd_kv4* cache,
+                         const int32_t* idx, int64_t idx_stride, const int32_t* count,
+                         int64_t max_count, float scale, float* out, float* lse,
+                         void* workspace, size_t ws_bytes, void* stream) {
+  Dims s;
+  int rc = check_shape(shape, &s);
+  if (rc) return rc;
+  if (!idx || !count) return fail(SD_ERR_INVALID_ARG, "sd_kv4_gather_attend: NULL input");
+  if ((uintptr_t)idx % 4 || (uintptr_t)count % 4)
+    return fail(SD_ERR_INVALID_ARG,
+                "sd_kv4_gather_attend: idx and count must be 4-byte aligned");
+  if (max_count < 0 || max_count >= (int64_t)1 << 31 || idx_stride < max_count)
+    return fail(SD_ERR_INVALID_ARG, "sd_kv4_gather_attend: bad max_count / idx_stride");
+  if ((rc = check_kv4_attend("sd_kv4_gather_attend", s, q, cache, out, lse, workspace, ws_bytes,
+                             kv4_attend_workspace_bytes(s, max_count))))
+    return rc;
+  return launch_kv4_attend(s, (const uint16_t*)q, *cache, idx, idx_stride, count, max_count,
+                           nullptr, nullptr, scale, out, lse, workspace, (cudaStream_t)stream);
+}
+
 int sd_delta_select(const sd_shape* shape, const sd_select* sel, const float* scores,
                     const int32_t* idx, int64_t idx_stride, const int32_t* count,
                     int32_t admit_cap, int32_t step, const sd_resident* res,

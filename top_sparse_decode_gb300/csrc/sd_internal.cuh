@@ -198,6 +198,17 @@ int launch_shard_select(int64_t rows, const int32_t* sel, int64_t sel_stride,
                         int32_t* out, int64_t out_stride, int32_t* ocount, cudaStream_t st);
 int launch_attend_combine(int S, int64_t BH, const float* outs, const float* lses, float* out,
                           float* lse, cudaStream_t st);
+// The 4-bit K/V cache (sd_kv4.cu, sd_kv4_attend.cu).  launch_kv4_move: the write or the
+// read of m tokens per sequence, strides resolved.  launch_kv4_attend: over idx / count
+// rows, or with idx null over [begin, end) of each sequence.
+int launch_kv4_move(bool write, const Dims& s, const sd_kv4& c, void* K, const sd_strides& ks,
+                    void* V, const sd_strides& vs, int64_t m, int64_t first, const int32_t* pos,
+                    const int32_t* length, cudaStream_t st);
+size_t kv4_attend_workspace_bytes(const Dims& s, int64_t max_tokens);
+int launch_kv4_attend(const Dims& s, const uint16_t* q, const sd_kv4& c, const int32_t* idx,
+                      int64_t idx_stride, const int32_t* count, int64_t max_count,
+                      const int32_t* begin, const int32_t* end, float scale, float* out,
+                      float* lse, void* ws, cudaStream_t st);
 int launch_offload_gather(const Dims& s, const uint32_t* host_planes, const uint16_t* host_scales,
                           const uint8_t* plan, uint32_t* dev_planes, uint16_t* dev_scales,
                           cudaStream_t st);
