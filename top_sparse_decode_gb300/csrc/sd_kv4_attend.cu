@@ -2,26 +2,26 @@
 // Inference, 2.1): z_i = scale <q, k_i>, o = sum e^{z_i - m} v_i / sum e^{z_i - m}, over a
 // range of each sequence's tokens or over selected ones (2.5, rows read in place).
 //
-// With k_ij = c_ij s_ig + m_ig (g = the group of channel j):
+// With k_ij = c_ij s_ig + m_ig and v_ij = (c_ij - 7.5) s_ig + m'_ig (g = the group of channel
+// j, m' = m + 7.5 s the middle of its range):
 //   z_i = scale sum_g [ s_ig sum_{j in g} q_j c_ij + m_ig sum_{j in g} q_j ]
-//   o_j = [ sum_i (p_i s_ig) c_ij + sum_i p_i m_ig ] / sum_i p_i
-// so the codes are only ever multiplied as whole numbers, by the tensor cores, and scales
-// and minima enter once per token and group, in fp32.
-//  * A code needs no conversion: the four bits, masked in place, are an f16 subnormal c
-//    2^-24 (bits 0..3 of a half-word) or 16 c 2^-24 (bits 4..7), both exact.  The 16 goes
-//    into q (QK^T) and into the outputs at the end (PV).
+//   o_j = [ sum_i (p_i s_ig) (c_ij - 7.5) + sum_i p_i m'_ig ] / sum_i p_i
+// so only codes are multiplied by the tensor cores, as small whole (or half) numbers, and
+// scales and minima enter once per token and group, in fp32.  Both sums of o are of numbers
+// that change sign: with c in place of c - 7.5 they would be large and cancel.
+//  * A code becomes an f16 number by a mask and one multiplication (ka_code_lo).
 //  * z: S = K q^T, m16n8k16 with 16 tokens as rows and the heads as columns: 8 MMAs per 16
 //    tokens.  q is scaled by a power of two per head to f16; bf16 values stay exact
-//    unless they are 2^-36 below the head's largest.
+//    unless they are 2^-32 below the head's largest.
 //  * PV: O^T = V^T P^T, 16 channels as rows, heads as columns, 16 tokens deep.  w = p s f is
 //    split in two f16 parts (22 bits; f a power of two per head and group that holds the
 //    largest w in [2^7, 2^14], raised and lowered as an online softmax moves its
 //    maximum).  With G <= 4 the columns 4..7 repeat the heads and take the low parts (8
 //    MMAs per 16 tokens), with G = 8 the low parts are 8 more.
 //  * p = 2^(z log2 e - m); m, a whole number per head, is raised only when a logit
-//    exceeds it by 8.
+//    exceeds it by about 8.
 //
-// Each warp pulls 16-token tiles (2,304 bytes) through a ring of its own in shared memory
+// Each warp pulls 32-token tiles (4,608 bytes) through a ring of its own in shared memory
 // with 16-byte asynchronous copies; rows are swizzled there so that both operands read
 // without bank conflicts.
 #include <cooperative_groups.h>
@@ -36,10 +36,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kKaTile = 16;    // tokens per tile
-constexpr int kKaWarps = 8;    // warps per CTA
+constexpr int kKaTile = 32;    // tokens per tile
+constexpr int kKaWarps = 6;    // warps per CTA
 constexpr int kKaThreads = 32 * kKaWarps;
-constexpr int kKaDepth = 5;    // tiles in a warp's ring
+constexpr int kKaDepth = 3;    // tiles in a warp's ring
 constexpr int kKaOffV = kKaTile * kKv4Row, kKaOffS = 2 * kKaOffV;
 constexpr int kKaOffMask = kKaOffS + kKaTile * 2 * kKv4Scales;
 constexpr int kKaStage = kKaOffMask + 16;
@@ -47,8 +47,8 @@ constexpr int kKaRing = kKaDepth * kKaStage;
 constexpr float kKaLog2e = 1.4426950408889634f;
 constexpr float kKaLn2 = 0.6931471805599453f;
 constexpr float kKaEmpty = -1e30f;   // m before the first token
-constexpr float kKaSlack = 8.0f;     // log2 headroom of p over m
-constexpr float kKaWMax = 16384.0f;  // largest w that is not rescaled
+constexpr float kKaPMax = 512.0f;    // a lane's largest sum of four p that leaves m as it is
+constexpr float kKaWMax = 16384.0f;  // largest w that leaves f as it is (0x7400 in f16)
 constexpr float kKaF0 = 1.2676506e30f;  // 2^100: f before the first token, and its limit
 
 struct KaArgs {
@@ -93,6 +93,9 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 // 16 bytes into shared memory; zeros where v is false.
+__device__ __forceinline__ void ka_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void ka_copy16(uint32_t dst, const void* src, bool v) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
                "r"(v ? 16 : 0)
@@ -130,44 +133,83 @@ __device__ __forceinline__ float ka_exp2(float x) {
   return y;
 }
 
-// Requests tile `tile` of a row into a stage.  Lane l copies chunk l % 4 of the rows of
-// tokens l / 4 and l / 4 + 8 (chunks swizzled by 2 where the token's bit 1 is set) and,
-// below 16, the scale record of token l.  Tokens past the row, and indices outside [0,
-// n), become zeros; the stage's mask lists the others.
+// Where a warp's next tile comes from.  Lane l copies chunk l % 4 of the rows of tokens l / 4
+// + 8 h (swizzled by 2 where the token's bit 1 is set) and the scale record of token l.
+// Tokens past the row, and indices outside [0, n), become zeros; a gathered stage keeps
+// the mask of the others.
 template <bool GATHER>
-__device__ __forceinline__ void ka_issue(const KaArgs& a, uint32_t stage, int64_t row,
-                                         const KaRow& r, int tile, int lane) {
-  const int p = tile * kKaTile + (lane & 15);
-  bool ok = p < r.len;
-  int tok = 0;
-  if (GATHER) {
-    if (ok) tok = __ldg(a.idx + row * a.idx_stride + p);
-    ok = ok && tok >= 0 && tok < a.n;
-    if (!ok) tok = 0;
-  } else if (ok) {
-    tok = r.t0 + p;
+struct KaSrc {
+  const uint8_t *k, *v;     // this lane's chunk: of the tile's first token, or of token 0
+  const uint16_t* s;        // ... its token's scale record, or token 0's
+  const int32_t* idx;       // gathered: the tile's index of this lane
+  int left;                 // tokens of the row from the tile on
+  int tok;                  // gathered: this lane's index, requested a tile ahead
+  __device__ __forceinline__ void fetch(int lane) {
+    if (GATHER) tok = lane < left ? __ldg(idx) : -1;
   }
-  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
-  const int64_t base = row * a.ncap;
-  const int tl = lane >> 2, ch = lane & 3;
-  const uint32_t dst = stage + tl * kKv4Row + ((ch ^ (lane >> 2 & 2)) * 16);
+  __device__ __forceinline__ void set(const KaArgs& a, int64_t row, const KaRow& r, int tile,
+                                      int lane) {
+    left = r.len - tile * kKaTile;
+    const int64_t at = row * a.ncap + (GATHER ? 0 : r.t0 + (int64_t)tile * kKaTile);
+    const int64_t off = (at + (GATHER ? 0 : lane >> 2)) * kKv4Row + (lane & 3) * 16;
+    k = a.c.k + off;
+    v = a.c.v + off;
+    s = a.c.scale + (at + (GATHER ? 0 : lane)) * kKv4Scales;
+    if (GATHER) idx = a.idx + row * a.idx_stride + tile * (int64_t)kKaTile + lane;
+    fetch(lane);
+  }
+  __device__ __forceinline__ void advance(int tiles, int lane) {
+    left -= tiles * kKaTile;
+    if (GATHER) {
+      idx += (int64_t)tiles * kKaTile;
+    } else {
+      k += (int64_t)tiles * kKaTile * kKv4Row;
+      v += (int64_t)tiles * kKaTile * kKv4Row;
+      s += (int64_t)tiles * kKaTile * kKv4Scales;
+    }
+    fetch(lane);
+  }
+  __device__ __forceinline__ void issue(const KaArgs& a, uint32_t stage, int lane) const {
+    const int tl = lane >> 2;
+    const uint32_t dst = stage + tl * kKv4Row + (((lane & 3) ^ (tl & 2)) * 16);
+    const uint32_t dsts = stage + kKaOffS + lane * 16;
+    if (GATHER) {
+      const bool ok = (unsigned)tok < (unsigned)a.n;
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
+      const int safe = ok ? tok : 0;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int t = __shfl_sync(0xFFFFFFFFu, tok, tl + 8 * h);
-    const bool v = mask >> (tl + 8 * h) & 1u;
-    const int64_t off = (base + t) * kKv4Row + ch * 16;
-    ka_copy16(dst + h * 8 * kKv4Row, a.c.k + off, v);
-    ka_copy16(dst + h * 8 * kKv4Row + kKaOffV, a.c.v + off, v);
+      for (int h = 0; h < 4; ++h) {
+        const int64_t off = (int64_t)__shfl_sync(0xFFFFFFFFu, safe, tl + 8 * h) * kKv4Row;
+        const bool val = mask >> (tl + 8 * h) & 1u;
+        ka_copy16(dst + h * 8 * kKv4Row, k + off, val);
+        ka_copy16(dst + h * 8 * kKv4Row + kKaOffV, v + off, val);
+      }
+      ka_copy16(dsts, s + (int64_t)safe * kKv4Scales, ok);
+      if (lane == 0) sts32(stage + kKaOffMask, mask);
+    } else if (left >= kKaTile) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        ka_copy16(dst + h * 8 * kKv4Row, k + h * 8 * kKv4Row);
+        ka_copy16(dst + h * 8 * kKv4Row + kKaOffV, v + h * 8 * kKv4Row);
+      }
+      ka_copy16(dsts, s);
+    } else {  // addresses past the row's last token stay at the tile's first
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const bool val = tl + 8 * h < left;
+        const int64_t off = val ? h * 8 * kKv4Row : -(int64_t)tl * kKv4Row;
+        ka_copy16(dst + h * 8 * kKv4Row, k + off, val);
+        ka_copy16(dst + h * 8 * kKv4Row + kKaOffV, v + off, val);
+      }
+      ka_copy16(dsts, lane < left ? s : s - (int64_t)lane * kKv4Scales, lane < left);
+    }
   }
-  if (lane < kKaTile)
-    ka_copy16(stage + kKaOffS + lane * 16, a.c.scale + (base + tok) * kKv4Scales, ok);
-  if (lane == 0) sts32(stage + kKaOffMask, mask);
-}
+};
 
 // q as the B operand, and per-head constants of the lane's two columns (heads).
 struct KaQ {
   uint32_t b[2][4][2];  // [group][k-step][half]
-  float ch[2];          // scale log2(e) 2^24 / (q's power of two)
+  float ch[2];          // scale log2(e) 2^9 / (q's power of two)
   float qs[2][2];       // [column][group]: scale log2(e) sum of the group's q
 };
 
@@ -204,26 +246,19 @@ __device__ __forceinline__ void ka_load_q(KaQ& Q, const KaArgs& a, int64_t row, 
     sum[0] += __shfl_xor_sync(0xFFFFFFFFu, sum[0], o);
     sum[1] += __shfl_xor_sync(0xFFFFFFFFu, sum[1], o);
   }
-  // 2^k q has its largest value in [2^14, 2^15) (k at most 120: smaller heads are 0 to
-  // any cache)
+  // 2^k q has its largest value in [2^14, 2^15) (k at most 120: smaller heads give 0)
   const int k = top > 0.0f ? min(14 - ((int)(__float_as_uint(top) >> 23) - 127), 120) : 0;
   const float up = __uint_as_float((uint32_t)(127 + k) << 23);
 #pragma unroll
   for (int g = 0; g < 2; ++g)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      // word 4 tig + 2 j + g: nibbles i and i + 4 of a half-word pair, i = 0..3
+      // word 4 tig + 2 j + g: channels i and i + 4 of the octet are a half-word pair
       const uint32_t x[4] = {w[g][j].x, w[g][j].y, w[g][j].z, w[g][j].w};
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(x[i]) * up;
-        f[2 * i + 1] = bf16_hi(x[i]) * up;
-      }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const __half2 lo = __floats2half2_rn(f[2 * s], f[2 * s + 4]);
-        const __half2 hi = __floats2half2_rn(f[2 * s + 1] * 0.0625f, f[2 * s + 5] * 0.0625f);
+        const __half2 lo = __floats2half2_rn(bf16_lo(x[s]) * up, bf16_lo(x[s + 2]) * up);
+        const __half2 hi = __floats2half2_rn(bf16_hi(x[s]) * up, bf16_hi(x[s + 2]) * up);
         Q.b[g][2 * j + s][0] = *reinterpret_cast<const uint32_t*>(&lo);
         Q.b[g][2 * j + s][1] = *reinterpret_cast<const uint32_t*>(&hi);
       }
@@ -233,15 +268,44 @@ __device__ __forceinline__ void ka_load_q(KaQ& Q, const KaArgs& a, int64_t row, 
   for (int e = 0; e < 2; ++e) {
     const int src = 4 * (2 * tig + e);  // a lane that loaded the column's head
     const int kc = __shfl_sync(0xFFFFFFFFu, k, src);
-    Q.ch[e] = sl * __uint_as_float((uint32_t)(127 + 24 - kc) << 23);
+    Q.ch[e] = sl * 512.0f * __uint_as_float((uint32_t)(127 - kc) << 23);
     Q.qs[e][0] = sl * __shfl_sync(0xFFFFFFFFu, sum[0], src);
     Q.qs[e][1] = sl * __shfl_sync(0xFFFFFFFFu, sum[1], src);
   }
 }
 
-// A warp's online softmax.  o: O^T in units of 2^-24 / f (odd channels 16 times that);
-// tile 4 g + u holds channels 64 g + 8 gid + 2 u (o[..][e]) and + 1 (o[..][2 + e]) of
-// columns 2 tig + e.  l, mo: this lane's tokens only.
+// f16 pairs of the codes that a word holds at bits 0..3 (lo) or 4..7 (hi) of its halves:
+// masked in place they are the subnormals c 2^-24 or 16 c 2^-24; a multiplication takes
+// them to c 2^-9, normal numbers (the tensor cores align products by their nominal
+// exponents and cut the rest, which would cost subnormals up to ten bits).
+__device__ __forceinline__ uint32_t ka_code_lo(uint32_t x) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(x & 0x000F000Fu), "r"(0x78007800u));  // 2^15
+  return y;
+}
+__device__ __forceinline__ uint32_t ka_code_hi(uint32_t x) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(x & 0x00F000F0u), "r"(0x68006800u));  // 2^11
+  return y;
+}
+// The same, centred: (c - 7.5) 2^-9.
+__device__ __forceinline__ uint32_t ka_mid_lo(uint32_t x) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;\n"
+      : "=r"(y)
+      : "r"(x & 0x000F000Fu), "r"(0x78007800u), "r"(0xA380A380u));  // -7.5 2^-9
+  return y;
+}
+__device__ __forceinline__ uint32_t ka_mid_hi(uint32_t x) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;\n"
+      : "=r"(y)
+      : "r"(x & 0x00F000F0u), "r"(0x68006800u), "r"(0xA380A380u));
+  return y;
+}
+
+// A warp's online softmax.  o: sum w (c - 7.5) in units of 2^-9; tile 4 g + u holds channels 64 g + 8 gid + 2 u (o[..][e]) and + 1 (o[..][2 + e]) of
+// columns 2 tig + e.  mo: sum p (m + 7.5 s).  l, mo: this lane's tokens only.
 struct KaState {
   float o[8][4];
   float m[2], l[2];
@@ -271,50 +335,40 @@ __device__ __forceinline__ float ka_col_max(float x) {
   return x;
 }
 
-// Raises the columns' m where a logit exceeds it by more than the slack.
-__device__ __forceinline__ void ka_raise_m(KaState& S, const float (&z)[2][2]) {
+// Raises m to the whole number above `top`, the tile's largest logit of column e.
+__device__ __forceinline__ void ka_raise_m(KaState& S, int e, float top) {
+  if (!(top > S.m[e])) return;  // uniform over the column's lanes
+  const float up = ceilf(top), d = up - S.m[e], al = ka_exp2(-d);
+  S.m[e] = up;
+  S.l[e] *= al;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float top = ka_col_max(fmaxf(z[0][e], z[1][e]));
-    if (!(top > S.m[e] + kKaSlack)) continue;  // uniform over the column's lanes
-    const float up = ceilf(top), d = up - S.m[e], al = ka_exp2(-d);
-    S.m[e] = up;
-    S.l[e] *= al;
+  for (int g = 0; g < 2; ++g) {
+    S.mo[e][g] *= al;
+    // what was summed weighs 2^-d now: f takes up the factor, o stays, up to f's limit
+    const float fn = fminf(S.f[e][g] * ka_exp2(fminf(d, 126.0f)), kKaF0);
+    const float r = (fn / S.f[e][g]) * al;
+    S.f[e][g] = fn;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      S.mo[e][g] *= al;
-      // what was summed weighs 2^-d now: f takes up the factor, o stays, up to f's limit
-      const float fn = fminf(S.f[e][g] * ka_exp2(fminf(d, 126.0f)), kKaF0);
-      const float r = (fn / S.f[e][g]) * al;
-      S.f[e][g] = fn;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        S.o[4 * g + u][e] *= r;
-        S.o[4 * g + u][2 + e] *= r;
-      }
+    for (int u = 0; u < 4; ++u) {
+      S.o[4 * g + u][e] *= r;
+      S.o[4 * g + u][2 + e] *= r;
     }
   }
 }
 
-// Lowers f where p s f exceeds kKaWMax, to bring the largest to [2^7, 2^8).
-__device__ __forceinline__ void ka_lower_f(KaState& S, const float (&p)[2][2],
-                                        const float (&sv)[2][2]) {
+// Lowers f where it takes `top`, the tile's largest p s of column e and group g, above
+// kKaWMax, to bring it to [2^7, 2^8).
+__device__ __forceinline__ void ka_lower_f(KaState& S, int e, int g, float top) {
+  if (!(top * S.f[e][g] > kKaWMax) || !(top < INFINITY)) return;
+  const int ex = (int)(__float_as_uint(top) >> 23) - 127;  // top >= 2^-86: normal
+  const float fn = __uint_as_float((uint32_t)(127 + max(7 - ex, -126)) << 23);
+  const float r = fn / S.f[e][g];
+  S.f[e][g] = fn;
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const float top = ka_col_max(fmaxf(p[0][e] * sv[0][g], p[1][e] * sv[1][g]));
-      if (!(top * S.f[e][g] > kKaWMax) || !(top < INFINITY)) continue;
-      const int ex = (int)(__float_as_uint(top) >> 23) - 127;  // top >= 2^-86: normal
-      const float fn = __uint_as_float((uint32_t)(127 + max(7 - ex, -126)) << 23);
-      const float r = fn / S.f[e][g];
-      S.f[e][g] = fn;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        S.o[4 * g + u][e] *= r;
-        S.o[4 * g + u][2 + e] *= r;
-      }
-    }
+  for (int u = 0; u < 4; ++u) {
+    S.o[4 * g + u][e] *= r;
+    S.o[4 * g + u][2 + e] *= r;
+  }
 }
 
 __device__ __forceinline__ uint32_t ka_pack(float lo, float hi) {
@@ -323,120 +377,171 @@ __device__ __forceinline__ uint32_t ka_pack(float lo, float hi) {
   return d;
 }
 
-// One 16-token tile.  Row r of the score tile is token tau(r) (r < 8: r / 2, odd rows 4 +
-// (r / 2 ^ 1)) or tau(r - 8) + 8: with the swizzle, any eight lanes of a K read and any
-// sixteen of a V read touch each bank once.
+// One tile, as two 16-token halves; valid: its tokens.  Row r of a half's score tile is
+// token tau(r) (r < 8: r / 2, odd rows 4 + (r / 2 ^ 1)) or tau(r - 8) + 8: with the
+// swizzle, any eight lanes of a K read and any sixteen of a V read touch each bank once.
 template <int G>
-__device__ __forceinline__ void ka_tile(KaState& S, const KaQ& Q, uint32_t st, int lane) {
+__device__ __forceinline__ void ka_tile(KaState& S, const KaQ& Q, uint32_t st, uint32_t valid,
+                                        int lane) {
   const int gid = lane >> 2, tig = lane & 3;
   const int tk = (gid & 1) ? 4 + (gid >> 1 ^ 1) : gid >> 1;
-  const uint32_t ak = st + tk * kKv4Row + ((tig ^ (gid >> 1 & 2)) * 16);
-  const uint4 ka = lds128(ak), kb = lds128(ak + 8 * kKv4Row);
-  const uint32_t as = st + kKaOffS + tk * 16;
-  const uint4 sa = lds128(as), sb = lds128(as + 8 * 16);
-  const uint32_t mask = lds32(st + kKaOffMask);
-  const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-  constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;
-  float acc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+  float dot[4][2];                               // [2 half + r][column]: sum_g s_g <q, c>_g
+  float mk[4][2], sv[4][2], mv[4][2];            // [2 half + r][group]
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int hf = 0; hf < 2; ++hf) {
+    const uint32_t ak = st + (16 * hf + tk) * kKv4Row + ((tig ^ (gid >> 1 & 2)) * 16);
+    const uint4 ka = lds128(ak), kb = lds128(ak + 8 * kKv4Row);
+    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+    float acc[2][4];  // [group]
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const uint32_t xa = wa[2 * j + g] >> (8 * s), xb = wb[2 * j + g] >> (8 * s);
-        mma_f16(acc[g], xa & kLo, xb & kLo, xa & kHi, xb & kHi, Q.b[g][2 * j + s][0],
-                Q.b[g][2 * j + s][1]);
-      }
-  float z[2][2], sv[2][2], mv[2][2];
-  {
-    const uint4 sc[2] = {sa, sb};
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t xa = wa[2 * j + g] >> (8 * s), xb = wb[2 * j + g] >> (8 * s);
+          const uint32_t a0 = ka_code_lo(xa), a1 = ka_code_lo(xb);
+          const uint32_t a2 = ka_code_hi(xa), a3 = ka_code_hi(xb);
+          const uint32_t(&qb)[2] = Q.b[g][2 * j + s];
+          if (j + s == 0)
+            mma_f16_zero(acc[g], a0, a1, a2, a3, qb[0], qb[1]);
+          else
+            mma_f16(acc[g], a0, a1, a2, a3, qb[0], qb[1]);
+        }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float s0 = bf16_lo(sc[r].x), m0 = bf16_hi(sc[r].x);
-      const float s1 = bf16_lo(sc[r].y), m1 = bf16_hi(sc[r].y);
-      sv[r][0] = bf16_lo(sc[r].z);
-      mv[r][0] = bf16_hi(sc[r].z);
-      sv[r][1] = bf16_lo(sc[r].w);
-      mv[r][1] = bf16_hi(sc[r].w);
+      const uint4 sc = lds128(st + kKaOffS + (16 * hf + tk + 8 * r) * 16);
+      const int i = 2 * hf + r;
+      const float sk0 = bf16_lo(sc.x), sk1 = bf16_lo(sc.y);
+      mk[i][0] = bf16_hi(sc.x);
+      mk[i][1] = bf16_hi(sc.y);
+      sv[i][0] = bf16_lo(sc.z);
+      sv[i][1] = bf16_lo(sc.w);
+      mv[i][0] = fmaf(7.5f, sv[i][0], bf16_hi(sc.z));  // the middle of the group's range
+      mv[i][1] = fmaf(7.5f, sv[i][1], bf16_hi(sc.w));
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        z[r][e] = fmaf(fmaf(s1, acc[1][2 * r + e], s0 * acc[0][2 * r + e]), Q.ch[e],
-                       fmaf(m1, Q.qs[e][1], m0 * Q.qs[e][0]));
+        dot[i][e] = fmaf(sk1, acc[1][2 * r + e], sk0 * acc[0][2 * r + e]);
     }
   }
-  if (mask != 0xFFFFu) {
+  // log2 of the weight over 2^sub
+  auto logit = [&](int i, int e, float sub) {
+    return fmaf(dot[i][e], Q.ch[e], fmaf(mk[i][1], Q.qs[e][1], fmaf(mk[i][0], Q.qs[e][0], -sub)));
+  };
+  auto ok = [&](int i) { return valid >> (16 * (i >> 1) + tk + 8 * (i & 1)) & 1u; };
+  float p[4][2], sum[2];
+  auto weights = [&](int e) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      if (!(mask >> (tk + 8 * r) & 1u)) z[r][0] = z[r][1] = -INFINITY;
-  }
-  const bool raise = fmaxf(z[0][0], z[1][0]) > S.m[0] + kKaSlack ||
-                     fmaxf(z[0][1], z[1][1]) > S.m[1] + kKaSlack;
-  if (__any_sync(0xFFFFFFFFu, raise)) ka_raise_m(S, z);
-  float p[2][2], w[2][2][2];
+    for (int i = 0; i < 4; ++i) p[i][e] = ka_exp2(logit(i, e, S.m[e]));
+    if (valid != 0xFFFFFFFFu) {
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    p[0][e] = ka_exp2(z[0][e] - S.m[e]);
-    p[1][e] = ka_exp2(z[1][e] - S.m[e]);
-    S.l[e] += p[0][e] + p[1][e];
+      for (int i = 0; i < 4; ++i)
+        if (!ok(i)) p[i][e] = 0.0f;
+    }
+    sum[e] = (p[0][e] + p[1][e]) + (p[2][e] + p[3][e]);
+  };
+  weights(0);
+  weights(1);
+  uint32_t hi[4][2];  // w's high parts, a pair of columns each
+  auto weigh = [&]() {
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
-      S.mo[e][g] = fmaf(p[1][e], mv[1][g], fmaf(p[0][e], mv[0][g], S.mo[e][g]));
-  }
-  float top = 0.0f;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+      for (int g = 0; g < 2; ++g)
+        hi[i][g] = ka_pack(p[i][0] * (sv[i][g] * S.f[0][g]), p[i][1] * (sv[i][g] * S.f[1][g]));
+  };
+  weigh();
+  __half2 ht = *reinterpret_cast<__half2*>(&hi[0][0]);
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+  for (int i = 1; i < 8; ++i) ht = __hmax2(ht, *reinterpret_cast<__half2*>(&hi[i >> 1][i & 1]));
+  const uint32_t hb = *reinterpret_cast<uint32_t*>(&ht);
+  const bool over = fmaxf(sum[0], sum[1]) > kKaPMax || (hb & 0xFFFFu) > 0x7400u || hb > 0x7400FFFFu;
+  if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float zt = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (ok(i)) zt = fmaxf(zt, logit(i, e, 0.0f));
+      ka_raise_m(S, e, ka_col_max(zt));
+      weights(e);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        w[r][e][g] = p[r][e] * (sv[r][g] * S.f[e][g]);
-        top = fmaxf(top, w[r][e][g]);
+        float wt = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wt = fmaxf(wt, p[i][e] * sv[i][g]);
+        ka_lower_f(S, e, g, ka_col_max(wt));
       }
-  if (__any_sync(0xFFFFFFFFu, top > kKaWMax)) {
-    ka_lower_f(S, p, sv);
+    }
+    weigh();
+  }
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+  for (int e = 0; e < 2; ++e) {
+    S.l[e] += sum[e];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+    for (int g = 0; g < 2; ++g)
 #pragma unroll
-        for (int g = 0; g < 2; ++g) w[r][e][g] = p[r][e] * (sv[r][g] * S.f[e][g]);
+      for (int i = 0; i < 4; ++i) S.mo[e][g] = fmaf(p[i][e], mv[i][g], S.mo[e][g]);
   }
   // P^T's high and low f16 parts, as B operands
-  uint32_t bh[2][2], bl[2][2];
+  uint32_t bh[2][2][2], bl[2][2][2];  // [half][group][r]
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float2 h2 = __half22float2(*reinterpret_cast<const __half2*>(&hi[i][g]));
+      const uint32_t lo = ka_pack(fmaf(p[i][0], sv[i][g] * S.f[0][g], -h2.x),
+                                  fmaf(p[i][1], sv[i][g] * S.f[1][g], -h2.y));
+      if (G == 8) {
+        bh[i >> 1][g][i & 1] = transpose_8x8(hi[i][g]);
+        bl[i >> 1][g][i & 1] = transpose_8x8(lo);
+      } else {
+        bh[i >> 1][g][i & 1] = transpose_8x8(tig < 2 ? hi[i][g] : lo);
+      }
+    }
+  // rows 2 tig, 2 tig + 1 (and + 8) of V's halves, 8 bytes from byte 8 gid: channels 8 gid ..
+  // + 7 of either group
+  uint2 v[2][4];
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    const uint32_t av = st + kKaOffV + 16 * hf * kKv4Row + ((gid >> 1 ^ (tig & 2)) * 16) +
+                        (gid & 1) * 8;
+    v[hf][0] = lds64(av + tig * kKv4Row);
+    v[hf][1] = lds64(av + (4 + (tig ^ 1)) * kKv4Row);
+    v[hf][2] = lds64(av + (tig + 8) * kKv4Row);
+    v[hf][3] = lds64(av + (12 + (tig ^ 1)) * kKv4Row);
+  }
 #pragma unroll
   for (int g = 0; g < 2; ++g)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const uint32_t hi = ka_pack(w[r][0][g], w[r][1][g]);
-      const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-      const uint32_t lo = ka_pack(w[r][0][g] - hf.x, w[r][1][g] - hf.y);
-      if (G == 8) {
-        bh[g][r] = transpose_8x8(hi);
-        bl[g][r] = transpose_8x8(lo);
-      } else {
-        bh[g][r] = transpose_8x8(tig < 2 ? hi : lo);
-      }
-    }
-  // rows 2 tig, 2 tig + 1 (and + 8) of V, 8 bytes from byte 8 gid: channels 8 gid .. + 7 of
-  // either group
-  const uint32_t av = st + kKaOffV + ((gid >> 1 ^ (tig & 2)) * 16) + (gid & 1) * 8;
-  const uint2 v0 = lds64(av + tig * kKv4Row), v1 = lds64(av + (4 + (tig ^ 1)) * kKv4Row);
-  const uint2 v2 = lds64(av + (tig + 8) * kKv4Row), v3 = lds64(av + (12 + (tig ^ 1)) * kKv4Row);
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const uint32_t w0 = g ? v0.y : v0.x, w1 = g ? v1.y : v1.x;
-    const uint32_t w2 = g ? v2.y : v2.x, w3 = g ? v3.y : v3.x;
-#pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t sel = u < 2 ? 0x5410u : 0x7632u;
-      const uint32_t x = __byte_perm(w0, w1, sel) >> (8 * (u & 1));
-      const uint32_t y = __byte_perm(w2, w3, sel) >> (8 * (u & 1));
-      mma_f16(S.o[4 * g + u], x & kLo, x & kHi, y & kLo, y & kHi, bh[g][0], bh[g][1]);
-      if (G == 8)
-        mma_f16(S.o[4 * g + u], x & kLo, x & kHi, y & kLo, y & kHi, bl[g][0], bl[g][1]);
+      // the tensor cores add by truncation: a tile is summed from zero and added by
+      // rounding, or the error would grow with the tokens
+      float t[4];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint32_t w0 = g ? v[hf][0].y : v[hf][0].x, w1 = g ? v[hf][1].y : v[hf][1].x;
+        const uint32_t w2 = g ? v[hf][2].y : v[hf][2].x, w3 = g ? v[hf][3].y : v[hf][3].x;
+        const uint32_t x = __byte_perm(w0, w1, sel) >> (8 * (u & 1));
+        const uint32_t y = __byte_perm(w2, w3, sel) >> (8 * (u & 1));
+        const uint32_t a0 = ka_mid_lo(x), a1 = ka_mid_hi(x), a2 = ka_mid_lo(y), a3 = ka_mid_hi(y);
+        if (hf == 0)
+          mma_f16_zero(t, a0, a1, a2, a3, bh[hf][g][0], bh[hf][g][1]);
+        else
+          mma_f16(t, a0, a1, a2, a3, bh[hf][g][0], bh[hf][g][1]);
+        if (G == 8) mma_f16(t, a0, a1, a2, a3, bl[hf][g][0], bl[hf][g][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S.o[4 * g + u][i] += t[i];
     }
-  }
+}
+
+// The mask of a row's tile whose first token has `left` tokens of the row from it on.
+template <bool GATHER>
+__device__ __forceinline__ uint32_t ka_valid(uint32_t stage, int left) {
+  if (GATHER) return lds32(stage + kKaOffMask);
+  return left >= kKaTile ? 0xFFFFFFFFu : (1u << left) - 1u;
 }
 
 // The state of a warp in natural units, written to so [G][kD] and sml [G] = (m, l).
@@ -456,7 +561,7 @@ __device__ __forceinline__ void ka_flush(KaState& S, float* so, float2* sml, int
     if (mine && gid == 0) sml[hd] = make_float2(S.m[e], S.l[e]);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const float k = 16777216.0f / S.f[e][g];
+      const float k = 512.0f / S.f[e][g];
       float x[8];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -466,7 +571,7 @@ __device__ __forceinline__ void ka_flush(KaState& S, float* so, float2* sml, int
           odd += __shfl_xor_sync(0xFFFFFFFFu, odd, 2);
         }
         x[2 * u] = fmaf(even, k, S.mo[e][g]);
-        x[2 * u + 1] = fmaf(odd, k * 0.0625f, S.mo[e][g]);
+        x[2 * u + 1] = fmaf(odd, k, S.mo[e][g]);
       }
       if (mine) {
         float4* d = reinterpret_cast<float4*>(so + hd * kD + 64 * g + 8 * gid);
@@ -499,30 +604,36 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs
   const int64_t row = blockIdx.y;
   const int b = (int)(row / a.Hkv), h = (int)(row % a.Hkv);
   const KaRow r = ka_row<GATHER>(a, row, b);
-  const int tiles = (r.len + kKaTile - 1) / kKaTile, step = CS * kKaWarps;
+  const int step = CS * kKaWarps;
   const uint32_t ring = smem_addr(smem) + warp * kKaRing;
-  int next = rank * kKaWarps + warp;
+  const int first = rank * kKaWarps + warp;
+  KaSrc<GATHER> src;
+  src.set(a, row, r, first, lane);
 #pragma unroll
   for (int d = 0; d < kKaDepth - 1; ++d) {
-    if (next < tiles) ka_issue<GATHER>(a, ring + d * kKaStage, row, r, next, lane);
+    if (src.left > 0) {
+      src.issue(a, ring + d * kKaStage, lane);
+      src.advance(step, lane);
+    }
     ka_commit();
-    next += step;
   }
   KaQ Q;
   ka_load_q<G>(Q, a, row, lane);
   KaState S;
   S.clear();
-  uint32_t slot = 0;
-  for (int t = rank * kKaWarps + warp; t < tiles; t += step) {
-    const uint32_t put = slot == 0 ? (kKaDepth - 1) * kKaStage : slot - kKaStage;
-    if (next < tiles) ka_issue<GATHER>(a, ring + put, row, r, next, lane);
+  uint32_t slot = ring, put = ring + (kKaDepth - 1) * kKaStage;
+  for (int left = r.len - first * kKaTile; left > 0; left -= step * kKaTile) {
+    if (src.left > 0) {
+      src.issue(a, put, lane);
+      src.advance(step, lane);
+    }
     ka_commit();
-    next += step;
     ka_wait<kKaDepth - 1>();
     __syncwarp();
-    ka_tile<G>(S, Q, ring + slot, lane);
+    ka_tile<G>(S, Q, slot, ka_valid<GATHER>(slot, left), lane);
     __syncwarp();
-    slot = slot == (kKaDepth - 1) * kKaStage ? 0 : slot + kKaStage;
+    put = slot;
+    slot = slot == ring + (kKaDepth - 1) * kKaStage ? ring : slot + kKaStage;
   }
   ka_wait<0>();
   __syncthreads();  // the rings become the warps' states
@@ -568,9 +679,240 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs
   cl.sync();  // every CTA's state stays alive until the others have read it
 }
 
+// Many tokens: the rows' tiles, in row-major order, are cut into equal ranges, one per
+// CTA; within a CTA they are dealt to the warps in turn and each warp's ring runs on
+// across rows.  A row that lies within a range is written at once; a row cut by ranges
+// leaves a partial per range, and the CTA that brings its last one (a ticket) joins them
+// in range order.
+constexpr int kKaMaxCtas = 320;  // partials of the workspace: two per CTA
+
+// Items of the partition: sequences of Hkv rows each, or single rows with counts of
+// their own.
+template <bool GATHER>
+__device__ __forceinline__ int ka_item_tiles(const KaArgs& a, int64_t item) {
+  const KaRow r = ka_row<GATHER>(a, item, (int)item);  // either reads its one index only
+  return (r.len + kKaTile - 1) / kKaTile;
+}
+
+// A segment: tiles [a0, a1) of a row; left: tiles of the range from a0 on.
+template <bool GATHER>
+struct KaSeg {
+  int row, left, a0, a1, tiles;
+  KaRow r;
+  __device__ __forceinline__ void load(const KaArgs& a) {
+    r = ka_row<GATHER>(a, row, row / a.Hkv);
+    tiles = (r.len + kKaTile - 1) / kKaTile;
+    a1 = min(tiles, a0 + left);
+  }
+  // The range's next segment; false at its end.
+  __device__ __forceinline__ bool next(const KaArgs& a) {
+    left -= a1 - a0;
+    if (left <= 0) return false;
+    a0 = 0;
+    do {
+      ++row;
+      load(a);
+    } while (tiles == 0 && row + 1 < (int)a.rows);
+    return true;
+  }
+};
+
 template <int G, bool GATHER>
-int ka_launch(const Dims& s, const KaArgs& a, int64_t most, cudaStream_t st) {
+__global__ void __launch_bounds__(kKaThreads, 2) kv4_balanced_kernel(const KaArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ long long part[kKaWarps], s_row;
+  __shared__ int s_tile, s_last;
+  float* so = reinterpret_cast<float*>(smem + kKaWarps * kKaRing);  // [warps][G][kD]
+  float2* sml = reinterpret_cast<float2*>(so + kKaWarps * G * kD);            // [warps][G]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t cta = blockIdx.x;
+  // every thread counts the tiles of a run of items, a scan gives where its run begins
+  const int64_t items = GATHER ? a.rows : a.rows / a.Hkv, mult = GATHER ? 1 : a.Hkv;
+  const int64_t per = (items + kKaThreads - 1) / kKaThreads;
+  const int64_t i0 = imin64(threadIdx.x * per, items), i1 = imin64(i0 + per, items);
+  long long mine = 0;
+  for (int64_t i = i0; i < i1; ++i) mine += ka_item_tiles<GATHER>(a, i) * mult;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) part[warp] = incl;
+  // rows without tokens, dealt to all warps of the grid
+  for (int64_t r = cta * kKaWarps + warp; r < a.rows; r += (int64_t)gridDim.x * kKaWarps) {
+    const int b = (int)(r / a.Hkv);
+    if (ka_row<GATHER>(a, r, b).len > 0) continue;
+    const int64_t bq = (int64_t)b * a.Hq + (r % a.Hkv) * G;
+    for (int e = lane; e < G * kD; e += 32) ka_write(a, bq + e / kD, e % kD, 0.0f, 0.0f, 0.0f);
+  }
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kKaWarps; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  const int64_t N = imin64(gridDim.x, total);  // no range is empty
+  if (cta >= N) return;
+  const int64_t g0 = cta * total / N, g1 = (cta + 1) * total / N;
+  if (before <= g0 && g0 < before + mine) {  // one thread's run holds the first tile
+    int64_t at = before;
+    for (int64_t i = i0; i < i1; ++i) {
+      const int t = ka_item_tiles<GATHER>(a, i);
+      if (g0 < at + t * mult) {
+        s_row = i * mult + (g0 - at) / t;
+        s_tile = (int)((g0 - at) % t);
+        break;
+      }
+      at += t * mult;
+    }
+  }
+  __syncthreads();
+  KaSeg<GATHER> cur;
+  cur.row = (int)s_row;
+  cur.a0 = s_tile;
+  cur.left = (int)(g1 - g0);  // a GPU's memory holds far fewer than 2^31 tiles a CTA
+  cur.load(a);
+  // tiles are dealt by their number in the range; `it` runs ahead of `cur`
+  KaSeg<GATHER> it = cur;
+  int dealt = 0, ahead = 0;  // tiles of the range before cur's and it's segment (mod warps)
+  auto deal = [&](int before) { return warp >= before ? warp - before : warp - before + kKaWarps; };
+  bool more = true;
+  KaSrc<GATHER> src;
+  int itile = it.a0 + warp;
+  src.set(a, it.row, it.r, itile, lane);
+  const uint32_t ring = smem_addr(smem) + warp * kKaRing;
+  // past the segment: on to the next one that has a tile for this warp
+  auto settle = [&]() {
+    if (itile < it.a1) return;
+    do {
+      ahead = (ahead + it.a1 - it.a0) % kKaWarps;
+      more = it.next(a);
+      itile = it.a0 + deal(ahead);
+    } while (more && itile >= it.a1);
+    if (more) src.set(a, it.row, it.r, itile, lane);
+  };
+  settle();
+  auto issue = [&](uint32_t stage) {
+    if (more) {
+      src.issue(a, stage, lane);
+      itile += kKaWarps;
+      if (itile < it.a1)
+        src.advance(kKaWarps, lane);
+      else
+        settle();
+    }
+    ka_commit();
+  };
+#pragma unroll
+  for (int d = 0; d < kKaDepth - 1; ++d) issue(ring + d * kKaStage);
+  uint32_t slot = ring, put = ring + (kKaDepth - 1) * kKaStage;
+  bool go = true;
+  while (go) {
+    KaQ Q;
+    ka_load_q<G>(Q, a, cur.row, lane);
+    KaState S;
+    S.clear();
+    for (int t = cur.a0 + deal(dealt); t < cur.a1; t += kKaWarps) {
+      issue(put);
+      ka_wait<kKaDepth - 1>();
+      __syncwarp();
+      ka_tile<G>(S, Q, slot, ka_valid<GATHER>(slot, cur.r.len - t * kKaTile), lane);
+      __syncwarp();
+      put = slot;
+      slot = slot == ring + (kKaDepth - 1) * kKaStage ? ring : slot + kKaStage;
+    }
+    ka_flush<G>(S, so + warp * G * kD, sml + warp * G, lane);
+    __syncthreads();
+    const int b = (int)(cur.row / a.Hkv);
+    const int64_t bq = (int64_t)b * a.Hq + (cur.row % a.Hkv) * G;
+    const bool whole = cur.a0 == 0 && cur.a1 == cur.tiles;
+    const int64_t mypart = 2 * cta + (cur.a0 == 0 ? 1 : 0);
+    for (int e = threadIdx.x; e < G * kD; e += kKaThreads) {
+      const int g = e / kD;
+      float top = kKaEmpty, l = 0.0f, o = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kKaWarps; ++w) top = fmaxf(top, sml[w * G + g].x);
+#pragma unroll
+      for (int w = 0; w < kKaWarps; ++w) {
+        const float f = ka_weight(sml[w * G + g], top);
+        l = fmaf(sml[w * G + g].y, f, l);
+        o = fmaf(so[w * G * kD + e], f, o);
+      }
+      if (whole) {
+        ka_write(a, bq + g, e % kD, o, top, l);
+      } else {
+        a.part_o[mypart * G * kD + e] = o;
+        if (e % kD == 0) a.part_ml[mypart * G + g] = make_float2(top, l);
+      }
+    }
+    if (!whole) {
+      // the row's first tile in the grid's order, hence the CTAs that hold its tiles
+      const int64_t gr = g1 - cur.left - cur.a0;
+      const int64_t ca = ((gr + 1) * N - 1) / total, cz = ((gr + cur.tiles) * N - 1) / total;
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0)
+        s_last = atomicAdd(a.ticket + cur.row, 1u) == (uint32_t)(cz - ca);
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        const int np = (int)(cz - ca) + 1;  // partial 1 of CTA ca, 0 of the ones after it
+        auto at = [&](int i) { return 2 * (ca + i) + (i == 0 ? 1 : 0); };
+        // the weights of all partials, where the states were
+        static_assert(kKaMaxCtas <= kKaWarps * kD / 2, "the states' space holds the weights");
+        float2* w = reinterpret_cast<float2*>(so);
+        for (int i = threadIdx.x; i < np * G; i += kKaThreads)
+          w[i] = __ldcg(a.part_ml + at(i / G) * G + i % G);
+        __syncthreads();
+        for (int e4 = threadIdx.x; e4 < G * kD / 4; e4 += kKaThreads) {
+          const int g = e4 / (kD / 4), j = 4 * (e4 % (kD / 4));
+          float top = kKaEmpty, l = 0.0f;
+          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int i = 0; i < np; ++i) top = fmaxf(top, w[i * G + g].x);
+#pragma unroll 8
+          for (int i = 0; i < np; ++i) {
+            const float4 v =
+                __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * G * kD) + e4);
+            const float f = ka_weight(w[i * G + g], top);
+            l = fmaf(w[i * G + g].y, f, l);
+            o.x = fmaf(v.x, f, o.x);
+            o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z);
+            o.w = fmaf(v.w, f, o.w);
+          }
+          ka_write(a, bq + g, j, o.x, top, l);
+          ka_write(a, bq + g, j + 1, o.y, top, l);
+          ka_write(a, bq + g, j + 2, o.z, top, l);
+          ka_write(a, bq + g, j + 3, o.w, top, l);
+        }
+      }
+    }
+    dealt = (dealt + cur.a1 - cur.a0) % kKaWarps;
+    go = cur.next(a);
+    __syncthreads();  // the states have been read
+  }
+  ka_wait<0>();
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <int G, bool GATHER>
+int ka_launch(const KaArgs& a, int64_t most, cudaStream_t st) {
   const int64_t tiles = (most + kKaTile - 1) / kKaTile;
+  const bool bal = a.rows * tiles >= 1 << 14;
+  if (bal) {
+    const size_t bytes = (size_t)kKaWarps * (kKaRing + G * (kD * 4 + 8));
+    auto kern = kv4_balanced_kernel<G, GATHER>;
+    if (int rc = set_smem_limit((const void*)kern, bytes, "kv4 attend")) return rc;
+    if (cudaMemsetAsync(a.ticket, 0, sizeof(uint32_t) * a.rows, st) != cudaSuccess)
+      return check_launch("kv4 attend: ticket clear");
+    const int grid = (int)imin64(2 * device_sm_count(), kKaMaxCtas);
+    kern<<<grid, kKaThreads, bytes, st>>>(a);
+    note_launches(1);
+    return check_launch("kv4 attend");
+  }
   int cs = 1;
   while (cs < 8 && a.rows * cs * 2 <= 2 * device_sm_count() && cs * 2 * kKaWarps <= tiles) cs *= 2;
   const size_t bytes = (size_t)kKaWarps * kKaRing;
@@ -594,13 +936,16 @@ int ka_launch(const Dims& s, const KaArgs& a, int64_t most, cudaStream_t st) {
 }
 
 template <int G>
-int ka_pick(const Dims& s, const KaArgs& a, int64_t most, cudaStream_t st) {
-  return a.idx ? ka_launch<G, true>(s, a, most, st) : ka_launch<G, false>(s, a, most, st);
+int ka_pick(const KaArgs& a, int64_t most, cudaStream_t st) {
+  return a.idx ? ka_launch<G, true>(a, most, st) : ka_launch<G, false>(a, most, st);
 }
 
 }  // namespace
 
-size_t kv4_attend_workspace_bytes(const Dims&, int64_t) { return 16; }
+size_t kv4_attend_workspace_bytes(const Dims& s, int64_t) {
+  return align256(sizeof(uint32_t) * s.B * s.Hkv) +
+         (size_t)2 * kKaMaxCtas * s.G * (sizeof(float) * kD + sizeof(float2));
+}
 
 int launch_kv4_attend(const Dims& s, const uint16_t* q, const sd_kv4& c, const int32_t* idx,
                       int64_t idx_stride, const int32_t* count, int64_t max_count,
@@ -623,12 +968,17 @@ int launch_kv4_attend(const Dims& s, const uint16_t* q, const sd_kv4& c, const i
   a.scale = scale;
   a.out = out;
   a.lse = lse;
+  uint8_t* p = (uint8_t*)ws;
+  a.ticket = (uint32_t*)p;
+  p += align256(sizeof(uint32_t) * a.rows);
+  a.part_o = (float*)p;
+  a.part_ml = (float2*)(p + sizeof(float) * 2 * kKaMaxCtas * s.G * kD);
   const int64_t most = idx ? max_count : s.n;
   switch (s.G) {
-    case 1: return ka_pick<1>(s, a, most, st);
-    case 2: return ka_pick<2>(s, a, most, st);
-    case 4: return ka_pick<4>(s, a, most, st);
-    default: return ka_pick<8>(s, a, most, st);
+    case 1: return ka_pick<1>(a, most, st);
+    case 2: return ka_pick<2>(a, most, st);
+    case 4: return ka_pick<4>(a, most, st);
+    default: return ka_pick<8>(a, most, st);
   }
 }
 

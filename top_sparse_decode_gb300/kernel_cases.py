@@ -29,6 +29,11 @@ the cases fix those.  Cases:
                 maxima (sd_topk_wmax), as in the long-context step
   attend_1m     gather-attend of 8 rows x 512 selected tokens (sd_gather_attend), the
                 long-context step's shape; K/V of 131,072 tokens
+  kv4_write     4-bit cache: 4 x 8 heads x 32,768 tokens of bf16 K/V quantised (537 MB read)
+  kv4_read      ... and read back as bf16
+  kv4_attend    decode attention over a 4-bit cache, 8 KV heads x 256K tokens (302 MB)
+  kv4_gather    ... over 129 blocks of 16 tokens per KV head, 64 x 8 heads x 16,384 tokens
+                (152 MB gathered)
   topk_quest    top-128 of 1,024 block scores (16-token blocks, last block forced) in
                 each of 64 x 8 rows (sd_topk), the Quest step's selection
 """
@@ -238,6 +243,36 @@ def make_case(name: str):
         lse = torch.empty((1, Hkv * G), dtype=torch.float32, device=DEV)
         return lambda: sd.sd_gather_attend(shp, q, K, V, idx, c, cnt, c, 1 / math.sqrt(128), out,
                                            lse, ws)
+    if name in ("kv4_write", "kv4_read"):
+        B, Hkv, n = 4, 8, 32768
+        K, V = _bf16((B, Hkv, n, 128), gen), _bf16((B, Hkv, n, 128), gen)
+        shp, cache = sd.make_shape(B, Hkv, Hkv, n), sd.Kv4Cache(B, Hkv, n)
+        if name == "kv4_write":
+            return lambda: sd.sd_kv4_write(shp, cache, K, V, n)
+        sd.sd_kv4_write(shp, cache, K, V, n)
+        return lambda: sd.sd_kv4_read(shp, cache, K, V, n)
+    if name in ("kv4_attend", "kv4_gather"):
+        B, n = (1, 1 << 18) if name == "kv4_attend" else (64, 16384)
+        Hkv, G = 8, 4
+        shp, cache = sd.make_shape(B, Hkv * G, Hkv, n), sd.Kv4Cache(B, Hkv, n)
+        for t in range(0, n, 4096):  # written in pieces: a few GB on the device at most
+            K, V = _bf16((B, Hkv, 4096, 128), gen), _bf16((B, Hkv, 4096, 128), gen)
+            sd.sd_kv4_write(shp, cache, K, V, 4096, first=t)
+        q = _bf16((B, Hkv * G, 128), gen)
+        out = torch.empty((B, Hkv * G, 128), dtype=torch.float32, device=DEV)
+        lse = torch.empty((B, Hkv * G), dtype=torch.float32, device=DEV)
+        c = 129 * 16
+        ws = torch.empty(max(sd.sd_kv4_attend_workspace_size(shp),
+                             sd.sd_kv4_gather_attend_workspace_size(shp, c)), dtype=torch.uint8,
+                         device=DEV)
+        if name == "kv4_attend":
+            return lambda: sd.sd_kv4_attend(shp, q, cache, 1 / math.sqrt(128), out, lse, ws)
+        blk = torch.rand((B * Hkv, n // 16), device=DEV, generator=gen).argsort(dim=1)[:, :129]
+        idx = (torch.sort(blk, dim=1).values[..., None] * 16 +
+               torch.arange(16, device=DEV)).flatten(1).to(torch.int32).contiguous()
+        cnt = torch.full((B * Hkv,), c, dtype=torch.int32, device=DEV)
+        return lambda: sd.sd_kv4_gather_attend(shp, q, cache, idx, c, cnt, c, 1 / math.sqrt(128),
+                                               out, lse, ws)
     if name == "merge":
         S, rows, k = 16, 64, 512
         cs = torch.randn((S, rows, k), device=DEV, generator=gen)
