@@ -8,8 +8,9 @@
 // A group is 64 channels of one token's K or V: m = min, s = bf16((max - m) / 15),
 // c = clamp(rint((x - m) / s), 0, 15), and a channel stands for c s + m.
 //
-// One warp per token: lanes 0..15 its K row, lanes 16..31 its V row, 8 channels (one
-// 16-byte load, one 32-bit word of codes) per lane, 8 lanes per group.
+// A warp's lanes 0..15 take a token's K row and lanes 16..31 its V row, 8 channels (one
+// 16-byte access of bf16, one 32-bit word of codes) per lane, 8 lanes per group; four
+// tokens at a time, the next four requested before the current ones are worked on.
 #include "sd_internal.cuh"
 #include "sd_kv4.cuh"
 
@@ -17,6 +18,8 @@ namespace sd {
 namespace {
 
 constexpr int kKvWarps = 8;
+constexpr int kKvRun = 4;                     // tokens a warp has in hand
+constexpr int kKvStep = kKvWarps * kKvRun;    // tokens of a CTA's step
 
 struct KvMoveArgs {
   uint16_t* x[2];        // K, V rows (read by the write, written by the read); null: skipped
@@ -41,67 +44,113 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
+// What a lane moves: its half (0: K, 1: V), octet and row, and the tokens' range.
+struct KvLane {
+  int half, l;
+  int64_t row, t, len, p0, x;  // x: offset of the lane's octet of token 0 in the caller's array
+  __device__ __forceinline__ KvLane(const KvMoveArgs& a) {
+    const int lane = threadIdx.x & 31;
+    half = lane >> 4;
+    l = lane & 15;
+    row = blockIdx.y;
+    const int b = (int)(row / a.hkv), h = (int)(row % a.hkv);
+    kv_range(a, b, len, p0);
+    t = (int64_t)blockIdx.x * kKvStep + (threadIdx.x >> 5) * kKvRun;
+    // tokens [t, len) whose positions lie in the cache, of a half that is asked for
+    len = a.x[half] ? imin64(len, a.n - p0) : 0;
+    x = b * a.sb[half] + h * a.sh[half] + 8 * l;
+  }
+  __device__ __forceinline__ bool in(int64_t i) const { return i < len && p0 + i >= 0; }
+};
+
 __global__ void __launch_bounds__(32 * kKvWarps) kv4_write_kernel(const KvMoveArgs a) {
-  const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-  const int row = blockIdx.y, b = row / a.hkv, h = row % a.hkv;
-  int64_t len, p0;
-  kv_range(a, b, len, p0);
-  const int64_t t = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
-  const int64_t p = p0 + t;
-  if (t >= len || p < 0 || p >= a.n || !a.x[half]) return;  // whole half-warps
-  const unsigned mask = half ? 0xFFFF0000u : 0x0000FFFFu;
-  const uint4 w = *reinterpret_cast<const uint4*>(a.x[half] + b * a.sb[half] + h * a.sh[half] +
-                                                  t * a.st[half] + 8 * l);
-  const float x[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
-                      bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
-  float lo = x[0], hi = x[0];
+  KvLane L(a);
+  const uint16_t* src = a.x[L.half] + L.x;
+  const int64_t base = L.row * a.ncap + L.p0, st = a.st[L.half];
+  uint32_t* code = reinterpret_cast<uint32_t*>(a.code[L.half]) + 2 * (L.l & 7) + (L.l >> 3);
+  uint32_t* scale = reinterpret_cast<uint32_t*>(a.scale) + 2 * L.half + (L.l >> 3);
+  uint4 next[kKvRun];
+  auto fetch = [&](int64_t t) {
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = min_nan(lo, x[i]);
-    hi = fmax_nan(hi, x[i]);
-  }
+    for (int k = 0; k < kKvRun; ++k)
+      next[k] = L.in(t + k) ? __ldcs(reinterpret_cast<const uint4*>(src + (t + k) * st))
+                            : make_uint4(0u, 0u, 0u, 0u);
+  };
+  const int64_t step = (int64_t)gridDim.x * kKvStep;
+  const int64_t most = a.length ? imin64(a.m, a.length[L.row / a.hkv]) : a.m;  // both halves'
+  fetch(L.t);
+  for (int64_t t = L.t; t < most; t += step) {
+    uint4 cur[kKvRun];
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(mask, lo, o));
-    hi = fmax_nan(hi, __shfl_xor_sync(mask, hi, o));
-  }
-  uint32_t sm, word = 0;
-  const float s = kv4_step(lo, hi);
-  if (s != s) {
-    sm = kKv4NanPair;  // a value that is not finite: the group reads as NaN
-  } else {
-    sm = (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
-    const float y = s > 0.0f ? __frcp_rn(s) : 0.0f;
+    for (int k = 0; k < kKvRun; ++k) cur[k] = next[k];
+    fetch(t + step);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) word |= kv4_code(x[i] - lo, s, y) << (4 * i);
+    for (int k = 0; k < kKvRun; ++k) {
+      const uint4 w = cur[k];
+      float lo = min_nan(min_nan(min_nan(bf16_lo(w.x), bf16_hi(w.x)), min_nan(bf16_lo(w.y), bf16_hi(w.y))),
+                         min_nan(min_nan(bf16_lo(w.z), bf16_hi(w.z)), min_nan(bf16_lo(w.w), bf16_hi(w.w))));
+      float hi = fmax_nan(fmax_nan(fmax_nan(bf16_lo(w.x), bf16_hi(w.x)), fmax_nan(bf16_lo(w.y), bf16_hi(w.y))),
+                          fmax_nan(fmax_nan(bf16_lo(w.z), bf16_hi(w.z)), fmax_nan(bf16_lo(w.w), bf16_hi(w.w))));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+        hi = fmax_nan(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+      }
+      const float s = kv4_step(lo, hi);
+      uint32_t sm = (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
+      uint32_t word = kv4_word(w, lo, s, s > 0.0f ? __frcp_rn(s) : 0.0f);
+      if (s != s) {  // a value that is not finite: the group reads as NaN
+        sm = kKv4NanPair;
+        word = 0;
+      }
+      if (L.in(t + k)) {
+        const int64_t tok = base + t + k;
+        code[tok * (kKv4Row / 4)] = word;
+        if ((L.l & 7) == 0) scale[tok * (kKv4Scales / 2)] = sm;
+      }
+    }
   }
-  const int64_t tok = (int64_t)row * a.ncap + p;
-  reinterpret_cast<uint32_t*>(a.code[half] + tok * kKv4Row)[2 * (l & 7) + (l >> 3)] = word;
-  if ((l & 7) == 0)
-    reinterpret_cast<uint32_t*>(a.scale + tok * kKv4Scales)[2 * half + (l >> 3)] = sm;
 }
 
 __global__ void __launch_bounds__(32 * kKvWarps) kv4_read_kernel(const KvMoveArgs a) {
-  const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-  const int row = blockIdx.y, b = row / a.hkv, h = row % a.hkv;
-  int64_t len, p0;
-  kv_range(a, b, len, p0);
-  const int64_t t = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
-  const int64_t p = p0 + t;
-  if (t >= len || p < 0 || p >= a.n || !a.x[half]) return;
-  const int64_t tok = (int64_t)row * a.ncap + p;
-  const uint32_t word =
-      reinterpret_cast<const uint32_t*>(a.code[half] + tok * kKv4Row)[2 * (l & 7) + (l >> 3)];
-  const uint32_t sm =
-      reinterpret_cast<const uint32_t*>(a.scale + tok * kKv4Scales)[2 * half + (l >> 3)];
-  const float s = bf16_lo(sm), m = bf16_hi(sm);
-  uint4 o;
-  o.x = kv4_pair(word, 0, s, m);
-  o.y = kv4_pair(word, 8, s, m);
-  o.z = kv4_pair(word, 16, s, m);
-  o.w = kv4_pair(word, 24, s, m);
-  *reinterpret_cast<uint4*>(a.x[half] + b * a.sb[half] + h * a.sh[half] + t * a.st[half] +
-                            8 * l) = o;
+  KvLane L(a);
+  uint16_t* dst = a.x[L.half] + L.x;
+  const int64_t base = L.row * a.ncap + L.p0, st = a.st[L.half];
+  const uint32_t* code =
+      reinterpret_cast<const uint32_t*>(a.code[L.half]) + 2 * (L.l & 7) + (L.l >> 3);
+  const uint32_t* scale = reinterpret_cast<const uint32_t*>(a.scale) + 2 * L.half + (L.l >> 3);
+  uint32_t nw[kKvRun], ns[kKvRun];
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int k = 0; k < kKvRun; ++k) {
+      const bool ok = L.in(t + k);
+      const int64_t tok = base + t + k;
+      nw[k] = ok ? __ldcs(code + tok * (kKv4Row / 4)) : 0u;
+      ns[k] = ok ? __ldcs(scale + tok * (kKv4Scales / 2)) : 0u;
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * kKvStep;
+  fetch(L.t);
+  for (int64_t t = L.t; t < L.len; t += step) {
+    uint32_t cw[kKvRun], cs[kKvRun];
+#pragma unroll
+    for (int k = 0; k < kKvRun; ++k) {
+      cw[k] = nw[k];
+      cs[k] = ns[k];
+    }
+    fetch(t + step);
+#pragma unroll
+    for (int k = 0; k < kKvRun; ++k) {
+      if (!L.in(t + k)) continue;
+      const float s = bf16_lo(cs[k]), m = bf16_hi(cs[k]);
+      uint4 o;
+      o.x = kv4_pair(cw[k], 0, s, m);
+      o.y = kv4_pair(cw[k], 8, s, m);
+      o.z = kv4_pair(cw[k], 16, s, m);
+      o.w = kv4_pair(cw[k], 24, s, m);
+      *reinterpret_cast<uint4*>(dst + (t + k) * st) = o;
+    }
+  }
 }
 
 }  // namespace
@@ -128,8 +177,10 @@ int launch_kv4_move(bool write, const Dims& s, const sd_kv4& c, void* K, const s
   a.first = first;
   a.pos = pos;
   a.length = length;
-  const int64_t warps = imin64(m, kKvWarps);
-  const dim3 grid((unsigned)((m + warps - 1) / warps), (unsigned)(s.B * s.Hkv));
+  // a few steps per CTA where there are many tokens: four waves of the GPU
+  const int64_t rows = (int64_t)s.B * s.Hkv, steps = (m + kKvStep - 1) / kKvStep;
+  const int64_t waves = imax64(1, (int64_t)device_sm_count() * 32 / rows);
+  const dim3 grid((unsigned)imin64(steps, waves), (unsigned)rows);
   if (write)
     kv4_write_kernel<<<grid, 32 * kKvWarps, 0, st>>>(a);
   else

@@ -11,30 +11,77 @@ constexpr int kKv4Row = 64;     // code bytes of a token's K (or V) row
 constexpr int kKv4Scales = 8;   // bf16 values of a token's scale record
 constexpr uint32_t kKv4NanPair = 0x7FC07FC0u;
 
+// Pairs of fp32 values, one instruction for both.
+__device__ __forceinline__ uint64_t f2_make(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// d / s from y = 1 / s, correctly rounded: t = d y, t + y (d - t s) (P. W. Markstein, IBM J.
+// Res. Dev. 34(1), 1990).  A plain product d y would break the exact ties that coarse
+// bf16 inputs hit often.
+__device__ __forceinline__ float kv4_divide(float d, float s, float y) {
+  const float t = d * y;
+  return fmaf(fmaf(-t, s, d), y, t);
+}
+__device__ __forceinline__ uint64_t kv4_divide2(uint64_t d, uint64_t neg_s, uint64_t y) {
+  const uint64_t t = f2_mul(d, y);
+  return f2_fma(f2_fma(t, neg_s, d), y, t);
+}
+
 // A group's step: bf16((hi - lo) / 15), the fp32 quotient rounded to nearest even; 0
-// below 2^-100 (the remainders that kv4_code forms stay exact); NaN when a value of the
+// below 2^-100 (the remainders of the divisions by it stay exact); NaN when a value of the
 // group is not finite or the step overflows.
 __device__ __forceinline__ float kv4_step(float lo, float hi) {
-  const float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(hi - lo, 15.0f)));
+  const float q = kv4_divide(hi - lo, 15.0f, 0.0666666701f);  // the fp32 nearest to 1 / 15
+  const float s = __bfloat162float(__float2bfloat16_rn(q));
   if (!(s < INFINITY)) return __uint_as_float(0x7FC00000u);
   return s < 7.8886091e-31f ? 0.0f : s;
 }
 
-// clamp(rint(d / s), 0, 15) for d >= 0; y = 1 / s correctly rounded (0 for s = 0).  The
-// quotient is formed as t = d y, t + y (d - t s), which is the correctly rounded d / s
-// (P. W. Markstein, IBM J. Res. Dev. 34(1), 1990): a plain product d y breaks the exact
-// ties that coarse bf16 inputs hit often.
-__device__ __forceinline__ uint32_t kv4_code(float d, float s, float y) {
-  const float t = d * y;
-  const float q = fmaf(fmaf(-t, s, d), y, t);
-  return (uint32_t)fminf(rintf(q), 15.0f);
+// A word of codes from the octet x: clamp(rint((x - lo) / s), 0, 15) at bits 4 i; y = 1 / s
+// correctly rounded, or 0 for s = 0 (codes 0).
+__device__ __forceinline__ uint32_t kv4_word(const uint4& x, float lo, float s, float y) {
+  const uint64_t l2 = f2_make(-lo, -lo), s2 = f2_make(-s, -s), y2 = f2_make(y, y);
+  // adding 1.5 2^23 rounds to a whole number (ties to even) in the low mantissa bits
+  constexpr float kMagic = 12582912.0f;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    float q0, q1;
+    f2_split(kv4_divide2(f2_add(f2_make(bf16_lo(w[i]), bf16_hi(w[i])), l2), s2, y2), q0, q1);
+    word = word * 16u + (__float_as_uint(fminf(q1, 15.0f) + kMagic) - 0x4B400000u);
+    word = word * 16u + (__float_as_uint(fminf(q0, 15.0f) + kMagic) - 0x4B400000u);
+  }
+  return word;
 }
 
 // Two channels of a word of codes (from bit sh) as packed bf16.
 __device__ __forceinline__ uint32_t kv4_pair(uint32_t word, int sh, float s, float m) {
-  const float a = fmaf((float)((word >> sh) & 15u), s, m);
-  const float b = fmaf((float)((word >> (sh + 4)) & 15u), s, m);
-  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  // a code under the exponent of 2^23 is 2^23 + c
+  const float a = __uint_as_float((word >> sh & 15u) | 0x4B000000u) - 8388608.0f;
+  const float b = __uint_as_float((word >> (sh + 4) & 15u) | 0x4B000000u) - 8388608.0f;
+  const __nv_bfloat162 r = __floats2bfloat162_rn(fmaf(a, s, m), fmaf(b, s, m));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 

@@ -16,7 +16,7 @@
 //  * PV: O^T = V^T P^T, 16 channels as rows, heads as columns, 16 tokens deep.  w = p s f is
 //    split in two f16 parts (22 bits; f a power of two per head and group that holds the
 //    largest w in [2^7, 2^14], raised and lowered as an online softmax moves its
-//    maximum).  With G <= 4 the columns 4..7 repeat the heads and take the low parts (8
+//    maximum).  With G <= 4 columns 0..3 take the high parts and 4..7 the low ones (8
 //    MMAs per 16 tokens), with G = 8 the low parts are 8 more.
 //  * p = 2^(z log2 e - m); m, a whole number per head, is raised only when a logit
 //    exceeds it by about 8.
@@ -66,9 +66,9 @@ struct KaArgs {
   float scale;
   float* out;
   float* lse;
-  uint32_t* ticket;  // [rows], zero at launch (balanced kernel)
-  float* part_o;     // [2 CTAs][G][kD]
-  float2* part_ml;   // [2 CTAs][G]
+  int2* meta;       // [rows]: the first warp that holds tiles of the row and how many do
+  float* part_o;    // [2 warps][G][kD]
+  float2* part_ml;  // [2 warps][G]
 };
 
 // Tokens of a row: positions [t0, t0 + len) of the sequence, or len entries of idx.
@@ -95,6 +95,11 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
 // 16 bytes into shared memory; zeros where v is false.
 __device__ __forceinline__ void ka_copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+// ... of scattered rows: without more of the neighbourhood than a 64-byte row.
+__device__ __forceinline__ void ka_copy16_near(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16;\n" ::"r"(dst), "l"(src)
+               : "memory");
 }
 __device__ __forceinline__ void ka_copy16(uint32_t dst, const void* src, bool v) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
@@ -169,6 +174,12 @@ struct KaSrc {
     }
     fetch(lane);
   }
+  // p + t bytes
+  static __device__ __forceinline__ const uint8_t* at(const uint8_t* p, uint32_t t, int bytes) {
+    uint64_t r;
+    asm("mad.wide.u32 %0, %1, %2, %3;\n" : "=l"(r) : "r"(t), "r"(bytes), "l"(p));
+    return reinterpret_cast<const uint8_t*>(r);
+  }
   __device__ __forceinline__ void issue(const KaArgs& a, uint32_t stage, int lane) const {
     const int tl = lane >> 2;
     const uint32_t dst = stage + tl * kKv4Row + (((lane & 3) ^ (tl & 2)) * 16);
@@ -176,15 +187,25 @@ struct KaSrc {
     if (GATHER) {
       const bool ok = (unsigned)tok < (unsigned)a.n;
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
-      const int safe = ok ? tok : 0;
+      const uint32_t safe = ok ? tok : 0;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const int64_t off = (int64_t)__shfl_sync(0xFFFFFFFFu, safe, tl + 8 * h) * kKv4Row;
-        const bool val = mask >> (tl + 8 * h) & 1u;
-        ka_copy16(dst + h * 8 * kKv4Row, k + off, val);
-        ka_copy16(dst + h * 8 * kKv4Row + kKaOffV, v + off, val);
+        const uint32_t t = __shfl_sync(0xFFFFFFFFu, safe, tl + 8 * h);
+        const uint8_t *kt = at(k, t, kKv4Row), *vt = at(v, t, kKv4Row);
+        if (mask == 0xFFFFFFFFu) {
+          ka_copy16_near(dst + h * 8 * kKv4Row, kt);
+          ka_copy16_near(dst + h * 8 * kKv4Row + kKaOffV, vt);
+        } else {
+          const bool val = mask >> (tl + 8 * h) & 1u;
+          ka_copy16(dst + h * 8 * kKv4Row, kt, val);
+          ka_copy16(dst + h * 8 * kKv4Row + kKaOffV, vt, val);
+        }
       }
-      ka_copy16(dsts, s + (int64_t)safe * kKv4Scales, ok);
+      const uint8_t* stk = at(reinterpret_cast<const uint8_t*>(s), safe, 2 * kKv4Scales);
+      if (mask == 0xFFFFFFFFu)
+        ka_copy16_near(dsts, stk);
+      else
+        ka_copy16(dsts, stk, ok);
       if (lane == 0) sts32(stage + kKaOffMask, mask);
     } else if (left >= kKaTile) {
 #pragma unroll
@@ -207,8 +228,10 @@ struct KaSrc {
 };
 
 // q as the B operand, and per-head constants of the lane's two columns (heads).
+template <int G>
 struct KaQ {
-  uint32_t b[2][4][2];  // [group][k-step][half]
+  // [columns 0..3 or 4..7 (G = 8: all at once)][group][k-step][half]
+  uint32_t b[G == 8 ? 1 : 2][2][4][2];
   float ch[2];          // scale log2(e) 2^9 / (q's power of two)
   float qs[2][2];       // [column][group]: scale log2(e) sum of the group's q
 };
@@ -220,7 +243,7 @@ __device__ __forceinline__ int ka_head(int c) {
 }
 
 template <int G>
-__device__ __forceinline__ void ka_load_q(KaQ& Q, const KaArgs& a, int64_t row, int lane) {
+__device__ __forceinline__ void ka_load_q(KaQ<G>& Q, const KaArgs& a, int64_t row, int lane) {
   const int gid = lane >> 2, tig = lane & 3;
   const int b = (int)(row / a.Hkv), h = (int)(row % a.Hkv), hd = ka_head<G>(gid);
   const bool real = hd < G;
@@ -259,8 +282,18 @@ __device__ __forceinline__ void ka_load_q(KaQ& Q, const KaArgs& a, int64_t row, 
       for (int s = 0; s < 2; ++s) {
         const __half2 lo = __floats2half2_rn(bf16_lo(x[s]) * up, bf16_lo(x[s + 2]) * up);
         const __half2 hi = __floats2half2_rn(bf16_hi(x[s]) * up, bf16_hi(x[s + 2]) * up);
-        Q.b[g][2 * j + s][0] = *reinterpret_cast<const uint32_t*>(&lo);
-        Q.b[g][2 * j + s][1] = *reinterpret_cast<const uint32_t*>(&hi);
+        const uint32_t x0 = *reinterpret_cast<const uint32_t*>(&lo);
+        const uint32_t x1 = *reinterpret_cast<const uint32_t*>(&hi);
+        if constexpr (G == 8) {
+          Q.b[0][g][2 * j + s][0] = x0;
+          Q.b[0][g][2 * j + s][1] = x1;
+        } else {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            Q.b[t][g][2 * j + s][0] = gid >> 2 == t ? x0 : 0u;
+            Q.b[t][g][2 * j + s][1] = gid >> 2 == t ? x1 : 0u;
+          }
+        }
       }
     }
   const float sl = a.scale * kKaLog2e;
@@ -305,7 +338,8 @@ __device__ __forceinline__ uint32_t ka_mid_hi(uint32_t x) {
 }
 
 // A warp's online softmax.  o: sum w (c - 7.5) in units of 2^-9; tile 4 g + u holds channels 64 g + 8 gid + 2 u (o[..][e]) and + 1 (o[..][2 + e]) of
-// columns 2 tig + e.  mo: sum p (m + 7.5 s).  l, mo: this lane's tokens only.
+// columns 2 tig + e (G <= 4: columns 4..7 the low parts).  m, f: of those columns' heads;
+// mo: sum p (m + 7.5 s); l, mo: this lane's tokens only.
 struct KaState {
   float o[8][4];
   float m[2], l[2];
@@ -328,10 +362,11 @@ struct KaState {
   }
 };
 
-// The largest x over the lanes that hold the same columns.
-__device__ __forceinline__ float ka_col_max(float x) {
+// The largest x over the lanes that hold the same heads.
+template <int G>
+__device__ __forceinline__ float ka_head_max(float x) {
 #pragma unroll
-  for (int o = 4; o <= 16; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  for (int o = G == 8 ? 4 : 2; o <= 16; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
   return x;
 }
 
@@ -380,19 +415,23 @@ __device__ __forceinline__ uint32_t ka_pack(float lo, float hi) {
 // One tile, as two 16-token halves; valid: its tokens.  Row r of a half's score tile is
 // token tau(r) (r < 8: r / 2, odd rows 4 + (r / 2 ^ 1)) or tau(r - 8) + 8: with the
 // swizzle, any eight lanes of a K read and any sixteen of a V read touch each bank once.
+// G = 8: a lane has the logits of two heads and four tokens.  G <= 4: the first half's
+// heads are columns 0..3 and the second's 4..7 (q's other columns are zero), so that a
+// lane has two heads and the two tokens of its half, and no logit is computed twice.
 template <int G>
-__device__ __forceinline__ void ka_tile(KaState& S, const KaQ& Q, uint32_t st, uint32_t valid,
+__device__ __forceinline__ void ka_tile(KaState& S, const KaQ<G>& Q, uint32_t st, uint32_t valid,
                                         int lane) {
+  constexpr int NR = G == 8 ? 4 : 2;  // this lane's tokens
   const int gid = lane >> 2, tig = lane & 3;
   const int tk = (gid & 1) ? 4 + (gid >> 1 ^ 1) : gid >> 1;
-  float dot[4][2];                               // [2 half + r][column]: sum_g s_g <q, c>_g
-  float mk[4][2], sv[4][2], mv[4][2];            // [2 half + r][group]
+  const int side = G == 8 ? 0 : tig >> 1;  // G <= 4: the half of this lane's tokens
+  float acc[G == 8 ? 2 : 1][2][4];         // [half][group]
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
     const uint32_t ak = st + (16 * hf + tk) * kKv4Row + ((tig ^ (gid >> 1 & 2)) * 16);
     const uint4 ka = lds128(ak), kb = lds128(ak + 8 * kKv4Row);
     const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-    float acc[2][4];  // [group]
+    constexpr bool both = G != 8;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -402,50 +441,53 @@ __device__ __forceinline__ void ka_tile(KaState& S, const KaQ& Q, uint32_t st, u
           const uint32_t xa = wa[2 * j + g] >> (8 * s), xb = wb[2 * j + g] >> (8 * s);
           const uint32_t a0 = ka_code_lo(xa), a1 = ka_code_lo(xb);
           const uint32_t a2 = ka_code_hi(xa), a3 = ka_code_hi(xb);
-          const uint32_t(&qb)[2] = Q.b[g][2 * j + s];
-          if (j + s == 0)
-            mma_f16_zero(acc[g], a0, a1, a2, a3, qb[0], qb[1]);
+          const uint32_t(&qb)[2] = Q.b[both ? hf : 0][g][2 * j + s];
+          if (j + s == 0 && (!both || hf == 0))
+            mma_f16_zero(acc[both ? 0 : hf][g], a0, a1, a2, a3, qb[0], qb[1]);
           else
-            mma_f16(acc[g], a0, a1, a2, a3, qb[0], qb[1]);
+            mma_f16(acc[both ? 0 : hf][g], a0, a1, a2, a3, qb[0], qb[1]);
         }
+  }
+  float dot[NR][2], mk[NR][2], sv[NR][2], mv[NR][2];  // [token][column or group]
+  auto token = [&](int i) { return (G == 8 ? 16 * (i >> 1) : 16 * side) + tk + 8 * (i & 1); };
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const uint4 sc = lds128(st + kKaOffS + (16 * hf + tk + 8 * r) * 16);
-      const int i = 2 * hf + r;
-      const float sk0 = bf16_lo(sc.x), sk1 = bf16_lo(sc.y);
-      mk[i][0] = bf16_hi(sc.x);
-      mk[i][1] = bf16_hi(sc.y);
-      sv[i][0] = bf16_lo(sc.z);
-      sv[i][1] = bf16_lo(sc.w);
-      mv[i][0] = fmaf(7.5f, sv[i][0], bf16_hi(sc.z));  // the middle of the group's range
-      mv[i][1] = fmaf(7.5f, sv[i][1], bf16_hi(sc.w));
+  for (int i = 0; i < NR; ++i) {
+    const uint4 sc = lds128(st + kKaOffS + token(i) * 16);
+    const float sk0 = bf16_lo(sc.x), sk1 = bf16_lo(sc.y);
+    mk[i][0] = bf16_hi(sc.x);
+    mk[i][1] = bf16_hi(sc.y);
+    sv[i][0] = bf16_lo(sc.z);
+    sv[i][1] = bf16_lo(sc.w);
+    mv[i][0] = fmaf(7.5f, sv[i][0], bf16_hi(sc.z));  // the middle of the group's range
+    mv[i][1] = fmaf(7.5f, sv[i][1], bf16_hi(sc.w));
+    const float(&ac)[2][4] = acc[i >> 1];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        dot[i][e] = fmaf(sk1, acc[1][2 * r + e], sk0 * acc[0][2 * r + e]);
-    }
+    for (int e = 0; e < 2; ++e)
+      dot[i][e] = fmaf(sk1, ac[1][2 * (i & 1) + e], sk0 * ac[0][2 * (i & 1) + e]);
   }
   // log2 of the weight over 2^sub
   auto logit = [&](int i, int e, float sub) {
     return fmaf(dot[i][e], Q.ch[e], fmaf(mk[i][1], Q.qs[e][1], fmaf(mk[i][0], Q.qs[e][0], -sub)));
   };
-  auto ok = [&](int i) { return valid >> (16 * (i >> 1) + tk + 8 * (i & 1)) & 1u; };
-  float p[4][2], sum[2];
+  auto ok = [&](int i) { return valid >> token(i) & 1u; };
+  float p[NR][2], sum[2];
   auto weights = [&](int e) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i][e] = ka_exp2(logit(i, e, S.m[e]));
+    for (int i = 0; i < NR; ++i) p[i][e] = ka_exp2(logit(i, e, S.m[e]));
     if (valid != 0xFFFFFFFFu) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < NR; ++i)
         if (!ok(i)) p[i][e] = 0.0f;
     }
-    sum[e] = (p[0][e] + p[1][e]) + (p[2][e] + p[3][e]);
+    sum[e] = p[0][e] + p[1][e];
+    if constexpr (NR == 4) sum[e] += p[2][e] + p[3][e];
   };
   weights(0);
   weights(1);
-  uint32_t hi[4][2];  // w's high parts, a pair of columns each
+  uint32_t hi[NR][2];  // w's high parts, a pair of columns each
   auto weigh = [&]() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
       for (int g = 0; g < 2; ++g)
         hi[i][g] = ka_pack(p[i][0] * (sv[i][g] * S.f[0][g]), p[i][1] * (sv[i][g] * S.f[1][g]));
@@ -453,24 +495,26 @@ __device__ __forceinline__ void ka_tile(KaState& S, const KaQ& Q, uint32_t st, u
   weigh();
   __half2 ht = *reinterpret_cast<__half2*>(&hi[0][0]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) ht = __hmax2(ht, *reinterpret_cast<__half2*>(&hi[i >> 1][i & 1]));
+  for (int i = 1; i < 2 * NR; ++i)
+    ht = __hmax2(ht, *reinterpret_cast<__half2*>(&hi[i >> 1][i & 1]));
   const uint32_t hb = *reinterpret_cast<uint32_t*>(&ht);
-  const bool over = fmaxf(sum[0], sum[1]) > kKaPMax || (hb & 0xFFFFu) > 0x7400u || hb > 0x7400FFFFu;
+  const bool over =
+      fmaxf(sum[0], sum[1]) > kKaPMax || (hb & 0xFFFFu) > 0x7400u || hb > 0x7400FFFFu;
   if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float zt = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < NR; ++i)
         if (ok(i)) zt = fmaxf(zt, logit(i, e, 0.0f));
-      ka_raise_m(S, e, ka_col_max(zt));
+      ka_raise_m(S, e, ka_head_max<G>(zt));
       weights(e);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         float wt = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wt = fmaxf(wt, p[i][e] * sv[i][g]);
-        ka_lower_f(S, e, g, ka_col_max(wt));
+        for (int i = 0; i < NR; ++i) wt = fmaxf(wt, p[i][e] * sv[i][g]);
+        ka_lower_f(S, e, g, ka_head_max<G>(wt));
       }
     }
     weigh();
@@ -481,22 +525,26 @@ __device__ __forceinline__ void ka_tile(KaState& S, const KaQ& Q, uint32_t st, u
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S.mo[e][g] = fmaf(p[i][e], mv[i][g], S.mo[e][g]);
+      for (int i = 0; i < NR; ++i) S.mo[e][g] = fmaf(p[i][e], mv[i][g], S.mo[e][g]);
   }
-  // P^T's high and low f16 parts, as B operands
+  // P^T's high and low f16 parts, as B operands: G = 8 bh and bl; G <= 4 columns 0..3 of bh
+  // the high parts of its half's heads, 4..7 the low parts
   uint32_t bh[2][2][2], bl[2][2][2];  // [half][group][r]
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < NR; ++i)
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const float2 h2 = __half22float2(*reinterpret_cast<const __half2*>(&hi[i][g]));
       const uint32_t lo = ka_pack(fmaf(p[i][0], sv[i][g] * S.f[0][g], -h2.x),
                                   fmaf(p[i][1], sv[i][g] * S.f[1][g], -h2.y));
-      if (G == 8) {
+      if constexpr (G == 8) {
         bh[i >> 1][g][i & 1] = transpose_8x8(hi[i][g]);
         bl[i >> 1][g][i & 1] = transpose_8x8(lo);
-      } else {
-        bh[i >> 1][g][i & 1] = transpose_8x8(tig < 2 ? hi[i][g] : lo);
+      } else {  // the first half's low parts move to the lanes of columns 4..7, the
+                // second's high parts to those of 0..3
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, side ? hi[i][g] : lo, 2);
+        bh[0][g][i] = transpose_8x8(side ? got : hi[i][g]);
+        bh[1][g][i] = transpose_8x8(side ? lo : got);
       }
     }
   // rows 2 tig, 2 tig + 1 (and + 8) of V's halves, 8 bytes from byte 8 gid: channels 8 gid ..
@@ -544,21 +592,31 @@ __device__ __forceinline__ uint32_t ka_valid(uint32_t stage, int left) {
   return left >= kKaTile ? 0xFFFFFFFFu : (1u << left) - 1u;
 }
 
-// The state of a warp in natural units, written to so [G][kD] and sml [G] = (m, l).
-template <int G>
-__device__ __forceinline__ void ka_flush(KaState& S, float* so, float2* sml, int lane) {
+// The state of a warp in natural units, written to so [G][kD] and sml [G] = (m, l); with
+// DONE it is the whole row's: so is out, divided by l, and lse (or null) takes the place
+// of sml.
+template <int G, bool DONE>
+__device__ __forceinline__ void ka_flush(KaState& S, float* so, float2* sml, float* lse,
+                                         int lane) {
   const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
 #pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) {
+    for (int o = G == 8 ? 4 : 2; o <= 16; o <<= 1) {
       S.l[e] += __shfl_xor_sync(0xFFFFFFFFu, S.l[e], o);
       S.mo[e][0] += __shfl_xor_sync(0xFFFFFFFFu, S.mo[e][0], o);
       S.mo[e][1] += __shfl_xor_sync(0xFFFFFFFFu, S.mo[e][1], o);
     }
     const int c = 2 * tig + e, hd = ka_head<G>(c);
     const bool mine = c < G;
-    if (mine && gid == 0) sml[hd] = make_float2(S.m[e], S.l[e]);
+    const float l = S.l[e];
+    if (mine && gid == 0) {
+      if (!DONE)
+        sml[hd] = make_float2(S.m[e], l);
+      else if (lse)
+        lse[hd] = l != 0.0f ? (S.m[e] + log2f(l)) * kKaLn2 : -INFINITY;
+    }
+    const float inv = !DONE ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;  // an empty row gives 0
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const float k = 512.0f / S.f[e][g];
@@ -570,8 +628,8 @@ __device__ __forceinline__ void ka_flush(KaState& S, float* so, float2* sml, int
           even += __shfl_xor_sync(0xFFFFFFFFu, even, 2);
           odd += __shfl_xor_sync(0xFFFFFFFFu, odd, 2);
         }
-        x[2 * u] = fmaf(even, k, S.mo[e][g]);
-        x[2 * u + 1] = fmaf(odd, k, S.mo[e][g]);
+        x[2 * u] = fmaf(even, k, S.mo[e][g]) * inv;
+        x[2 * u + 1] = fmaf(odd, k, S.mo[e][g]) * inv;
       }
       if (mine) {
         float4* d = reinterpret_cast<float4*>(so + hd * kD + 64 * g + 8 * gid);
@@ -617,7 +675,7 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs
     }
     ka_commit();
   }
-  KaQ Q;
+  KaQ<G> Q;
   ka_load_q<G>(Q, a, row, lane);
   KaState S;
   S.clear();
@@ -641,7 +699,7 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs
   float2* sml = reinterpret_cast<float2*>(so + kKaWarps * G * kD);  // [warps][G]
   float* co = reinterpret_cast<float*>(sml + kKaWarps * G);  // the CTA's: [G][kD]
   float2* cml = reinterpret_cast<float2*>(co + G * kD);      // [G]
-  ka_flush<G>(S, so + warp * G * kD, sml + warp * G, lane);
+  ka_flush<G, false>(S, so + warp * G * kD, sml + warp * G, nullptr, lane);
   __syncthreads();
   for (int e = threadIdx.x; e < G * kD; e += kKaThreads) {
     const int g = e / kD;
@@ -680,11 +738,10 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs
 }
 
 // Many tokens: the rows' tiles, in row-major order, are cut into equal ranges, one per
-// CTA; within a CTA they are dealt to the warps in turn and each warp's ring runs on
-// across rows.  A row that lies within a range is written at once; a row cut by ranges
-// leaves a partial per range, and the CTA that brings its last one (a ticket) joins them
-// in range order.
-constexpr int kKaMaxCtas = 320;  // partials of the workspace: two per CTA
+// warp of the grid, and each warp's ring runs on across rows.  A row that lies within a
+// range is written at once; a row cut by ranges leaves a partial per range, and a second
+// kernel joins them in range order.
+constexpr int kKaMaxWarps = 320 * kKaWarps;  // partials of the workspace: two per warp
 
 // Items of the partition: sequences of Hkv rows each, or single rows with counts of
 // their own.
@@ -694,7 +751,8 @@ __device__ __forceinline__ int ka_item_tiles(const KaArgs& a, int64_t item) {
   return (r.len + kKaTile - 1) / kKaTile;
 }
 
-// A segment: tiles [a0, a1) of a row; left: tiles of the range from a0 on.
+// A segment: tiles [a0, a1) of a row; left: tiles of the range from a0 on (a GPU's memory
+// holds far fewer than 2^31 tiles a warp).
 template <bool GATHER>
 struct KaSeg {
   int row, left, a0, a1, tiles;
@@ -718,21 +776,17 @@ struct KaSeg {
 };
 
 template <int G, bool GATHER>
-__global__ void __launch_bounds__(kKaThreads, 2) kv4_balanced_kernel(const KaArgs a) {
+__global__ void __launch_bounds__(kKaThreads, 2) kv4_stream_kernel(const KaArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ long long part[kKaWarps], s_row;
-  __shared__ int s_tile, s_last;
-  float* so = reinterpret_cast<float*>(smem + kKaWarps * kKaRing);  // [warps][G][kD]
-  float2* sml = reinterpret_cast<float2*>(so + kKaWarps * G * kD);            // [warps][G]
+  __shared__ long long ends[kKaThreads], part[kKaWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t cta = blockIdx.x;
-  // every thread counts the tiles of a run of items, a scan gives where its run begins
+  const int64_t gw = (int64_t)blockIdx.x * kKaWarps + warp, W = (int64_t)gridDim.x * kKaWarps;
+  // every thread counts the tiles of a run of items, a scan gives where its run ends
   const int64_t items = GATHER ? a.rows : a.rows / a.Hkv, mult = GATHER ? 1 : a.Hkv;
   const int64_t per = (items + kKaThreads - 1) / kKaThreads;
   const int64_t i0 = imin64(threadIdx.x * per, items), i1 = imin64(i0 + per, items);
-  long long mine = 0;
-  for (int64_t i = i0; i < i1; ++i) mine += ka_item_tiles<GATHER>(a, i) * mult;
-  long long incl = mine;
+  long long incl = 0;
+  for (int64_t i = i0; i < i1; ++i) incl += ka_item_tiles<GATHER>(a, i) * mult;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
@@ -740,160 +794,156 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_balanced_kernel(const KaArg
   }
   if (lane == 31) part[warp] = incl;
   // rows without tokens, dealt to all warps of the grid
-  for (int64_t r = cta * kKaWarps + warp; r < a.rows; r += (int64_t)gridDim.x * kKaWarps) {
+  for (int64_t r = gw; r < a.rows; r += W) {
     const int b = (int)(r / a.Hkv);
     if (ka_row<GATHER>(a, r, b).len > 0) continue;
     const int64_t bq = (int64_t)b * a.Hq + (r % a.Hkv) * G;
     for (int e = lane; e < G * kD; e += 32) ka_write(a, bq + e / kD, e % kD, 0.0f, 0.0f, 0.0f);
+    if (lane == 0) a.meta[r] = make_int2(0, 0);
   }
   __syncthreads();
-  long long before = incl - mine, total = 0;
+  long long total = 0;
 #pragma unroll
   for (int w = 0; w < kKaWarps; ++w) {
-    if (w < warp) before += part[w];
+    if (w < warp) incl += part[w];
     total += part[w];
   }
-  const int64_t N = imin64(gridDim.x, total);  // no range is empty
-  if (cta >= N) return;
-  const int64_t g0 = cta * total / N, g1 = (cta + 1) * total / N;
-  if (before <= g0 && g0 < before + mine) {  // one thread's run holds the first tile
-    int64_t at = before;
-    for (int64_t i = i0; i < i1; ++i) {
-      const int t = ka_item_tiles<GATHER>(a, i);
-      if (g0 < at + t * mult) {
-        s_row = i * mult + (g0 - at) / t;
-        s_tile = (int)((g0 - at) % t);
-        break;
-      }
-      at += t * mult;
-    }
-  }
+  ends[threadIdx.x] = incl;
   __syncthreads();
+  const int64_t N = imin64(W, total);  // no range is empty
+  if (gw >= N) return;
+  const int64_t g0 = gw * total / N, g1 = (gw + 1) * total / N;
   KaSeg<GATHER> cur;
-  cur.row = (int)s_row;
-  cur.a0 = s_tile;
-  cur.left = (int)(g1 - g0);  // a GPU's memory holds far fewer than 2^31 tiles a CTA
-  cur.load(a);
-  // tiles are dealt by their number in the range; `it` runs ahead of `cur`
-  KaSeg<GATHER> it = cur;
-  int dealt = 0, ahead = 0;  // tiles of the range before cur's and it's segment (mod warps)
-  auto deal = [&](int before) { return warp >= before ? warp - before : warp - before + kKaWarps; };
+  {
+    // the run that holds the first tile, then the item in it
+    int run = 0;
+#pragma unroll
+    for (int k = 0; k < kKaWarps; ++k)
+      run += __popc(__ballot_sync(0xFFFFFFFFu, ends[32 * k + lane] <= g0));
+    int64_t at = run ? ends[run - 1] : 0, item = run * per;
+    int t = ka_item_tiles<GATHER>(a, item);
+    while (g0 >= at + t * mult && item + 1 < items) {
+      at += t * mult;
+      t = ka_item_tiles<GATHER>(a, ++item);
+    }
+    cur.row = (int)(item * mult + (g0 - at) / t);
+    cur.a0 = (int)((g0 - at) % t);
+    cur.left = (int)(g1 - g0);
+    cur.load(a);
+  }
+  KaSeg<GATHER> it = cur;  // runs ahead of cur
   bool more = true;
+  int itile = it.a0;
   KaSrc<GATHER> src;
-  int itile = it.a0 + warp;
   src.set(a, it.row, it.r, itile, lane);
   const uint32_t ring = smem_addr(smem) + warp * kKaRing;
-  // past the segment: on to the next one that has a tile for this warp
-  auto settle = [&]() {
-    if (itile < it.a1) return;
-    do {
-      ahead = (ahead + it.a1 - it.a0) % kKaWarps;
-      more = it.next(a);
-      itile = it.a0 + deal(ahead);
-    } while (more && itile >= it.a1);
-    if (more) src.set(a, it.row, it.r, itile, lane);
-  };
-  settle();
   auto issue = [&](uint32_t stage) {
     if (more) {
       src.issue(a, stage, lane);
-      itile += kKaWarps;
-      if (itile < it.a1)
-        src.advance(kKaWarps, lane);
-      else
-        settle();
+      if (++itile < it.a1) {
+        src.advance(1, lane);
+      } else {
+        more = it.next(a);
+        itile = 0;
+        if (more) src.set(a, it.row, it.r, 0, lane);
+      }
     }
     ka_commit();
   };
 #pragma unroll
   for (int d = 0; d < kKaDepth - 1; ++d) issue(ring + d * kKaStage);
   uint32_t slot = ring, put = ring + (kKaDepth - 1) * kKaStage;
-  bool go = true;
-  while (go) {
-    KaQ Q;
+  do {
+    KaQ<G> Q;
     ka_load_q<G>(Q, a, cur.row, lane);
     KaState S;
     S.clear();
-    for (int t = cur.a0 + deal(dealt); t < cur.a1; t += kKaWarps) {
+    int left = cur.r.len - cur.a0 * kKaTile;
+    for (int t = cur.a0; t < cur.a1; ++t, left -= kKaTile) {
       issue(put);
       ka_wait<kKaDepth - 1>();
       __syncwarp();
-      ka_tile<G>(S, Q, slot, ka_valid<GATHER>(slot, cur.r.len - t * kKaTile), lane);
+      ka_tile<G>(S, Q, slot, ka_valid<GATHER>(slot, left), lane);
       __syncwarp();
       put = slot;
       slot = slot == ring + (kKaDepth - 1) * kKaStage ? ring : slot + kKaStage;
     }
-    ka_flush<G>(S, so + warp * G * kD, sml + warp * G, lane);
-    __syncthreads();
-    const int b = (int)(cur.row / a.Hkv);
-    const int64_t bq = (int64_t)b * a.Hq + (cur.row % a.Hkv) * G;
     const bool whole = cur.a0 == 0 && cur.a1 == cur.tiles;
-    const int64_t mypart = 2 * cta + (cur.a0 == 0 ? 1 : 0);
-    for (int e = threadIdx.x; e < G * kD; e += kKaThreads) {
-      const int g = e / kD;
-      float top = kKaEmpty, l = 0.0f, o = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kKaWarps; ++w) top = fmaxf(top, sml[w * G + g].x);
-#pragma unroll
-      for (int w = 0; w < kKaWarps; ++w) {
-        const float f = ka_weight(sml[w * G + g], top);
-        l = fmaf(sml[w * G + g].y, f, l);
-        o = fmaf(so[w * G * kD + e], f, o);
-      }
-      if (whole) {
-        ka_write(a, bq + g, e % kD, o, top, l);
-      } else {
-        a.part_o[mypart * G * kD + e] = o;
-        if (e % kD == 0) a.part_ml[mypart * G + g] = make_float2(top, l);
-      }
+    if (cur.a0 == 0 && lane == 0) {
+      const int64_t last = ((g1 - cur.left + cur.tiles) * N - 1) / total;
+      a.meta[cur.row] = make_int2((int)gw, whole ? 0 : (int)(last - gw) + 1);
     }
-    if (!whole) {
-      // the row's first tile in the grid's order, hence the CTAs that hold its tiles
-      const int64_t gr = g1 - cur.left - cur.a0;
-      const int64_t ca = ((gr + 1) * N - 1) / total, cz = ((gr + cur.tiles) * N - 1) / total;
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0)
-        s_last = atomicAdd(a.ticket + cur.row, 1u) == (uint32_t)(cz - ca);
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        const int np = (int)(cz - ca) + 1;  // partial 1 of CTA ca, 0 of the ones after it
-        auto at = [&](int i) { return 2 * (ca + i) + (i == 0 ? 1 : 0); };
-        // the weights of all partials, where the states were
-        static_assert(kKaMaxCtas <= kKaWarps * kD / 2, "the states' space holds the weights");
-        float2* w = reinterpret_cast<float2*>(so);
-        for (int i = threadIdx.x; i < np * G; i += kKaThreads)
-          w[i] = __ldcg(a.part_ml + at(i / G) * G + i % G);
-        __syncthreads();
-        for (int e4 = threadIdx.x; e4 < G * kD / 4; e4 += kKaThreads) {
-          const int g = e4 / (kD / 4), j = 4 * (e4 % (kD / 4));
-          float top = kKaEmpty, l = 0.0f;
-          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int i = 0; i < np; ++i) top = fmaxf(top, w[i * G + g].x);
-#pragma unroll 8
-          for (int i = 0; i < np; ++i) {
-            const float4 v =
-                __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * G * kD) + e4);
-            const float f = ka_weight(w[i * G + g], top);
-            l = fmaf(w[i * G + g].y, f, l);
-            o.x = fmaf(v.x, f, o.x);
-            o.y = fmaf(v.y, f, o.y);
-            o.z = fmaf(v.z, f, o.z);
-            o.w = fmaf(v.w, f, o.w);
-          }
-          ka_write(a, bq + g, j, o.x, top, l);
-          ka_write(a, bq + g, j + 1, o.y, top, l);
-          ka_write(a, bq + g, j + 2, o.z, top, l);
-          ka_write(a, bq + g, j + 3, o.w, top, l);
-        }
-      }
+    if (whole) {
+      const int64_t bq = (int64_t)(cur.row / a.Hkv) * a.Hq + (cur.row % a.Hkv) * G;
+      ka_flush<G, true>(S, a.out + bq * kD, nullptr, a.lse ? a.lse + bq : nullptr, lane);
+    } else {  // partial 1 of the row's first warp, 0 of the others
+      const int64_t p = (2 * gw + (cur.a0 == 0 ? 1 : 0)) * G;
+      ka_flush<G, false>(S, a.part_o + p * kD, a.part_ml + p, nullptr, lane);
     }
-    dealt = (dealt + cur.a1 - cur.a0) % kKaWarps;
-    go = cur.next(a);
-    __syncthreads();  // the states have been read
-  }
+  } while (cur.next(a));
   ka_wait<0>();
+}
+
+// Joins the partials of the rows that were cut: a CTA per head of a row, each warp every
+// eighth partial.
+template <int G>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const KaArgs a) {
+  __shared__ float4 so[8][32];
+  __shared__ float2 sml[8];
+  const int g = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const int2 mt = a.meta[row];
+    if (mt.y == 0) continue;  // uniform over the CTA
+    auto at = [&](int i) { return (2 * ((int64_t)mt.x + i) + (i == 0 ? 1 : 0)) * G + g; };
+    float top = kKaEmpty, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = warp; i0 < mt.y; i0 += 64) {  // eight partials in flight
+      float2 ml[8];
+      float4 v[8];
+      float t8 = top;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + 8 * k;
+        ml[k] = i < mt.y ? a.part_ml[at(i)] : make_float2(kKaEmpty, 0.0f);
+        v[k] = i < mt.y ? reinterpret_cast<const float4*>(a.part_o + at(i) * kD)[lane]
+                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        t8 = fmaxf(t8, ml[k].x);
+      }
+      const float f0 = exp2f(top - t8);
+      top = t8;
+      l *= f0;
+      o.x *= f0;
+      o.y *= f0;
+      o.z *= f0;
+      o.w *= f0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float f = ka_weight(ml[k], top);
+        l = fmaf(ml[k].y, f, l);
+        o.x = fmaf(v[k].x, f, o.x);
+        o.y = fmaf(v[k].y, f, o.y);
+        o.z = fmaf(v[k].z, f, o.z);
+        o.w = fmaf(v[k].w, f, o.w);
+      }
+    }
+    so[warp][lane] = o;
+    if (lane == 0) sml[warp] = make_float2(top, l);
+    __syncthreads();
+    if (threadIdx.x < kD) {
+      const int j = threadIdx.x;
+      float tt = kKaEmpty, ll = 0.0f, oo = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) tt = fmaxf(tt, sml[w].x);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float f = ka_weight(sml[w], tt);
+        ll = fmaf(sml[w].y, f, ll);
+        oo = fmaf(reinterpret_cast<const float*>(so[w])[j], f, oo);
+      }
+      ka_write(a, (int64_t)(row / a.Hkv) * a.Hq + (row % a.Hkv) * G + g, j, oo, tt, ll);
+    }
+    __syncthreads();
+  }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -901,16 +951,15 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 template <int G, bool GATHER>
 int ka_launch(const KaArgs& a, int64_t most, cudaStream_t st) {
   const int64_t tiles = (most + kKaTile - 1) / kKaTile;
-  const bool bal = a.rows * tiles >= 1 << 14;
+  const bool bal = a.rows * tiles >= 1 << 13;
   if (bal) {
-    const size_t bytes = (size_t)kKaWarps * (kKaRing + G * (kD * 4 + 8));
-    auto kern = kv4_balanced_kernel<G, GATHER>;
+    const size_t bytes = (size_t)kKaWarps * kKaRing;
+    auto kern = kv4_stream_kernel<G, GATHER>;
     if (int rc = set_smem_limit((const void*)kern, bytes, "kv4 attend")) return rc;
-    if (cudaMemsetAsync(a.ticket, 0, sizeof(uint32_t) * a.rows, st) != cudaSuccess)
-      return check_launch("kv4 attend: ticket clear");
-    const int grid = (int)imin64(2 * device_sm_count(), kKaMaxCtas);
+    const int grid = (int)imin64(2 * device_sm_count(), kKaMaxWarps / kKaWarps);
     kern<<<grid, kKaThreads, bytes, st>>>(a);
-    note_launches(1);
+    kv4_join_kernel<G><<<dim3((unsigned)imin64(a.rows, 2 * device_sm_count()), G), 256, 0, st>>>(a);
+    note_launches(2);
     return check_launch("kv4 attend");
   }
   int cs = 1;
@@ -943,8 +992,8 @@ int ka_pick(const KaArgs& a, int64_t most, cudaStream_t st) {
 }  // namespace
 
 size_t kv4_attend_workspace_bytes(const Dims& s, int64_t) {
-  return align256(sizeof(uint32_t) * s.B * s.Hkv) +
-         (size_t)2 * kKaMaxCtas * s.G * (sizeof(float) * kD + sizeof(float2));
+  return align256(sizeof(int2) * s.B * s.Hkv) +
+         (size_t)2 * kKaMaxWarps * s.G * (sizeof(float) * kD + sizeof(float2));
 }
 
 int launch_kv4_attend(const Dims& s, const uint16_t* q, const sd_kv4& c, const int32_t* idx,
@@ -969,10 +1018,10 @@ int launch_kv4_attend(const Dims& s, const uint16_t* q, const sd_kv4& c, const i
   a.out = out;
   a.lse = lse;
   uint8_t* p = (uint8_t*)ws;
-  a.ticket = (uint32_t*)p;
-  p += align256(sizeof(uint32_t) * a.rows);
+  a.meta = (int2*)p;
+  p += align256(sizeof(int2) * a.rows);
   a.part_o = (float*)p;
-  a.part_ml = (float2*)(p + sizeof(float) * 2 * kKaMaxCtas * s.G * kD);
+  a.part_ml = (float2*)(p + sizeof(float) * 2 * kKaMaxWarps * s.G * kD);
   const int64_t most = idx ? max_count : s.n;
   switch (s.G) {
     case 1: return ka_pick<1>(a, most, st);
