@@ -38,107 +38,125 @@ __device__ __forceinline__ void kv_range(const KvMoveArgs& a, int b, int64_t& le
   p0 = a.first + (a.pos ? a.pos[b] : 0);
 }
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// Of both bf16 halves; a NaN stays.
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
-// What a lane moves: its half (0: K, 1: V), octet and row, and the tokens' range.
+// What a lane moves: its half (0: K, 1: V), octet and row, and the tokens [t0, t1) of the
+// row that have a place in the cache.
 struct KvLane {
-  int half, l;
-  int64_t row, t, len, p0, x;  // x: offset of the lane's octet of token 0 in the caller's array
+  int half, l, t, t0, t1;
+  int64_t row, tok;  // tok: token 0's place among the cache's tokens
+  int64_t x;         // offset of token 0's octet in the caller's array
   __device__ __forceinline__ KvLane(const KvMoveArgs& a) {
     const int lane = threadIdx.x & 31;
     half = lane >> 4;
     l = lane & 15;
     row = blockIdx.y;
     const int b = (int)(row / a.hkv), h = (int)(row % a.hkv);
+    int64_t len, p0;
     kv_range(a, b, len, p0);
-    t = (int64_t)blockIdx.x * kKvStep + (threadIdx.x >> 5) * kKvRun;
-    // tokens [t, len) whose positions lie in the cache, of a half that is asked for
-    len = a.x[half] ? imin64(len, a.n - p0) : 0;
+    t = blockIdx.x * kKvStep + (threadIdx.x >> 5) * kKvRun;
+    t0 = (int)imin64(imax64(0, -p0), a.m);
+    t1 = (int)imax64(t0, imin64(len, a.n - p0));
+    tok = row * a.ncap + p0;
     x = b * a.sb[half] + h * a.sh[half] + 8 * l;
   }
-  __device__ __forceinline__ bool in(int64_t i) const { return i < len && p0 + i >= 0; }
+  __device__ __forceinline__ bool in(int i) const {
+    return (unsigned)(i - t0) < (unsigned)(t1 - t0);
+  }
 };
 
 __global__ void __launch_bounds__(32 * kKvWarps) kv4_write_kernel(const KvMoveArgs a) {
-  KvLane L(a);
-  const uint16_t* src = a.x[L.half] + L.x;
-  const int64_t base = L.row * a.ncap + L.p0, st = a.st[L.half];
-  uint32_t* code = reinterpret_cast<uint32_t*>(a.code[L.half]) + 2 * (L.l & 7) + (L.l >> 3);
-  uint32_t* scale = reinterpret_cast<uint32_t*>(a.scale) + 2 * L.half + (L.l >> 3);
+  const KvLane L(a);
+  const bool asked = a.x[L.half] != nullptr;
+  const int64_t st = a.st[L.half];
+  const uint16_t* src = a.x[L.half] + L.x + L.t * st;
+  uint32_t* code = reinterpret_cast<uint32_t*>(a.code[L.half] + (L.tok + L.t) * kKv4Row) +
+                   2 * (L.l & 7) + (L.l >> 3);
+  uint32_t* scale = reinterpret_cast<uint32_t*>(a.scale + (L.tok + L.t) * kKv4Scales) +
+                    2 * L.half + (L.l >> 3);
   uint4 next[kKvRun];
-  auto fetch = [&](int64_t t) {
+  auto fetch = [&](int t) {
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k)
-      next[k] = L.in(t + k) ? __ldcs(reinterpret_cast<const uint4*>(src + (t + k) * st))
-                            : make_uint4(0u, 0u, 0u, 0u);
+      next[k] = asked && L.in(t + k) ? __ldcs(reinterpret_cast<const uint4*>(src + k * st))
+                                     : make_uint4(0u, 0u, 0u, 0u);
   };
-  const int64_t step = (int64_t)gridDim.x * kKvStep;
-  const int64_t most = a.length ? imin64(a.m, a.length[L.row / a.hkv]) : a.m;  // both halves'
+  const int step = gridDim.x * kKvStep;
   fetch(L.t);
-  for (int64_t t = L.t; t < most; t += step) {
+  for (int t = L.t; t < L.t1; t += step) {  // the same for both halves
     uint4 cur[kKvRun];
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k) cur[k] = next[k];
-    fetch(t + step);
+    src += step * st;
+    if (t < L.t1 - step) fetch(t + step);
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k) {
       const uint4 w = cur[k];
-      float lo = min_nan(min_nan(min_nan(bf16_lo(w.x), bf16_hi(w.x)), min_nan(bf16_lo(w.y), bf16_hi(w.y))),
-                         min_nan(min_nan(bf16_lo(w.z), bf16_hi(w.z)), min_nan(bf16_lo(w.w), bf16_hi(w.w))));
-      float hi = fmax_nan(fmax_nan(fmax_nan(bf16_lo(w.x), bf16_hi(w.x)), fmax_nan(bf16_lo(w.y), bf16_hi(w.y))),
-                          fmax_nan(fmax_nan(bf16_lo(w.z), bf16_hi(w.z)), fmax_nan(bf16_lo(w.w), bf16_hi(w.w))));
+      // (min, -max) in the halves of one word, then over the group's eight lanes
+      const uint32_t mn = min2_nan(min2_nan(w.x, w.y), min2_nan(w.z, w.w));
+      const uint32_t mx = max2_nan(max2_nan(w.x, w.y), max2_nan(w.z, w.w)) ^ 0x80008000u;
+      uint32_t r = min2_nan(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-        hi = fmax_nan(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-      }
-      const float s = kv4_step(lo, hi);
-      uint32_t sm = (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
-      uint32_t word = kv4_word(w, lo, s, s > 0.0f ? __frcp_rn(s) : 0.0f);
+      for (int o = 4; o > 0; o >>= 1) r = min2_nan(r, __shfl_xor_sync(0xFFFFFFFFu, r, o));
+      const float lo = bf16_lo(r), s = kv4_step(lo, -bf16_hi(r));
+      uint32_t sm = __byte_perm(__float_as_uint(s), r, 0x5432);
+      uint32_t word = kv4_word(w, lo, s, s > 0.0f ? kv4_rcp(s) : 0.0f);
       if (s != s) {  // a value that is not finite: the group reads as NaN
         sm = kKv4NanPair;
         word = 0;
       }
-      if (L.in(t + k)) {
-        const int64_t tok = base + t + k;
-        code[tok * (kKv4Row / 4)] = word;
-        if ((L.l & 7) == 0) scale[tok * (kKv4Scales / 2)] = sm;
+      if (asked && L.in(t + k)) {
+        code[k * (kKv4Row / 4)] = word;
+        if ((L.l & 7) == 0) scale[k * (kKv4Scales / 2)] = sm;
       }
     }
+    code += (int64_t)step * (kKv4Row / 4);
+    scale += (int64_t)step * (kKv4Scales / 2);
   }
 }
 
 __global__ void __launch_bounds__(32 * kKvWarps) kv4_read_kernel(const KvMoveArgs a) {
-  KvLane L(a);
-  uint16_t* dst = a.x[L.half] + L.x;
-  const int64_t base = L.row * a.ncap + L.p0, st = a.st[L.half];
+  const KvLane L(a);
+  const int64_t st = a.st[L.half];
+  uint16_t* dst = a.x[L.half] + L.x + L.t * st;
   const uint32_t* code =
-      reinterpret_cast<const uint32_t*>(a.code[L.half]) + 2 * (L.l & 7) + (L.l >> 3);
-  const uint32_t* scale = reinterpret_cast<const uint32_t*>(a.scale) + 2 * L.half + (L.l >> 3);
+      reinterpret_cast<const uint32_t*>(a.code[L.half] + (L.tok + L.t) * kKv4Row) +
+      2 * (L.l & 7) + (L.l >> 3);
+  const uint32_t* scale =
+      reinterpret_cast<const uint32_t*>(a.scale + (L.tok + L.t) * kKv4Scales) + 2 * L.half +
+      (L.l >> 3);
+  if (!a.x[L.half]) return;  // whole half-warps, which work alone
   uint32_t nw[kKvRun], ns[kKvRun];
-  auto fetch = [&](int64_t t) {
+  auto fetch = [&](int t) {
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k) {
       const bool ok = L.in(t + k);
-      const int64_t tok = base + t + k;
-      nw[k] = ok ? __ldcs(code + tok * (kKv4Row / 4)) : 0u;
-      ns[k] = ok ? __ldcs(scale + tok * (kKv4Scales / 2)) : 0u;
+      nw[k] = ok ? __ldcs(code + k * (kKv4Row / 4)) : 0u;
+      ns[k] = ok ? __ldcs(scale + k * (kKv4Scales / 2)) : 0u;
     }
   };
-  const int64_t step = (int64_t)gridDim.x * kKvStep;
+  const int step = gridDim.x * kKvStep;
   fetch(L.t);
-  for (int64_t t = L.t; t < L.len; t += step) {
+  for (int t = L.t; t < L.t1; t += step) {
     uint32_t cw[kKvRun], cs[kKvRun];
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k) {
       cw[k] = nw[k];
       cs[k] = ns[k];
     }
-    fetch(t + step);
+    code += (int64_t)step * (kKv4Row / 4);
+    scale += (int64_t)step * (kKv4Scales / 2);
+    if (t < L.t1 - step) fetch(t + step);
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k) {
       if (!L.in(t + k)) continue;
@@ -148,8 +166,9 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv4_read_kernel(const KvMoveArg
       o.y = kv4_pair(cw[k], 8, s, m);
       o.z = kv4_pair(cw[k], 16, s, m);
       o.w = kv4_pair(cw[k], 24, s, m);
-      *reinterpret_cast<uint4*>(dst + (t + k) * st) = o;
+      *reinterpret_cast<uint4*>(dst + k * st) = o;
     }
+    dst += step * st;
   }
 }
 

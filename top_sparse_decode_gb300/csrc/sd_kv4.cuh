@@ -58,22 +58,30 @@ __device__ __forceinline__ float kv4_step(float lo, float hi) {
   return s < 7.8886091e-31f ? 0.0f : s;
 }
 
+// 1 / s correctly rounded, for a normal s of eight significant bits: the hardware's
+// approximation and one Newton step (equal to the IEEE reciprocal for every such s).
+__device__ __forceinline__ float kv4_rcp(float s) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(s));
+  return fmaf(fmaf(-s, y, 1.0f), y, y);
+}
+
 // A word of codes from the octet x: clamp(rint((x - lo) / s), 0, 15) at bits 4 i; y = 1 / s
 // correctly rounded, or 0 for s = 0 (codes 0).
 __device__ __forceinline__ uint32_t kv4_word(const uint4& x, float lo, float s, float y) {
   const uint64_t l2 = f2_make(-lo, -lo), s2 = f2_make(-s, -s), y2 = f2_make(y, y);
-  // adding 1.5 2^23 rounds to a whole number (ties to even) in the low mantissa bits
-  constexpr float kMagic = 12582912.0f;
+  // adding 1.5 2^23 rounds to a whole number (ties to even): the bits 0x4B400000 + c
+  const uint64_t magic = f2_make(12582912.0f, 12582912.0f);
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t word = 0;
 #pragma unroll
   for (int i = 3; i >= 0; --i) {
     float q0, q1;
     f2_split(kv4_divide2(f2_add(f2_make(bf16_lo(w[i]), bf16_hi(w[i])), l2), s2, y2), q0, q1);
-    word = word * 16u + (__float_as_uint(fminf(q1, 15.0f) + kMagic) - 0x4B400000u);
-    word = word * 16u + (__float_as_uint(fminf(q0, 15.0f) + kMagic) - 0x4B400000u);
+    f2_split(f2_add(f2_make(fminf(q0, 15.0f), fminf(q1, 15.0f)), magic), q0, q1);
+    word = (word * 16u + __float_as_uint(q1)) * 16u + __float_as_uint(q0);
   }
-  return word;
+  return word - 0x4B400000u * 0x11111111u;  // modulo 2^32
 }
 
 // Two channels of a word of codes (from bit sh) as packed bf16.

@@ -37,9 +37,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kKaTile = 32;    // tokens per tile
-constexpr int kKaWarps = 6;    // warps per CTA
+constexpr int kKaWarps = 4;    // warps per CTA
 constexpr int kKaThreads = 32 * kKaWarps;
-constexpr int kKaDepth = 3;    // tiles in a warp's ring
+constexpr int kKaDepth = 4;    // tiles in a warp's ring
 constexpr int kKaOffV = kKaTile * kKv4Row, kKaOffS = 2 * kKaOffV;
 constexpr int kKaOffMask = kKaOffS + kKaTile * 2 * kKv4Scales;
 constexpr int kKaStage = kKaOffMask + 16;
@@ -412,26 +412,32 @@ __device__ __forceinline__ uint32_t ka_pack(float lo, float hi) {
   return d;
 }
 
-// One tile, as two 16-token halves; valid: its tokens.  Row r of a half's score tile is
-// token tau(r) (r < 8: r / 2, odd rows 4 + (r / 2 ^ 1)) or tau(r - 8) + 8: with the
-// swizzle, any eight lanes of a K read and any sixteen of a V read touch each bank once.
+// A tile is worked on as two 16-token halves, in three parts: the scores S = K q^T, the
+// weights, and the values O^T += V^T P^T.  Row r of a half's score tile is token tau(r)
+// (r < 8: r / 2, odd rows 4 + (r / 2 ^ 1)) or tau(r - 8) + 8: with the swizzle, any eight
+// lanes of a K read and any sixteen of a V read touch each bank once.
 // G = 8: a lane has the logits of two heads and four tokens.  G <= 4: the first half's
 // heads are columns 0..3 and the second's 4..7 (q's other columns are zero), so that a
 // lane has two heads and the two tokens of its half, and no logit is computed twice.
 template <int G>
-__device__ __forceinline__ void ka_tile(KaState& S, const KaQ<G>& Q, uint32_t st, uint32_t valid,
-                                        int lane) {
-  constexpr int NR = G == 8 ? 4 : 2;  // this lane's tokens
+struct KaScores {
+  float c[G == 8 ? 2 : 1][2][4];  // [half][group]
+};
+
+__device__ __forceinline__ int ka_tau(int gid) {
+  return (gid & 1) ? 4 + (gid >> 1 ^ 1) : gid >> 1;
+}
+
+template <int G>
+__device__ __forceinline__ void ka_scores(KaScores<G>& C, const KaQ<G>& Q, uint32_t st, int lane) {
   const int gid = lane >> 2, tig = lane & 3;
-  const int tk = (gid & 1) ? 4 + (gid >> 1 ^ 1) : gid >> 1;
-  const int side = G == 8 ? 0 : tig >> 1;  // G <= 4: the half of this lane's tokens
-  float acc[G == 8 ? 2 : 1][2][4];         // [half][group]
+  constexpr bool both = G != 8;
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
-    const uint32_t ak = st + (16 * hf + tk) * kKv4Row + ((tig ^ (gid >> 1 & 2)) * 16);
+    const uint32_t ak =
+        st + (16 * hf + ka_tau(gid)) * kKv4Row + ((tig ^ (gid >> 1 & 2)) * 16);
     const uint4 ka = lds128(ak), kb = lds128(ak + 8 * kKv4Row);
     const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-    constexpr bool both = G != 8;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -442,12 +448,30 @@ __device__ __forceinline__ void ka_tile(KaState& S, const KaQ<G>& Q, uint32_t st
           const uint32_t a0 = ka_code_lo(xa), a1 = ka_code_lo(xb);
           const uint32_t a2 = ka_code_hi(xa), a3 = ka_code_hi(xb);
           const uint32_t(&qb)[2] = Q.b[both ? hf : 0][g][2 * j + s];
+          float(&c)[4] = C.c[both ? 0 : hf][g];
           if (j + s == 0 && (!both || hf == 0))
-            mma_f16_zero(acc[both ? 0 : hf][g], a0, a1, a2, a3, qb[0], qb[1]);
+            mma_f16_zero(c, a0, a1, a2, a3, qb[0], qb[1]);
           else
-            mma_f16(acc[both ? 0 : hf][g], a0, a1, a2, a3, qb[0], qb[1]);
+            mma_f16(c, a0, a1, a2, a3, qb[0], qb[1]);
         }
   }
+}
+
+// P^T's high and low f16 parts, as B operands: G = 8 h and l; G <= 4 columns 0..3 of h the
+// high parts of its half's heads, 4..7 the low parts.
+struct KaP {
+  uint32_t h[2][2][2], l[2][2][2];  // [half][group][r]
+};
+
+// valid: the tile's tokens that count.
+template <int G>
+__device__ __forceinline__ void ka_weights(KaP& P, KaState& S, const KaScores<G>& C,
+                                           const KaQ<G>& Q, uint32_t st, uint32_t valid,
+                                           int lane) {
+  constexpr int NR = G == 8 ? 4 : 2;  // this lane's tokens
+  const int gid = lane >> 2, tig = lane & 3;
+  const int side = G == 8 ? 0 : tig >> 1;  // G <= 4: the half of this lane's tokens
+  const int tk = ka_tau(gid);
   float dot[NR][2], mk[NR][2], sv[NR][2], mv[NR][2];  // [token][column or group]
   auto token = [&](int i) { return (G == 8 ? 16 * (i >> 1) : 16 * side) + tk + 8 * (i & 1); };
 #pragma unroll
@@ -460,7 +484,7 @@ __device__ __forceinline__ void ka_tile(KaState& S, const KaQ<G>& Q, uint32_t st
     sv[i][1] = bf16_lo(sc.w);
     mv[i][0] = fmaf(7.5f, sv[i][0], bf16_hi(sc.z));  // the middle of the group's range
     mv[i][1] = fmaf(7.5f, sv[i][1], bf16_hi(sc.w));
-    const float(&ac)[2][4] = acc[i >> 1];
+    const float(&ac)[2][4] = C.c[i >> 1];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       dot[i][e] = fmaf(sk1, ac[1][2 * (i & 1) + e], sk0 * ac[0][2 * (i & 1) + e]);
@@ -527,9 +551,6 @@ __device__ __forceinline__ void ka_tile(KaState& S, const KaQ<G>& Q, uint32_t st
 #pragma unroll
       for (int i = 0; i < NR; ++i) S.mo[e][g] = fmaf(p[i][e], mv[i][g], S.mo[e][g]);
   }
-  // P^T's high and low f16 parts, as B operands: G = 8 bh and bl; G <= 4 columns 0..3 of bh
-  // the high parts of its half's heads, 4..7 the low parts
-  uint32_t bh[2][2][2], bl[2][2][2];  // [half][group][r]
 #pragma unroll
   for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -538,47 +559,62 @@ __device__ __forceinline__ void ka_tile(KaState& S, const KaQ<G>& Q, uint32_t st
       const uint32_t lo = ka_pack(fmaf(p[i][0], sv[i][g] * S.f[0][g], -h2.x),
                                   fmaf(p[i][1], sv[i][g] * S.f[1][g], -h2.y));
       if constexpr (G == 8) {
-        bh[i >> 1][g][i & 1] = transpose_8x8(hi[i][g]);
-        bl[i >> 1][g][i & 1] = transpose_8x8(lo);
+        P.h[i >> 1][g][i & 1] = transpose_8x8(hi[i][g]);
+        P.l[i >> 1][g][i & 1] = transpose_8x8(lo);
       } else {  // the first half's low parts move to the lanes of columns 4..7, the
                 // second's high parts to those of 0..3
         const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, side ? hi[i][g] : lo, 2);
-        bh[0][g][i] = transpose_8x8(side ? got : hi[i][g]);
-        bh[1][g][i] = transpose_8x8(side ? lo : got);
+        P.h[0][g][i] = transpose_8x8(side ? got : hi[i][g]);
+        P.h[1][g][i] = transpose_8x8(side ? lo : got);
       }
     }
-  // rows 2 tig, 2 tig + 1 (and + 8) of V's halves, 8 bytes from byte 8 gid: channels 8 gid ..
-  // + 7 of either group
-  uint2 v[2][4];
+}
+
+// V's codes as the MMAs' A operand before unpacking: rows 2 tig, 2 tig + 1 (and + 8) of either
+// half, 8 bytes from byte 8 gid (channels 8 gid .. + 7 of either group), the two tokens'
+// half-words paired.
+struct KaV {
+  uint32_t x[2][2][2][2];  // [half][group][low or high half-word][rows + 0 or 8]
+};
+
+__device__ __forceinline__ void ka_load_v(KaV& V, uint32_t st, int lane) {
+  const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
     const uint32_t av = st + kKaOffV + 16 * hf * kKv4Row + ((gid >> 1 ^ (tig & 2)) * 16) +
                         (gid & 1) * 8;
-    v[hf][0] = lds64(av + tig * kKv4Row);
-    v[hf][1] = lds64(av + (4 + (tig ^ 1)) * kKv4Row);
-    v[hf][2] = lds64(av + (tig + 8) * kKv4Row);
-    v[hf][3] = lds64(av + (12 + (tig ^ 1)) * kKv4Row);
+    const uint2 v0 = lds64(av + tig * kKv4Row), v1 = lds64(av + (4 + (tig ^ 1)) * kKv4Row);
+    const uint2 v2 = lds64(av + (tig + 8) * kKv4Row), v3 = lds64(av + (12 + (tig ^ 1)) * kKv4Row);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t sel = k ? 0x7632u : 0x5410u;
+      V.x[hf][0][k][0] = __byte_perm(v0.x, v1.x, sel);
+      V.x[hf][0][k][1] = __byte_perm(v2.x, v3.x, sel);
+      V.x[hf][1][k][0] = __byte_perm(v0.y, v1.y, sel);
+      V.x[hf][1][k][1] = __byte_perm(v2.y, v3.y, sel);
+    }
   }
+}
+
+template <int G>
+__device__ __forceinline__ void ka_values(KaState& S, const KaP& P, const KaV& V) {
 #pragma unroll
   for (int g = 0; g < 2; ++g)
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const uint32_t sel = u < 2 ? 0x5410u : 0x7632u;
       // the tensor cores add by truncation: a tile is summed from zero and added by
       // rounding, or the error would grow with the tokens
       float t[4];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const uint32_t w0 = g ? v[hf][0].y : v[hf][0].x, w1 = g ? v[hf][1].y : v[hf][1].x;
-        const uint32_t w2 = g ? v[hf][2].y : v[hf][2].x, w3 = g ? v[hf][3].y : v[hf][3].x;
-        const uint32_t x = __byte_perm(w0, w1, sel) >> (8 * (u & 1));
-        const uint32_t y = __byte_perm(w2, w3, sel) >> (8 * (u & 1));
+        const uint32_t x = V.x[hf][g][u >> 1][0] >> (8 * (u & 1));
+        const uint32_t y = V.x[hf][g][u >> 1][1] >> (8 * (u & 1));
         const uint32_t a0 = ka_mid_lo(x), a1 = ka_mid_hi(x), a2 = ka_mid_lo(y), a3 = ka_mid_hi(y);
         if (hf == 0)
-          mma_f16_zero(t, a0, a1, a2, a3, bh[hf][g][0], bh[hf][g][1]);
+          mma_f16_zero(t, a0, a1, a2, a3, P.h[hf][g][0], P.h[hf][g][1]);
         else
-          mma_f16(t, a0, a1, a2, a3, bh[hf][g][0], bh[hf][g][1]);
-        if (G == 8) mma_f16(t, a0, a1, a2, a3, bl[hf][g][0], bl[hf][g][1]);
+          mma_f16(t, a0, a1, a2, a3, P.h[hf][g][0], P.h[hf][g][1]);
+        if (G == 8) mma_f16(t, a0, a1, a2, a3, P.l[hf][g][0], P.l[hf][g][1]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) S.o[4 * g + u][i] += t[i];
@@ -590,6 +626,29 @@ template <bool GATHER>
 __device__ __forceinline__ uint32_t ka_valid(uint32_t stage, int left) {
   if (GATHER) return lds32(stage + kKaOffMask);
   return left >= kKaTile ? 0xFFFFFFFFu : (1u << left) - 1u;
+}
+
+// The tiles of a row (or a part of one), `tiles` of them, the first in stage `slot`:
+// `issue` requests one more tile into the stage it is given and commits.
+template <int G, bool GATHER, class Issue>
+__device__ __forceinline__ void ka_tiles(KaState& S, const KaQ<G>& Q, uint32_t ring, uint32_t& slot,
+                                         uint32_t& put, int tiles, int left, int step, Issue issue,
+                                         int lane) {
+  for (; tiles > 0; --tiles, left -= step) {
+    issue(put);
+    ka_wait<kKaDepth - 1>();
+    __syncwarp();
+    KaScores<G> C;
+    ka_scores<G>(C, Q, slot, lane);
+    KaV V;  // requested here, where the chain of the weights leaves the time
+    ka_load_v(V, slot, lane);
+    KaP P;
+    ka_weights<G>(P, S, C, Q, slot, ka_valid<GATHER>(slot, left), lane);
+    ka_values<G>(S, P, V);
+    __syncwarp();
+    put = slot;
+    slot = slot == ring + (kKaDepth - 1) * kKaStage ? ring : slot + kKaStage;
+  }
 }
 
 // The state of a warp in natural units, written to so [G][kD] and sml [G] = (m, l); with
@@ -680,19 +739,18 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs
   KaState S;
   S.clear();
   uint32_t slot = ring, put = ring + (kKaDepth - 1) * kKaStage;
-  for (int left = r.len - first * kKaTile; left > 0; left -= step * kKaTile) {
-    if (src.left > 0) {
-      src.issue(a, put, lane);
-      src.advance(step, lane);
-    }
-    ka_commit();
-    ka_wait<kKaDepth - 1>();
-    __syncwarp();
-    ka_tile<G>(S, Q, slot, ka_valid<GATHER>(slot, left), lane);
-    __syncwarp();
-    put = slot;
-    slot = slot == ring + (kKaDepth - 1) * kKaStage ? ring : slot + kKaStage;
-  }
+  const int tiles = (r.len + kKaTile - 1) / kKaTile;
+  ka_tiles<G, GATHER>(
+      S, Q, ring, slot, put, (tiles - first + step - 1) / step, r.len - first * kKaTile,
+      step * kKaTile,
+      [&](uint32_t stage) {
+        if (src.left > 0) {
+          src.issue(a, stage, lane);
+          src.advance(step, lane);
+        }
+        ka_commit();
+      },
+      lane);
   ka_wait<0>();
   __syncthreads();  // the rings become the warps' states
   float* so = reinterpret_cast<float*>(smem);             // [warps][G][kD]
@@ -831,6 +889,7 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_stream_kernel(const KaArgs 
     cur.left = (int)(g1 - g0);
     cur.load(a);
   }
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   KaSeg<GATHER> it = cur;  // runs ahead of cur
   bool more = true;
   int itile = it.a0;
@@ -858,16 +917,8 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_stream_kernel(const KaArgs 
     ka_load_q<G>(Q, a, cur.row, lane);
     KaState S;
     S.clear();
-    int left = cur.r.len - cur.a0 * kKaTile;
-    for (int t = cur.a0; t < cur.a1; ++t, left -= kKaTile) {
-      issue(put);
-      ka_wait<kKaDepth - 1>();
-      __syncwarp();
-      ka_tile<G>(S, Q, slot, ka_valid<GATHER>(slot, left), lane);
-      __syncwarp();
-      put = slot;
-      slot = slot == ring + (kKaDepth - 1) * kKaStage ? ring : slot + kKaStage;
-    }
+    ka_tiles<G, GATHER>(S, Q, ring, slot, put, cur.a1 - cur.a0, cur.r.len - cur.a0 * kKaTile,
+                        kKaTile, issue, lane);
     const bool whole = cur.a0 == 0 && cur.a1 == cur.tiles;
     if (cur.a0 == 0 && lane == 0) {
       const int64_t last = ((g1 - cur.left + cur.tiles) * N - 1) / total;
@@ -884,65 +935,102 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_stream_kernel(const KaArgs 
   ka_wait<0>();
 }
 
-// Joins the partials of the rows that were cut: a CTA per head of a row, each warp every
-// eighth partial.
+// Partials i0, i0 + step, .. of the np of one head of a row whose first warp is `first`:
+// their sum over the lanes' four channels each, and (m, l).
 template <int G>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const KaArgs a) {
-  __shared__ float4 so[8][32];
-  __shared__ float2 sml[8];
-  const int g = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const int2 mt = a.meta[row];
-    if (mt.y == 0) continue;  // uniform over the CTA
-    auto at = [&](int i) { return (2 * ((int64_t)mt.x + i) + (i == 0 ? 1 : 0)) * G + g; };
-    float top = kKaEmpty, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = warp; i0 < mt.y; i0 += 64) {  // eight partials in flight
-      float2 ml[8];
-      float4 v[8];
-      float t8 = top;
+__device__ __forceinline__ float4 ka_gather_parts(const KaArgs& a, int first, int np, int g, int i0,
+                                                  int step, int lane, float& top, float& l) {
+  auto at = [&](int i) { return (2 * ((int64_t)first + i) + (i == 0 ? 1 : 0)) * G + g; };
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  top = kKaEmpty;
+  l = 0.0f;
+  for (; i0 < np; i0 += 8 * step) {  // eight partials in flight
+    float2 ml[8];
+    float4 v[8];
+    float t8 = top;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int i = i0 + 8 * k;
-        ml[k] = i < mt.y ? a.part_ml[at(i)] : make_float2(kKaEmpty, 0.0f);
-        v[k] = i < mt.y ? reinterpret_cast<const float4*>(a.part_o + at(i) * kD)[lane]
-                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        t8 = fmaxf(t8, ml[k].x);
-      }
-      const float f0 = exp2f(top - t8);
-      top = t8;
-      l *= f0;
-      o.x *= f0;
-      o.y *= f0;
-      o.z *= f0;
-      o.w *= f0;
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + step * k;
+      ml[k] = i < np ? a.part_ml[at(i)] : make_float2(kKaEmpty, 0.0f);
+      v[k] = i < np ? reinterpret_cast<const float4*>(a.part_o + at(i) * kD)[lane]
+                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      t8 = fmaxf(t8, ml[k].x);
+    }
+    const float f0 = exp2f(top - t8);
+    top = t8;
+    l *= f0;
+    o.x *= f0;
+    o.y *= f0;
+    o.z *= f0;
+    o.w *= f0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float f = ka_weight(ml[k], top);
-        l = fmaf(ml[k].y, f, l);
-        o.x = fmaf(v[k].x, f, o.x);
-        o.y = fmaf(v[k].y, f, o.y);
-        o.z = fmaf(v[k].z, f, o.z);
-        o.w = fmaf(v[k].w, f, o.w);
+    for (int k = 0; k < 8; ++k) {
+      const float f = ka_weight(ml[k], top);
+      l = fmaf(ml[k].y, f, l);
+      o.x = fmaf(v[k].x, f, o.x);
+      o.y = fmaf(v[k].y, f, o.y);
+      o.z = fmaf(v[k].z, f, o.z);
+      o.w = fmaf(v[k].w, f, o.w);
+    }
+  }
+  return o;
+}
+
+// Joins the partials of the rows that were cut.  A CTA takes `run` heads of rows at a time,
+// a warp each; those of more than kKaAlone partials are summed by all its warps.
+constexpr int kKaJoinWarps = 8;
+constexpr int kKaAlone = 16;
+
+template <int G>
+__global__ void __launch_bounds__(32 * kKaJoinWarps) kv4_join_kernel(const KaArgs a, int run) {
+  __shared__ float4 so[kKaJoinWarps][32];
+  __shared__ float2 sml[kKaJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // for the end of the streaming kernel
+  const int64_t pairs = a.rows * G;
+  for (int64_t base = (int64_t)blockIdx.x * run; base < pairs; base += (int64_t)gridDim.x * run) {
+    const int64_t mine = base + warp;
+    bool wide = false;
+    if (warp < run && mine < pairs) {
+      const int64_t row = mine / G;
+      const int g = (int)(mine % G);
+      const int2 mt = a.meta[row];
+      wide = mt.y > kKaAlone;
+      if (mt.y > 0 && !wide) {
+        float top, l;
+        const float4 o = ka_gather_parts<G>(a, mt.x, mt.y, g, 0, 1, lane, top, l);
+        const int64_t bq = (row / a.Hkv) * a.Hq + (row % a.Hkv) * G + g;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        reinterpret_cast<float4*>(a.out + bq * kD)[lane] =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (a.lse && lane == 0) a.lse[bq] = l != 0.0f ? (top + log2f(l)) * kKaLn2 : -INFINITY;
       }
     }
-    so[warp][lane] = o;
-    if (lane == 0) sml[warp] = make_float2(top, l);
-    __syncthreads();
-    if (threadIdx.x < kD) {
-      const int j = threadIdx.x;
-      float tt = kKaEmpty, ll = 0.0f, oo = 0.0f;
+    if (!__syncthreads_or(wide)) continue;
+    for (int k = 0; k < run && base + k < pairs; ++k) {
+      const int64_t row = (base + k) / G;
+      const int g = (int)((base + k) % G);
+      const int2 mt = a.meta[row];
+      if (mt.y <= kKaAlone) continue;  // uniform over the CTA
+      float top, l;
+      so[warp][lane] = ka_gather_parts<G>(a, mt.x, mt.y, g, warp, kKaJoinWarps, lane, top, l);
+      if (lane == 0) sml[warp] = make_float2(top, l);
+      __syncthreads();
+      if (threadIdx.x < kD) {
+        const int j = threadIdx.x;
+        float tt = kKaEmpty, ll = 0.0f, oo = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) tt = fmaxf(tt, sml[w].x);
+        for (int w = 0; w < kKaJoinWarps; ++w) tt = fmaxf(tt, sml[w].x);
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const float f = ka_weight(sml[w], tt);
-        ll = fmaf(sml[w].y, f, ll);
-        oo = fmaf(reinterpret_cast<const float*>(so[w])[j], f, oo);
+        for (int w = 0; w < kKaJoinWarps; ++w) {
+          const float f = ka_weight(sml[w], tt);
+          ll = fmaf(sml[w].y, f, ll);
+          oo = fmaf(reinterpret_cast<const float*>(so[w])[j], f, oo);
+        }
+        ka_write(a, (row / a.Hkv) * a.Hq + (row % a.Hkv) * G + g, j, oo, tt, ll);
       }
-      ka_write(a, (int64_t)(row / a.Hkv) * a.Hq + (row % a.Hkv) * G + g, j, oo, tt, ll);
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -951,19 +1039,45 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 template <int G, bool GATHER>
 int ka_launch(const KaArgs& a, int64_t most, cudaStream_t st) {
   const int64_t tiles = (most + kKaTile - 1) / kKaTile;
-  const bool bal = a.rows * tiles >= 1 << 13;
+  bool bal = true;
+  int cs = 1;
+  {
+    const int64_t slots = 2 * device_sm_count(), W = slots * kKaWarps;
+    int64_t best = 0;
+    for (int c = 1; c <= 8; c *= 2) {
+      const int64_t t = (a.rows * c + slots - 1) / slots * ((tiles + c * kKaWarps - 1) / (c * kKaWarps));
+      if (c == 1 || t < best) {
+        best = t;
+        cs = c;
+      }
+    }
+    bal = best > a.rows * tiles / W + 4;
+  }
   if (bal) {
     const size_t bytes = (size_t)kKaWarps * kKaRing;
     auto kern = kv4_stream_kernel<G, GATHER>;
     if (int rc = set_smem_limit((const void*)kern, bytes, "kv4 attend")) return rc;
     const int grid = (int)imin64(2 * device_sm_count(), kKaMaxWarps / kKaWarps);
     kern<<<grid, kKaThreads, bytes, st>>>(a);
-    kv4_join_kernel<G><<<dim3((unsigned)imin64(a.rows, 2 * device_sm_count()), G), 256, 0, st>>>(a);
+    // launched while the streaming kernel still runs (its CTAs leave no room until they
+    // end), and waiting for it on the device
+    cudaLaunchConfig_t join = {};
+    const int64_t pairs = a.rows * G, ctas = 2 * device_sm_count();
+    const int run = (int)imin64((pairs + ctas - 1) / ctas, kKaJoinWarps);
+    join.gridDim = dim3((unsigned)imin64((pairs + run - 1) / run, 8 * ctas), 1, 1);
+    join.blockDim = dim3(32 * kKaJoinWarps, 1, 1);
+    join.stream = st;
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    join.attrs = early;
+    join.numAttrs = 1;
+    if (int rc = check_launch("kv4 attend")) return rc;
+    if (cudaLaunchKernelEx(&join, kv4_join_kernel<G>, a, run) != cudaSuccess)
+      return check_launch("kv4 attend join");
     note_launches(2);
     return check_launch("kv4 attend");
   }
-  int cs = 1;
-  while (cs < 8 && a.rows * cs * 2 <= 2 * device_sm_count() && cs * 2 * kKaWarps <= tiles) cs *= 2;
   const size_t bytes = (size_t)kKaWarps * kKaRing;
   auto kern = kv4_cluster_kernel<G, GATHER>;
   if (int rc = set_smem_limit((const void*)kern, bytes, "kv4 attend")) return rc;
