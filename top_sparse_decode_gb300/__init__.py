@@ -65,8 +65,15 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+# the current stream's handle without the object around it (a small call's time is
+# mostly the host's)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -250,14 +257,16 @@ class Kv4Cache:
 def _rows(t, shape: SdShape, m: int):
     """(pointer, strides) of a [B][hkv][>= m][128] tensor of any strides with consecutive
     channels; other contiguous tensors and addresses are taken as [B][hkv][m][128]."""
-    if isinstance(t, torch.Tensor) and t.dim() == 4:
-        if tuple(t.shape[:2]) != (shape.batch, shape.hkv) or t.shape[2] < m or t.shape[3] != shape.d:
-            raise ValueError(f"expected [{shape.batch}][{shape.hkv}][>= {m}][{shape.d}] rows, "
-                             f"got {tuple(t.shape)}")
-        if t.stride(3) != 1:
-            raise ValueError("libsd takes rows of consecutive channels")
-        return t.data_ptr(), ctypes.byref(_abi.SdStrides(*t.stride()[:3]))
-    return _ptr(t), None
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        return _ptr(t), None
+    b, h, n, d = t.shape
+    if b != shape.batch or h != shape.hkv or n < m or d != shape.d:
+        raise ValueError(f"expected [{shape.batch}][{shape.hkv}][>= {m}][{shape.d}] rows, "
+                         f"got {tuple(t.shape)}")
+    sb, sh, st, sd_ = t.stride()
+    if sd_ != 1:
+        raise ValueError("libsd takes rows of consecutive channels")
+    return t.data_ptr(), ctypes.byref(_abi.SdStrides(sb, sh, st))
 
 
 def sd_kv4_write(shape: SdShape, cache: Kv4Cache, K, V, m: int, pos=None, length=None,

@@ -1039,20 +1039,28 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 template <int G, bool GATHER>
 int ka_launch(const KaArgs& a, int64_t most, cudaStream_t st) {
   const int64_t tiles = (most + kKaTile - 1) / kKaTile;
-  bool bal = true;
+  // Which kernel, by tiles in a row of work (t), each ~0.6 to 1 us, with what a launch adds
+  // in the same units.  Clusters: the tiles of a warp, 4 for every wave of CTAs, and what
+  // joining c CTAs adds; c > 1 only where all CTAs run at once.  Stream: an even share,
+  // and 12 for finding it and joining.  Measured (us, clusters / stream): 8 rows of 8,192
+  // tokens 11.8 / 13.2, of 16,384 16.8 / 15.3; 128 rows of 4,096 24.1 / 26.5, of 16,384
+  // 66 / 62; 512 rows of 128 10.7 / 12.7, of 2,064 46 / 42.
+  const int64_t slots = 2 * device_sm_count();
+  constexpr int kJoin[4] = {0, 4, 3, 4};  // c = 1, 2, 4, 8
+  int64_t best = 0;
   int cs = 1;
-  {
-    const int64_t slots = 2 * device_sm_count(), W = slots * kKaWarps;
-    int64_t best = 0;
-    for (int c = 1; c <= 8; c *= 2) {
-      const int64_t t = (a.rows * c + slots - 1) / slots * ((tiles + c * kKaWarps - 1) / (c * kKaWarps));
-      if (c == 1 || t < best) {
-        best = t;
-        cs = c;
-      }
+  for (int i = 0; i < 4; ++i) {
+    const int64_t c = 1 << i, w = c * kKaWarps;
+    if (i && a.rows * c > slots) break;
+    const int64_t waves = (a.rows * c + slots - 1) / slots;
+    const int64_t t = (tiles + w - 1) / w + kJoin[i];
+    const int64_t cost = waves > 1 ? waves * (t + 4) : t;
+    if (i == 0 || cost <= best) {
+      best = cost;
+      cs = (int)c;
     }
-    bal = best > a.rows * tiles / W + 4;
   }
+  const bool bal = fallback_forced() || best > a.rows * tiles / (slots * kKaWarps) + 12;
   if (bal) {
     const size_t bytes = (size_t)kKaWarps * kKaRing;
     auto kern = kv4_stream_kernel<G, GATHER>;
