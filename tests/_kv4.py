@@ -9,7 +9,7 @@ truncate, so an addition counts 2 u):
      zmass = scale sum_j |q_j| (c_j s + |m|); |dz| <= 280 u zmass.
   e^(z - max): relative error e^(2 |dz|max) - 1 for the two arguments, and 2^-20 for the
      exponential, the split of p into two 11-bit parts and the scales (each < 2^-21.5).
-  sums over `count` tokens: at most count / 4 + 64 additions in a chain, 2 u each.
+  sums over `count` tokens: at most count / 8 + 64 additions in a chain, 2 u each.
   out: these over vmass = sum_i p_i (c s + |m|) (normalised p), twice: numerator and l.
 """
 import numpy as np
@@ -104,7 +104,7 @@ def attend_row(qb, k, v, rec, tok, scale):
         lse = (top + np.log(l))[:, 0]
         vmass = p @ (vc + np.abs(vm))
         dz = 280 * U * zmass.max(-1)
-        rel = np.expm1(2 * dz) + 2.0 ** -20 + 2 * U * (len(tok) / 4 + 64)
+        rel = np.expm1(2 * dz) + 2.0 ** -20 + 2 * U * (len(tok) / 8 + 64)
         return out, lse, 2 * rel[:, None] * vmass, rel + 4 * U * np.abs(lse)
 
 

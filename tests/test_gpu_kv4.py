@@ -448,3 +448,128 @@ def test_decode_loop(sd):
         q = kv.tokens(rng, (B, h * G), spread=False)
         out, lse = run_attend(sd, shp, q, c, end=lens)
         kv.check(out, lse, kv.attend(q, k, v, rec, ranges(B, h, ncap, None, lens), SCALE))
+
+
+def values(codes, rec, dtype):
+    """What a cache's rows stand for (torch, on the GPU): [..., 128] in `dtype`."""
+    w = codes.contiguous().view(torch.int32)[..., None]
+    c = ((w >> torch.arange(0, 32, 4, device="cuda")) & 15).to(dtype)      # [..., 16, 8]
+    c = c.unflatten(-2, (8, 2)).transpose(-3, -2).flatten(-2)              # [..., 2, 64]
+    sm = rec.to(dtype).unflatten(-1, (2, 2))
+    return (c * sm[..., :1] + sm[..., 1:]).flatten(-2)
+
+
+@pytest.mark.parametrize("B,h,G,n", [(1, 1, 4, 300), (3, 2, 8, 5000), (2, 2, 1, 20000),
+                                     (1, 2, 4, 300000), (1, 1, 8, 600000)])
+def test_as_exact_as_fp32(sd, B, h, G, n):
+    """The error against 64 bits, in the 2-norm, is at most twice that of the plain fp32
+    computation on the same cache (both round alike: one fp32 rounding per operation).
+    Worst-case bounds would pass a loss of many bits here: outputs of flat attention are
+    means of values that change sign, so a bias in the sums shows."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    c = sd.Kv4Cache(B, h, n)
+    shp = sd.make_shape(B, h * G, h, n)
+    for t in range(0, n, 65536):
+        m = min(65536, n - t)
+        kv2 = torch.randn((2, B, h, m, 128), device="cuda", generator=g).bfloat16()
+        sd.sd_kv4_write(shp, c, kv2[0], kv2[1], m, first=t)
+    q = torch.randn((B, h * G, 128), device="cuda", generator=g).bfloat16()
+    got = {}
+    out, lse = torch.empty((B, h * G, 128), device="cuda"), torch.empty((B, h * G), device="cuda")
+    ws = torch.empty(max(sd.sd_kv4_attend_workspace_size(shp),
+                         sd.sd_kv4_gather_attend_workspace_size(shp, n)), dtype=torch.uint8,
+                     device="cuda")
+    sd.sd_kv4_attend(shp, q, c, SCALE, out, lse, ws)
+    got["attend"] = out.clone(), lse.clone()
+    idx = torch.stack([torch.randperm(n, device="cuda", generator=g) for _ in range(B * h)]).int()
+    cnt = torch.full((B * h,), n, dtype=torch.int32, device="cuda")
+    sd.sd_kv4_gather_attend(shp, q, c, idx, n, cnt, n, SCALE, out, lse, ws)
+    got["gather"] = out.clone(), lse.clone()
+
+    def plain(dtype):
+        K, V = values(c.k, c.scale[..., :4], dtype), values(c.v, c.scale[..., 4:], dtype)
+        z = (q.to(dtype).unflatten(1, (h, G)) @ K.transpose(-1, -2)) * SCALE
+        top = z.amax(-1, keepdim=True)
+        p = torch.exp(z - top)
+        l = p.sum(-1, keepdim=True)
+        return ((p @ V) / l).flatten(1, 2).double(), (torch.log(l) + top).flatten(1).double()
+
+    ref, fp32 = plain(torch.float64), plain(torch.float32)
+    for name, pair in got.items():
+        for x, y, f in zip(pair, ref, fp32):
+            err = float((x.double() - y).norm() / y.norm())
+            base = float((f - y).norm() / y.norm())
+            assert err <= max(2 * base, 2e-7), (name, err, base)
+
+
+@pytest.mark.parametrize("kind", ["planes", "quest"])
+def test_step_over_the_cache(sd, kind):
+    """A sparse decode step whose only K and V are the 4-bit cache: written, its keys read
+    back for the index, the step run eagerly and as a graph.  The selection is the bf16
+    step's over the values read back, the attention is the plain one's over it."""
+    from top_sparse_decode_gb300.pipeline import DecodeStep, StepConfig, build_index
+    rng = np.random.default_rng(23)
+    B, h, G, n = 2, 2, 4, 4096
+    kw = dict(k=64, sink=4, local=32) if kind == "planes" else dict(k=8, sink=0, local=1)
+    cfg = StepConfig(sd.SD_IDX_PLANES if kind == "planes" else sd.SD_IDX_MINMAX, B, h * G, h, n,
+                     **kw)
+    shp = sd.make_shape(B, h * G, h, n)
+    c = sd.Kv4Cache(B, h, n)
+    sd.sd_kv4_write(shp, c, dev(kv.tokens(rng, (B, h, n))), dev(kv.tokens(rng, (B, h, n))), n)
+    K = torch.empty((B, h, n, 128), dtype=torch.bfloat16, device="cuda")
+    V = torch.empty_like(K)
+    sd.sd_kv4_read(shp, c, K, V, n)
+    index = build_index(cfg, K)
+    sigma2 = torch.rand((h, 128), device="cuda")
+    q = kv.tokens(rng, (B, h * G), spread=False)
+    dq = dev(q)
+    step = DecodeStep(cfg, None, None, index, sigma2=sigma2, kv4=c)
+    bf16 = DecodeStep(cfg, K, V, index, sigma2=sigma2)
+    step.run(dq)
+    bf16.run(dq)
+    torch.cuda.synchronize()
+    assert torch.equal(step.idx, bf16.idx) and torch.equal(step.count, bf16.count)
+    idx, cnt = host(step.idx, np.int32), host(step.count, np.int32)
+    toks = [idx[r, :cnt[r]] for r in range(B * h)]
+    k, v = host(c.k, np.uint8), host(c.v, np.uint8)
+    rec = host(c.scale.view(torch.int16), np.uint16)
+    ref = kv.attend(q, k, v, rec, toks, step.scale)
+    out, lse = host(step.out, np.float32).copy(), host(step.lse, np.float32).copy()
+    kv.check(out, lse, ref)
+    # the other step's K and V are rounded to bf16, 2^-9 of a value at most: logits move by
+    # dz <= 2^-9 scale sum |q k|, weights by e^(2 dz), outputs by both over the largest |v|
+    zm = (torch.from_numpy(kv.bf16_val(q)).cuda().abs().unflatten(1, (h, G)) @
+          K.float().abs().transpose(-1, -2)).amax().item() * step.scale
+    far = (2 * math.expm1(2 * 2.0 ** -9 * zm) + 2.0 ** -9) * V.float().abs().amax().item()
+    assert np.abs(host(bf16.out, np.float32) - out).max() <= far
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.run(dq)
+    step.out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(host(step.out, np.float32), out)
+    with pytest.raises(ValueError):
+        DecodeStep(cfg, None, None, index, sigma2=sigma2)
+    if kind == "planes":
+        with pytest.raises(ValueError):
+            DecodeStep(StepConfig(cfg.kind, B, h * G, h, n, select_attend=True), K, V, index,
+                       sigma2=sigma2, kv4=c)
+
+
+def test_fallback_switch(sd):
+    """sd_set_fallback_paths(1): the streaming kernel also where clusters would run, with the
+    same results within the bounds."""
+    rng = np.random.default_rng(29)
+    for B, h, G, n in ((1, 1, 4, 5), (3, 2, 8, 333), (2, 8, 2, 100)):
+        q, k, v, rec = setup(rng, B, h, G, n)
+        c = cache_of(sd, k, v, rec)
+        shp = sd.make_shape(B, h * G, h, n)
+        end = rng.integers(0, n + 1, B).astype(np.int32)
+        ref = kv.attend(q, k, v, rec, ranges(B, h, n, None, end), SCALE)
+        before = sd.sd_set_fallback_paths(True)
+        try:
+            out, lse = run_attend(sd, shp, q, c, end=end)
+        finally:
+            sd.sd_set_fallback_paths(before)
+        kv.check(out, lse, ref)

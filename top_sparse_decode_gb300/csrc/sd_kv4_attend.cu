@@ -616,8 +616,14 @@ __device__ __forceinline__ void ka_values(KaState& S, const KaP& P, const KaV& V
           mma_f16(t, a0, a1, a2, a3, P.h[hf][g][0], P.h[hf][g][1]);
         if (G == 8) mma_f16(t, a0, a1, a2, a3, P.l[hf][g][0], P.l[hf][g][1]);
       }
+      float(&o)[4] = S.o[4 * g + u];
+      if constexpr (G == 8) {  // in pairs (2% here; with G <= 4 single additions are 3% faster)
+        f2_split(f2_add(f2_make(o[0], o[1]), f2_make(t[0], t[1])), o[0], o[1]);
+        f2_split(f2_add(f2_make(o[2], o[3]), f2_make(t[2], t[3])), o[2], o[3]);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S.o[4 * g + u][i] += t[i];
+        for (int i = 0; i < 4; ++i) o[i] += t[i];
+      }
     }
 }
 
@@ -739,7 +745,7 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs
   KaState S;
   S.clear();
   uint32_t slot = ring, put = ring + (kKaDepth - 1) * kKaStage;
-  const int tiles = (r.len + kKaTile - 1) / kKaTile;
+  const int tiles = (int)(((unsigned)r.len + kKaTile - 1) / kKaTile);
   ka_tiles<G, GATHER>(
       S, Q, ring, slot, put, (tiles - first + step - 1) / step, r.len - first * kKaTile,
       step * kKaTile,
@@ -806,7 +812,7 @@ constexpr int kKaMaxWarps = 320 * kKaWarps;  // partials of the workspace: two p
 template <bool GATHER>
 __device__ __forceinline__ int ka_item_tiles(const KaArgs& a, int64_t item) {
   const KaRow r = ka_row<GATHER>(a, item, (int)item);  // either reads its one index only
-  return (r.len + kKaTile - 1) / kKaTile;
+  return (int)(((unsigned)r.len + kKaTile - 1) / kKaTile);
 }
 
 // A segment: tiles [a0, a1) of a row; left: tiles of the range from a0 on (a GPU's memory
@@ -817,7 +823,7 @@ struct KaSeg {
   KaRow r;
   __device__ __forceinline__ void load(const KaArgs& a) {
     r = ka_row<GATHER>(a, row, row / a.Hkv);
-    tiles = (r.len + kKaTile - 1) / kKaTile;
+    tiles = (int)(((unsigned)r.len + kKaTile - 1) / kKaTile);
     a1 = min(tiles, a0 + left);
   }
   // The range's next segment; false at its end.

@@ -17,6 +17,10 @@ StepConfig.fused the scan and the top-k run as one call instead (sd_score_topk,
 same results).  For signatures the scan
 and the top-k run as one call (sd_hamming_topk, same idx and count, no scores)
 unless StepConfig.hamming_fused is False.
+
+With a 4-bit K/V cache (DecodeStep's kv4: a Kv4Cache filled by sd_kv4_write) the last
+stage is sd_kv4_gather_attend, and the step needs no bf16 K and V; the index is built
+from the keys as they were written, or from sd_kv4_read's.
 """
 from __future__ import annotations
 
@@ -26,9 +30,10 @@ from typing import Optional
 
 import torch
 
-from . import (SD_IDX_LANDMARK, SD_IDX_MINMAX, SD_IDX_PLANES, SD_IDX_SIG, SD_PLAN_WATERFILL,
+from . import (Kv4Cache, SD_IDX_LANDMARK, SD_IDX_MINMAX, SD_IDX_PLANES, SD_IDX_SIG, SD_PLAN_WATERFILL,
                SD_SCORE_F32, SD_SCORE_I32, make_select, make_shape, sd_build_index, sd_encode_query,
-               sd_gather_attend, sd_gather_attend_workspace_size, sd_plan, sd_plan_score,
+               sd_gather_attend, sd_gather_attend_workspace_size, sd_kv4_gather_attend,
+               sd_kv4_gather_attend_workspace_size, sd_plan, sd_plan_score,
                sd_score, sd_score_topk, sd_score_topk_workspace_size, sd_topk,
                sd_hamming_topk, sd_hamming_topk_workspace_size, sd_select_attend,
                sd_select_attend_workspace_size, sd_topk_wmax,
@@ -110,13 +115,17 @@ def build_index(cfg: StepConfig, K: torch.Tensor, enc=None, stream=None) -> dict
 class DecodeStep:
     """Preallocated buffers and the call sequence of one decode step."""
 
-    def __init__(self, cfg: StepConfig, K: torch.Tensor, V: torch.Tensor, index: dict,
-                 enc=None, sigma2: Optional[torch.Tensor] = None,
-                 scale: Optional[float] = None):
-        self.cfg = cfg
+    def __init__(self, cfg: StepConfig, K: Optional[torch.Tensor], V: Optional[torch.Tensor],
+                 index: dict, enc=None, sigma2: Optional[torch.Tensor] = None,
+                 scale: Optional[float] = None, kv4: Optional[Kv4Cache] = None):
+        if kv4 is None and (K is None or V is None):
+            raise ValueError("DecodeStep needs K and V, or a 4-bit cache (kv4)")
+        if kv4 is not None and cfg.select_attend:
+            raise ValueError("select_attend runs over bf16 K and V, not over a 4-bit cache")
+        self.cfg, self.kv4 = cfg, kv4
         self.K, self.V, self.index, self.enc, self.sigma2 = K, V, index, enc, sigma2
         self.scale = 1.0 / math.sqrt(cfg.d) if scale is None else scale
-        dev = K.device
+        dev = K.device if kv4 is None else kv4.k.device
         c = cfg
         self.shape = make_shape(c.B, c.Hq, c.Hkv, c.n, c.d, c.n_cap)
         self.rows = c.B * c.Hkv
@@ -137,7 +146,8 @@ class DecodeStep:
         if self.fused:
             fws = sd_score_topk_workspace_size(self.shape, self.sel)
             self.fused_ws = torch.empty(max(fws, 256), dtype=torch.uint8, device=dev)
-        aws = sd_gather_attend_workspace_size(self.shape, c.max_count)
+        aws = (sd_gather_attend_workspace_size if kv4 is None else
+               sd_kv4_gather_attend_workspace_size)(self.shape, c.max_count)
         self.att_ws = torch.empty(max(aws, 256), dtype=torch.uint8, device=dev)
         self.use_sa = self.use_wmax and c.select_attend
         self.use_ht = c.kind == SD_IDX_SIG and c.hamming_fused and c.block == 1
@@ -204,6 +214,10 @@ class DecodeStep:
 
     def stage_attend(self, q, stream=None):
         c = self.cfg
+        if self.kv4 is not None:
+            sd_kv4_gather_attend(self.shape, q, self.kv4, self.idx, c.max_count, self.count,
+                                 c.max_count, self.scale, self.out, self.lse, self.att_ws, stream)
+            return
         sd_gather_attend(self.shape, q, self.K, self.V, self.idx, c.max_count, self.count,
                          c.max_count, self.scale, self.out, self.lse, self.att_ws, stream)
 
