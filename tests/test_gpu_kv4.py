@@ -25,6 +25,14 @@ def sd():
     return m
 
 
+@pytest.fixture(params=[False, True], ids=["chosen", "stream"])
+def path(sd, request):
+    """The kernel the library chooses, then the streaming one for every size."""
+    before = sd.sd_set_fallback_paths(request.param)
+    yield
+    sd.sd_set_fallback_paths(before)
+
+
 def cache_of(sd, k, v, rec):
     B, h, n = k.shape[:3]
     return sd.Kv4Cache(B, h, n, k=dev(k), v=dev(v), scale=dev(rec))
@@ -195,7 +203,7 @@ def ranges(B, h, n, begin, end):
 
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 33, 64, 127, 257, 1000, 4099])
-def test_attend_lengths(sd, n, G):
+def test_attend_lengths(sd, path, n, G):
     rng = np.random.default_rng(n * 10 + G)
     q, k, v, rec = setup(rng, 2, 2, G, n + 5)
     rec[:, :, n:] = 0x7FC0  # NaN behind the last token
@@ -210,7 +218,7 @@ def test_attend_lengths(sd, n, G):
 
 @pytest.mark.parametrize("B,h,G,n", [(7, 1, 4, 300), (40, 2, 8, 130), (130, 4, 2, 70),
                                      (9, 8, 1, 1025), (600, 1, 4, 40)])
-def test_attend_ragged(sd, B, h, G, n):
+def test_attend_ragged(sd, path, B, h, G, n):
     """Ranges of every kind: empty, inverted, outside [0, n), one token, all."""
     rng = np.random.default_rng(B)
     q, k, v, rec = setup(rng, B, h, G, n + 3)
@@ -242,7 +250,7 @@ def test_attend_ragged(sd, B, h, G, n):
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
 @pytest.mark.parametrize("B,h,mc", [(1, 1, 1), (2, 2, 17), (3, 2, 64), (2, 8, 530), (64, 2, 129),
                                     (300, 1, 33)])
-def test_gather(sd, B, h, mc, G):
+def test_gather(sd, path, B, h, mc, G):
     """Any order, duplicates, indices outside [0, n), counts of -1, 0 and above max_count."""
     rng = np.random.default_rng(mc * 31 + G)
     n, ncap, stride = 700, 704, mc + 3
@@ -275,7 +283,7 @@ def test_gather(sd, B, h, mc, G):
     assert np.array_equal(out, out2)
 
 
-def test_gather_none(sd):
+def test_gather_none(sd, path):
     rng = np.random.default_rng(1)
     q, k, v, rec = setup(rng, 2, 2, 4, 64)
     shp = sd.make_shape(2, 8, 2, 64)
@@ -285,7 +293,7 @@ def test_gather_none(sd):
 
 
 @pytest.mark.parametrize("gather", [False, True])
-def test_nan_stays_in_its_row_and_group(sd, gather):
+def test_nan_stays_in_its_row_and_group(sd, path, gather):
     """A NaN value makes its group of outputs NaN, a NaN key its whole KV head; other rows,
     also those that follow in the same call, are untouched."""
     rng = np.random.default_rng(11)
@@ -309,7 +317,7 @@ def test_nan_stays_in_its_row_and_group(sd, gather):
 
 @pytest.mark.parametrize("case", ["sharp", "flat", "growing", "big_v", "tiny", "zero_q",
                                   "negative_scale", "big_q", "huge_unweighted"])
-def test_attend_ranges_of_values(sd, case):
+def test_attend_ranges_of_values(sd, path, case):
     """Logits that differ by hundreds, maxima that grow along the cache, values whose scales
     differ by many powers of two, queries and caches at the ends of the range."""
     rng = np.random.default_rng(5)
@@ -555,6 +563,82 @@ def test_step_over_the_cache(sd, kind):
         with pytest.raises(ValueError):
             DecodeStep(StepConfig(cfg.kind, B, h * G, h, n, select_attend=True), K, V, index,
                        sigma2=sigma2, kv4=c)
+
+
+
+def test_two_streams_at_once(sd):
+    """Calls on two streams at the same time, each with a workspace of its own."""
+    rng = np.random.default_rng(31)
+    B, h, G, n = 4, 4, 4, 9000
+    q, k, v, rec = setup(rng, B, h, G, n)
+    c, shp = cache_of(sd, k, v, rec), sd.make_shape(B, h * G, h, n)
+    dq = dev(q)
+    ends = [dev(np.array(e, np.int32)) for e in ((n, 1, 4500, 0), (77, n, n, 8999))]
+    want = [run_attend(sd, shp, q, c, end=host(e, np.int32)) for e in ends]
+    streams = [torch.cuda.Stream() for _ in ends]
+    outs = [torch.zeros((B, h * G, 128), device="cuda") for _ in ends]
+    lses = [torch.zeros((B, h * G), device="cuda") for _ in ends]
+    ws = [torch.empty(sd.sd_kv4_attend_workspace_size(shp), dtype=torch.uint8, device="cuda")
+          for _ in ends]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            sd.sd_kv4_attend(shp, dq, c, SCALE, outs[i], lses[i], ws[i], end=ends[i], stream=st)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert np.array_equal(host(outs[i], np.float32), want[i][0])
+        assert np.array_equal(host(lses[i], np.float32), want[i][1])
+
+
+def test_arrays_at_16_bytes(sd):
+    """Cache arrays, q and outputs that start 16 bytes into an allocation."""
+    rng = np.random.default_rng(37)
+    B, h, G, n = 2, 3, 4, 301
+    q, k, v, rec = setup(rng, B, h, G, n)
+
+    def off(x):
+        t = dev(x).contiguous().view(torch.uint8).flatten()
+        buf = torch.zeros(t.numel() + 16, dtype=torch.uint8, device="cuda")
+        buf[16:] = t
+        return buf[16:]
+
+    c = sd.Kv4Cache(B, h, n, k=off(k), v=off(v), scale=off(rec))
+    shp = sd.make_shape(B, h * G, h, n)
+    out = torch.zeros(B * h * G * 128 + 4, device="cuda")[4:]
+    lse = torch.zeros(B * h * G + 1, device="cuda")[1:]
+    ws = torch.zeros(sd.sd_kv4_attend_workspace_size(shp) + 16, dtype=torch.uint8, device="cuda")[16:]
+    ref = kv.attend(q, k, v, rec, ranges(B, h, n, None, None), SCALE)
+    sd.sd_kv4_attend(shp, off(q), c, SCALE, out, lse, ws)
+    torch.cuda.synchronize()
+    kv.check(host(out, np.float32).reshape(B, h * G, 128), host(lse, np.float32).reshape(B, h * G), ref)
+    idx = np.stack([rng.permutation(n)[:100] for _ in range(B * h)]).astype(np.int32)
+    sd.sd_kv4_gather_attend(shp, off(q), c, dev(idx), 100, dev(np.full(B * h, 100, np.int32)), 100,
+                            SCALE, out, lse, ws)
+    torch.cuda.synchronize()
+    ref = kv.attend(q, k, v, rec, list(idx), SCALE)
+    kv.check(host(out, np.float32).reshape(B, h * G, 128), host(lse, np.float32).reshape(B, h * G), ref)
+    K = off(kv.tokens(rng, (B, h, n))).view(torch.bfloat16).view(B, h, n, 128)
+    sd.sd_kv4_write(shp, c, K, K, n)
+    ek = kv.encode(host(K.contiguous().view(torch.int16), np.uint16),
+                   host(K.contiguous().view(torch.int16), np.uint16))
+    assert np.array_equal(host(c.k, np.uint8).reshape(ek[0].shape), ek[0])
+    assert np.array_equal(host(c.v, np.uint8).reshape(ek[1].shape), ek[1])
+
+
+def test_many_rows(sd, path):
+    """20,000 rows, most of them empty or of one token."""
+    rng = np.random.default_rng(41)
+    B, h, G, n = 5000, 4, 2, 40
+    q, k, v, rec = setup(rng, B, h, G, n)
+    c, shp = cache_of(sd, k, v, rec), sd.make_shape(B, h * G, h, n)
+    end = rng.choice([0, 0, 1, 33, 40], B).astype(np.int32)
+    out, lse = run_attend(sd, shp, q, c, end=end)
+    some = np.concatenate((np.arange(40), rng.integers(0, B, 60)))
+    toks = [np.arange(end[b]) for b in some for _ in range(h)]
+    kv.check(out[some], lse[some], kv.attend(q[some], k[some], v[some], rec[some], toks, SCALE))
+    none = end == 0
+    assert not out[none].any() and np.all(np.isneginf(lse[none]))
+    assert np.all(np.isfinite(lse[~none]))
 
 
 def test_fallback_switch(sd):

@@ -14,16 +14,28 @@
 //    tokens.  q is scaled by a power of two per head to f16; bf16 values stay exact
 //    unless they are 2^-32 below the head's largest.
 //  * PV: O^T = V^T P^T, 16 channels as rows, heads as columns, 16 tokens deep.  w = p s f is
-//    split in two f16 parts (22 bits; f a power of two per head and group that holds the
-//    largest w in [2^7, 2^14], raised and lowered as an online softmax moves its
-//    maximum).  With G <= 4 columns 0..3 take the high parts and 4..7 the low ones (8
-//    MMAs per 16 tokens), with G = 8 the low parts are 8 more.
-//  * p = 2^(z log2 e - m); m, a whole number per head, is raised only when a logit
-//    exceeds it by about 8.
+//    split in two f16 parts (22 bits: one rounding to 11 would cost 2^-12 of an output; f
+//    a power of two per head and group that holds the largest w in [2^7, 2^14], raised and
+//    lowered as an online softmax moves its maximum).  With G <= 4 columns 0..3 take the
+//    high parts and 4..7 the low ones (8 MMAs per 16 tokens), with G = 8 the low parts are
+//    8 more.
+//  * p = 2^(z log2 e - m); m, a whole number per head, is raised only when weights
+//    exceed 2^8 or so.
 //
 // Each warp pulls 32-token tiles (4,608 bytes) through a ring of its own in shared memory
 // with 16-byte asynchronous copies; rows are swizzled there so that both operands read
-// without bank conflicts.
+// without bank conflicts.  No warp waits for another while it works.
+//
+// What bounds it: 144 bytes a token and KV head from HBM are 397 cycles of an SM's four
+// schedulers per 16 tokens at the measured copy rate; the work on them is ~311
+// instructions (G <= 4; 360 with G = 8), half of them integer operations that issue every
+// second cycle: ~88 to take the codes apart, 64 to scale and centre them, 16 (24) MMAs of
+// 8.4 cycles.  It runs at ~420 cycles (G <= 4).  Measured (GB300): 8 KV heads of 1,048,576
+// tokens, G = 4: 205 us, 5.9 TB/s, 87 % of the copy rate; 512 of 16,384, G = 8: 246 us, 4.9
+// TB/s.  Tried and slower: six warps a CTA (their 168 registers spill; 210 us), scores of
+// the next tile beside the values of this one (219 us), e4m3 MMAs for the scores
+// (converted to f16 by the compiler on this GPU; 284 us), subnormal codes without the
+// multiplication (216 us, but outputs off by up to 1e-2 of themselves).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -46,7 +58,7 @@ constexpr int kKaStage = kKaOffMask + 16;
 constexpr int kKaRing = kKaDepth * kKaStage;
 constexpr float kKaLog2e = 1.4426950408889634f;
 constexpr float kKaLn2 = 0.6931471805599453f;
-constexpr float kKaEmpty = -1e30f;   // m before the first token
+constexpr float kKaEmpty = -3e38f;   // m before the first token
 constexpr float kKaPMax = 512.0f;    // a lane's largest sum of four p that leaves m as it is
 constexpr float kKaWMax = 16384.0f;  // largest w that leaves f as it is (0x7400 in f16)
 constexpr float kKaF0 = 1.2676506e30f;  // 2^100: f before the first token, and its limit
@@ -716,8 +728,10 @@ __device__ __forceinline__ void ka_write(const KaArgs& a, int64_t bq, int j, flo
   if (a.lse && j == 0) a.lse[bq] = l != 0.0f ? (m + log2f(l)) * kKaLn2 : -INFINITY;
 }
 
-// A few rows: one cluster of CTAs per row, tiles dealt to its warps in turn, the states
-// joined through shared and distributed shared memory.
+// Few tiles: one cluster of CTAs per row, tiles dealt to its warps in turn, the states joined
+// through shared and distributed shared memory.  One launch and no workspace: a call of
+// one 4,096-token KV head takes 9 us as a graph node (10.3 with the streaming kernel), of
+// which an empty one is 4.8.
 template <int G, bool GATHER>
 __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -850,6 +864,7 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_stream_kernel(const KaArgs 
   const int64_t per = (items + kKaThreads - 1) / kKaThreads;
   const int64_t i0 = imin64(threadIdx.x * per, items), i1 = imin64(i0 + per, items);
   long long incl = 0;
+#pragma unroll 8
   for (int64_t i = i0; i < i1; ++i) incl += ka_item_tiles<GATHER>(a, i) * mult;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
