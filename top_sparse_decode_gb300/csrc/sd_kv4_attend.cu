@@ -51,11 +51,17 @@ namespace cg = cooperative_groups;
 constexpr int kKaTile = 32;    // tokens per tile
 constexpr int kKaWarps = 4;    // warps per CTA
 constexpr int kKaThreads = 32 * kKaWarps;
-constexpr int kKaDepth = 4;    // tiles in a warp's ring
 constexpr int kKaOffV = kKaTile * kKv4Row, kKaOffS = 2 * kKaOffV;
 constexpr int kKaOffMask = kKaOffS + kKaTile * 2 * kKv4Scales;
-constexpr int kKaStage = kKaOffMask + 16;
-constexpr int kKaRing = kKaDepth * kKaStage;
+constexpr int kKaOffQ = kKaOffMask + 16;  // the row's queries, where the tile is its first
+template <int G>
+constexpr int kKaStage = kKaOffQ + G * kD * 2;
+// Tiles in a warp's ring (G = 4: 204 us with 3 and 211 with 4 on the longest case above, G
+// = 8: 257 and 252).
+template <int G>
+constexpr int kKaDepth = G == 8 ? 4 : 3;
+template <int G>
+constexpr int kKaRing = kKaDepth<G> * kKaStage<G>;
 constexpr float kKaLog2e = 1.4426950408889634f;
 constexpr float kKaLn2 = 0.6931471805599453f;
 constexpr float kKaEmpty = -3e38f;   // m before the first token
@@ -254,19 +260,26 @@ __device__ __forceinline__ int ka_head(int c) {
   return G == 8 ? c : c & 3;
 }
 
+// Requests a row's queries into a stage, with its first tile.
 template <int G>
-__device__ __forceinline__ void ka_load_q(KaQ<G>& Q, const KaArgs& a, int64_t row, int lane) {
-  const int gid = lane >> 2, tig = lane & 3;
-  const int b = (int)(row / a.Hkv), h = (int)(row % a.Hkv), hd = ka_head<G>(gid);
+__device__ __forceinline__ void ka_issue_q(const KaArgs& a, uint32_t stage, int row, int lane) {
+  const uint16_t* q = a.q + ((int64_t)(row / a.Hkv) * a.Hq + row % a.Hkv * G) * kD;
+#pragma unroll
+  for (int c = lane; c < G * kD / 8; c += 32) ka_copy16(stage + kKaOffQ + 16 * c, q + 8 * c);
+}
+
+template <int G>
+__device__ __forceinline__ void ka_load_q(KaQ<G>& Q, const KaArgs& a, uint32_t stage, int lane) {
+  const int gid = lane >> 2, tig = lane & 3, hd = ka_head<G>(gid);
   const bool real = hd < G;
-  const uint16_t* qr = a.q + ((int64_t)b * a.Hq + h * G + (real ? hd : 0)) * kD;
+  const uint32_t qr = stage + kKaOffQ + (real ? hd : 0) * kD * 2;
   uint4 w[2][2];
   float top = 0.0f, sum[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int g = 0; g < 2; ++g)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      w[g][j] = *reinterpret_cast<const uint4*>(qr + 64 * g + 16 * tig + 8 * j);
+      w[g][j] = lds128(qr + 2 * (64 * g + 16 * tig + 8 * j));
       if (!real) w[g][j] = make_uint4(0u, 0u, 0u, 0u);
       const uint32_t x[4] = {w[g][j].x, w[g][j].y, w[g][j].z, w[g][j].w};
 #pragma unroll
@@ -646,26 +659,36 @@ __device__ __forceinline__ uint32_t ka_valid(uint32_t stage, int left) {
   return left >= kKaTile ? 0xFFFFFFFFu : (1u << left) - 1u;
 }
 
-// The tiles of a row (or a part of one), `tiles` of them, the first in stage `slot`:
-// `issue` requests one more tile into the stage it is given and commits.
+// The tiles of a row (or a part of one), `tiles` of them, the first in stage `slot` with the
+// queries: `issue` requests one more tile into the stage it is given and commits.
 template <int G, bool GATHER, class Issue>
-__device__ __forceinline__ void ka_tiles(KaState& S, const KaQ<G>& Q, uint32_t ring, uint32_t& slot,
-                                         uint32_t& put, int tiles, int left, int step, Issue issue,
-                                         int lane) {
+__device__ __forceinline__ void ka_tiles(KaState& S, const KaArgs& a, uint32_t ring,
+                                         uint32_t& slot, uint32_t& put, int tiles, int left,
+                                         int step, Issue issue, int lane) {
+  if (tiles <= 0) return;
+  KaQ<G> Q;
+  ka_wait<kKaDepth<G> - 2>();
+  __syncwarp();
+  ka_load_q<G>(Q, a, slot, lane);
   for (; tiles > 0; --tiles, left -= step) {
-    issue(put);
-    ka_wait<kKaDepth - 1>();
+    if constexpr (G != 8) {
+      issue(put);
+      ka_wait<kKaDepth<G> - 1>();
+    } else {
+      ka_wait<kKaDepth<G> - 2>();
+    }
     __syncwarp();
     KaScores<G> C;
     ka_scores<G>(C, Q, slot, lane);
     KaV V;  // requested here, where the chain of the weights leaves the time
     ka_load_v(V, slot, lane);
+    if constexpr (G == 8) issue(put);  // 244 us here, 252 at the top; with G <= 4 213 and 211
     KaP P;
     ka_weights<G>(P, S, C, Q, slot, ka_valid<GATHER>(slot, left), lane);
     ka_values<G>(S, P, V);
     __syncwarp();
     put = slot;
-    slot = slot == ring + (kKaDepth - 1) * kKaStage ? ring : slot + kKaStage;
+    slot = slot == ring + (kKaDepth<G> - 1) * kKaStage<G> ? ring : slot + kKaStage<G>;
   }
 }
 
@@ -742,26 +765,25 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs
   const int b = (int)(row / a.Hkv), h = (int)(row % a.Hkv);
   const KaRow r = ka_row<GATHER>(a, row, b);
   const int step = CS * kKaWarps;
-  const uint32_t ring = smem_addr(smem) + warp * kKaRing;
+  const uint32_t ring = smem_addr(smem) + warp * kKaRing<G>;
   const int first = rank * kKaWarps + warp;
   KaSrc<GATHER> src;
   src.set(a, row, r, first, lane);
 #pragma unroll
-  for (int d = 0; d < kKaDepth - 1; ++d) {
+  for (int d = 0; d < kKaDepth<G> - 1; ++d) {
     if (src.left > 0) {
-      src.issue(a, ring + d * kKaStage, lane);
+      if (d == 0) ka_issue_q<G>(a, ring, (int)row, lane);
+      src.issue(a, ring + d * kKaStage<G>, lane);
       src.advance(step, lane);
     }
     ka_commit();
   }
-  KaQ<G> Q;
-  ka_load_q<G>(Q, a, row, lane);
   KaState S;
   S.clear();
-  uint32_t slot = ring, put = ring + (kKaDepth - 1) * kKaStage;
+  uint32_t slot = ring, put = ring + (kKaDepth<G> - 1) * kKaStage<G>;
   const int tiles = (int)(((unsigned)r.len + kKaTile - 1) / kKaTile);
   ka_tiles<G, GATHER>(
-      S, Q, ring, slot, put, (tiles - first + step - 1) / step, r.len - first * kKaTile,
+      S, a, ring, slot, put, (tiles - first + step - 1) / step, r.len - first * kKaTile,
       step * kKaTile,
       [&](uint32_t stage) {
         if (src.left > 0) {
@@ -916,7 +938,8 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_stream_kernel(const KaArgs 
   int itile = it.a0;
   KaSrc<GATHER> src;
   src.set(a, it.row, it.r, itile, lane);
-  const uint32_t ring = smem_addr(smem) + warp * kKaRing;
+  const uint32_t ring = smem_addr(smem) + warp * kKaRing<G>;
+  ka_issue_q<G>(a, ring, it.row, lane);
   auto issue = [&](uint32_t stage) {
     if (more) {
       src.issue(a, stage, lane);
@@ -925,20 +948,24 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_stream_kernel(const KaArgs 
       } else {
         more = it.next(a);
         itile = 0;
-        if (more) src.set(a, it.row, it.r, 0, lane);
+        if (more) {
+          src.set(a, it.row, it.r, 0, lane);
+          // its queries into the stage that its first tile takes next (which may hold the
+          // tile being worked on, whose queries are in registers)
+          ka_issue_q<G>(a, stage == ring + (kKaDepth<G> - 1) * kKaStage<G> ? ring : stage + kKaStage<G>,
+                        it.row, lane);
+        }
       }
     }
     ka_commit();
   };
 #pragma unroll
-  for (int d = 0; d < kKaDepth - 1; ++d) issue(ring + d * kKaStage);
-  uint32_t slot = ring, put = ring + (kKaDepth - 1) * kKaStage;
+  for (int d = 0; d < kKaDepth<G> - 1; ++d) issue(ring + d * kKaStage<G>);
+  uint32_t slot = ring, put = ring + (kKaDepth<G> - 1) * kKaStage<G>;
   do {
-    KaQ<G> Q;
-    ka_load_q<G>(Q, a, cur.row, lane);
     KaState S;
     S.clear();
-    ka_tiles<G, GATHER>(S, Q, ring, slot, put, cur.a1 - cur.a0, cur.r.len - cur.a0 * kKaTile,
+    ka_tiles<G, GATHER>(S, a, ring, slot, put, cur.a1 - cur.a0, cur.r.len - cur.a0 * kKaTile,
                         kKaTile, issue, lane);
     const bool whole = cur.a0 == 0 && cur.a1 == cur.tiles;
     if (cur.a0 == 0 && lane == 0) {
@@ -1083,7 +1110,7 @@ int ka_launch(const KaArgs& a, int64_t most, cudaStream_t st) {
   }
   const bool bal = fallback_forced() || best > a.rows * tiles / (slots * kKaWarps) + 12;
   if (bal) {
-    const size_t bytes = (size_t)kKaWarps * kKaRing;
+    const size_t bytes = (size_t)kKaWarps * kKaRing<G>;
     auto kern = kv4_stream_kernel<G, GATHER>;
     if (int rc = set_smem_limit((const void*)kern, bytes, "kv4 attend")) return rc;
     const int grid = (int)imin64(2 * device_sm_count(), kKaMaxWarps / kKaWarps);
@@ -1107,7 +1134,7 @@ int ka_launch(const KaArgs& a, int64_t most, cudaStream_t st) {
     note_launches(2);
     return check_launch("kv4 attend");
   }
-  const size_t bytes = (size_t)kKaWarps * kKaRing;
+  const size_t bytes = (size_t)kKaWarps * kKaRing<G>;
   auto kern = kv4_cluster_kernel<G, GATHER>;
   if (int rc = set_smem_limit((const void*)kern, bytes, "kv4 attend")) return rc;
   cudaLaunchConfig_t cfg = {};
