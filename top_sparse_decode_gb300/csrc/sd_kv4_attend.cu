@@ -843,6 +843,13 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs
 // kernel joins them in range order.
 constexpr int kKaMaxWarps = 320 * kKaWarps;  // partials of the workspace: two per warp
 
+// The ranges are equal shares of the rows' weights: kKaRowCost places that stand for what a
+// row costs beside its tiles (queries, output, a last tile that is half empty), then one
+// place per tile.  Without them the warps that drew a ragged batch's short rows ended 20 us
+// after the others (64 x 8 rows of 1 to 16,384 tokens, G = 4: 127 us; 122, 118, 108, 109
+// and 110 with 1, 2, 4, 6 and 8).
+constexpr int kKaRowCost = 4;
+
 // Items of the partition: sequences of Hkv rows each, or single rows with counts of
 // their own.
 template <bool GATHER>
@@ -850,9 +857,12 @@ __device__ __forceinline__ int ka_item_tiles(const KaArgs& a, int64_t item) {
   const KaRow r = ka_row<GATHER>(a, item, (int)item);  // either reads its one index only
   return (int)(((unsigned)r.len + kKaTile - 1) / kKaTile);
 }
+__device__ __forceinline__ int64_t ka_weight_of(int tiles) {
+  return tiles > 0 ? (int64_t)tiles + kKaRowCost : 0;
+}
 
-// A segment: tiles [a0, a1) of a row; left: tiles of the range from a0 on (a GPU's memory
-// holds far fewer than 2^31 tiles a warp).
+// A segment: tiles [a0, a1) of a row; left: places of the range from tile a0's on (a GPU's
+// memory holds far fewer than 2^31 tiles a warp).
 template <bool GATHER>
 struct KaSeg {
   int row, left, a0, a1, tiles;
@@ -864,7 +874,7 @@ struct KaSeg {
   }
   // The range's next segment; false at its end.
   __device__ __forceinline__ bool next(const KaArgs& a) {
-    left -= a1 - a0;
+    left -= a1 - a0 + kKaRowCost;
     if (left <= 0) return false;
     a0 = 0;
     do {
@@ -887,7 +897,7 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_stream_kernel(const KaArgs 
   const int64_t i0 = imin64(threadIdx.x * per, items), i1 = imin64(i0 + per, items);
   long long incl = 0;
 #pragma unroll 8
-  for (int64_t i = i0; i < i1; ++i) incl += ka_item_tiles<GATHER>(a, i) * mult;
+  for (int64_t i = i0; i < i1; ++i) incl += ka_weight_of(ka_item_tiles<GATHER>(a, i)) * mult;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
@@ -922,14 +932,16 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_stream_kernel(const KaArgs 
     for (int k = 0; k < kKaWarps; ++k)
       run += __popc(__ballot_sync(0xFFFFFFFFu, ends[32 * k + lane] <= g0));
     int64_t at = run ? ends[run - 1] : 0, item = run * per;
-    int t = ka_item_tiles<GATHER>(a, item);
-    while (g0 >= at + t * mult && item + 1 < items) {
-      at += t * mult;
-      t = ka_item_tiles<GATHER>(a, ++item);
+    int64_t w = ka_weight_of(ka_item_tiles<GATHER>(a, item));
+    while (g0 >= at + w * mult && item + 1 < items) {
+      at += w * mult;
+      w = ka_weight_of(ka_item_tiles<GATHER>(a, ++item));
     }
-    cur.row = (int)(item * mult + (g0 - at) / t);
-    cur.a0 = (int)((g0 - at) % t);
-    cur.left = (int)(g1 - g0);
+    const int64_t in = (g0 - at) / w, off = g0 - at - in * w - kKaRowCost;
+    cur.row = (int)(item * mult + in);
+    cur.a0 = (int)imax64(off, 0);
+    cur.left = (int)(g1 - g0 + imin64(off, 0));
+    if (cur.left <= 0) return;  // only places before the row's first tile
     cur.load(a);
   }
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
