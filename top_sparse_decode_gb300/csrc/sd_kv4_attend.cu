@@ -1038,7 +1038,7 @@ __device__ __forceinline__ float4 ka_gather_parts(const KaArgs& a, int first, in
 
 // Joins the partials of the rows that were cut.  A CTA takes `run` heads of rows at a time,
 // a warp each; those of more than kKaAlone partials are summed by all its warps.
-constexpr int kKaJoinWarps = 8;
+constexpr int kKaJoinWarps = 16;
 constexpr int kKaAlone = 16;
 
 template <int G>
