@@ -81,6 +81,7 @@ struct KvLane {
 };
 
 __global__ void __launch_bounds__(32 * kKvWarps) kv4_write_kernel(const KvMoveArgs a) {
+  kv4_wait_prior();
   const KvLane L(a);
   const bool asked = a.x[L.half] != nullptr;
   const int64_t st = a.st[L.half];
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv4_write_kernel(const KvMoveAr
 }
 
 __global__ void __launch_bounds__(32 * kKvWarps) kv4_read_kernel(const KvMoveArgs a) {
+  kv4_wait_prior();
   const KvLane L(a);
   const int64_t st = a.st[L.half];
   uint16_t* dst = a.x[L.half] + L.x + L.t * st;
@@ -205,12 +207,8 @@ int launch_kv4_move(bool write, const Dims& s, const sd_kv4& c, void* K, const s
   const int64_t rows = (int64_t)s.B * s.Hkv, steps = (m + kKvStep - 1) / kKvStep;
   const int64_t waves = imax64(1, (int64_t)device_sm_count() * 32 / rows);
   const dim3 grid((unsigned)imin64(steps, waves), (unsigned)rows);
-  if (write)
-    kv4_write_kernel<<<grid, 32 * kKvWarps, 0, st>>>(a);
-  else
-    kv4_read_kernel<<<grid, 32 * kKvWarps, 0, st>>>(a);
-  note_launches(1);
-  return check_launch(write ? "kv4 write" : "kv4 read");
+  return write ? kv4_launch("kv4 write", kv4_write_kernel, grid, 32 * kKvWarps, 0, 0, st, a)
+               : kv4_launch("kv4 read", kv4_read_kernel, grid, 32 * kKvWarps, 0, 0, st, a);
 }
 
 }  // namespace sd

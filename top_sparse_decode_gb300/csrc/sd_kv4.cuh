@@ -11,6 +11,34 @@ constexpr int kKv4Row = 64;     // code bytes of a token's K (or V) row
 constexpr int kKv4Scales = 8;   // bf16 values of a token's scale record
 constexpr uint32_t kKv4NanPair = 0x7FC07FC0u;
 
+// Short kernels are launched while the kernel before them in the stream ends, and wait for
+// it here before they touch memory, which hides a part of the launch's latency (a write
+// and a read of 64 x 8 tokens 5.0 us, 5.8 without; a cluster attention 0.3 to 0.7 us less).
+__device__ __forceinline__ void kv4_wait_prior() {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+template <class... P, class... A>
+int kv4_launch(const char* what, void (*kern)(P...), dim3 grid, int threads, size_t smem,
+               int cluster, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return check_launch(what);
+  note_launches(1);
+  return check_launch(what);
+}
+
 // Pairs of fp32 values, one instruction for both.
 __device__ __forceinline__ uint64_t f2_make(float x, float y) {
   uint64_t r;

@@ -205,25 +205,26 @@ struct KaSrc {
     if (GATHER) {
       const bool ok = (unsigned)tok < (unsigned)a.n;
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
-      const uint32_t safe = ok ? tok : 0;
+      const uint8_t* sb = reinterpret_cast<const uint8_t*>(s);
+      if (mask == 0xFFFFFFFFu) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const uint32_t t = __shfl_sync(0xFFFFFFFFu, safe, tl + 8 * h);
-        const uint8_t *kt = at(k, t, kKv4Row), *vt = at(v, t, kKv4Row);
-        if (mask == 0xFFFFFFFFu) {
-          ka_copy16_near(dst + h * 8 * kKv4Row, kt);
-          ka_copy16_near(dst + h * 8 * kKv4Row + kKaOffV, vt);
-        } else {
-          const bool val = mask >> (tl + 8 * h) & 1u;
-          ka_copy16(dst + h * 8 * kKv4Row, kt, val);
-          ka_copy16(dst + h * 8 * kKv4Row + kKaOffV, vt, val);
+        for (int h = 0; h < 4; ++h) {
+          const uint32_t t = __shfl_sync(0xFFFFFFFFu, tok, tl + 8 * h);
+          ka_copy16_near(dst + h * 8 * kKv4Row, at(k, t, kKv4Row));
+          ka_copy16_near(dst + h * 8 * kKv4Row + kKaOffV, at(v, t, kKv4Row));
         }
+        ka_copy16_near(dsts, at(sb, tok, 2 * kKv4Scales));
+      } else {
+        const uint32_t safe = ok ? tok : 0;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const uint32_t t = __shfl_sync(0xFFFFFFFFu, safe, tl + 8 * h);
+          const bool val = mask >> (tl + 8 * h) & 1u;
+          ka_copy16(dst + h * 8 * kKv4Row, at(k, t, kKv4Row), val);
+          ka_copy16(dst + h * 8 * kKv4Row + kKaOffV, at(v, t, kKv4Row), val);
+        }
+        ka_copy16(dsts, at(sb, safe, 2 * kKv4Scales), ok);
       }
-      const uint8_t* stk = at(reinterpret_cast<const uint8_t*>(s), safe, 2 * kKv4Scales);
-      if (mask == 0xFFFFFFFFu)
-        ka_copy16_near(dsts, stk);
-      else
-        ka_copy16(dsts, stk, ok);
       if (lane == 0) sts32(stage + kKaOffMask, mask);
     } else if (left >= kKaTile) {
 #pragma unroll
@@ -758,6 +759,7 @@ __device__ __forceinline__ void ka_write(const KaArgs& a, int64_t bq, int j, flo
 template <int G, bool GATHER>
 __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
+  kv4_wait_prior();
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), CS = (int)cl.num_blocks();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1046,7 +1048,7 @@ __global__ void __launch_bounds__(32 * kKaJoinWarps) kv4_join_kernel(const KaArg
   __shared__ float4 so[kKaJoinWarps][32];
   __shared__ float2 sml[kKaJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // for the end of the streaming kernel
+  kv4_wait_prior();  // the streaming kernel
   const int64_t pairs = a.rows * G;
   for (int64_t base = (int64_t)blockIdx.x * run; base < pairs; base += (int64_t)gridDim.x * run) {
     const int64_t mine = base + warp;
@@ -1126,44 +1128,20 @@ int ka_launch(const KaArgs& a, int64_t most, cudaStream_t st) {
     auto kern = kv4_stream_kernel<G, GATHER>;
     if (int rc = set_smem_limit((const void*)kern, bytes, "kv4 attend")) return rc;
     const int grid = (int)imin64(2 * device_sm_count(), kKaMaxWarps / kKaWarps);
+    // (launched early like the others it was no faster, and 3 % slower on long rows)
     kern<<<grid, kKaThreads, bytes, st>>>(a);
-    // launched while the streaming kernel still runs (its CTAs leave no room until they
-    // end), and waiting for it on the device
-    cudaLaunchConfig_t join = {};
+    note_launches(1);
+    if (int rc = check_launch("kv4 attend")) return rc;
     const int64_t pairs = a.rows * G, ctas = 2 * device_sm_count();
     const int run = (int)imin64((pairs + ctas - 1) / ctas, kKaJoinWarps);
-    join.gridDim = dim3((unsigned)imin64((pairs + run - 1) / run, 8 * ctas), 1, 1);
-    join.blockDim = dim3(32 * kKaJoinWarps, 1, 1);
-    join.stream = st;
-    cudaLaunchAttribute early[1];
-    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early[0].val.programmaticStreamSerializationAllowed = 1;
-    join.attrs = early;
-    join.numAttrs = 1;
-    if (int rc = check_launch("kv4 attend")) return rc;
-    if (cudaLaunchKernelEx(&join, kv4_join_kernel<G>, a, run) != cudaSuccess)
-      return check_launch("kv4 attend join");
-    note_launches(2);
-    return check_launch("kv4 attend");
+    const dim3 jgrid((unsigned)imin64((pairs + run - 1) / run, 8 * ctas));
+    return kv4_launch("kv4 attend join", kv4_join_kernel<G>, jgrid, 32 * kKaJoinWarps, 0, 0, st, a,
+                      run);
   }
   const size_t bytes = (size_t)kKaWarps * kKaRing<G>;
   auto kern = kv4_cluster_kernel<G, GATHER>;
   if (int rc = set_smem_limit((const void*)kern, bytes, "kv4 attend")) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cs, (unsigned)a.rows, 1);
-  cfg.blockDim = dim3(kKaThreads, 1, 1);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return check_launch("kv4 attend");
-  note_launches(1);
-  return check_launch("kv4 attend");
+  return kv4_launch("kv4 attend", kern, dim3(cs, (unsigned)a.rows), kKaThreads, bytes, cs, st, a);
 }
 
 template <int G>
