@@ -650,7 +650,9 @@ int sd_device_status(void* stream);
  * thread-block clusters cannot be co-resident or bulk copies do not apply: the
  * split-n gather-attend with workspace partials, the sampled-threshold
  * sample/filter/finish top-k, the one-CTA word-maxima top-k, sd_select_attend
- * as its two calls, and the cp.async bit-plane scan.  Results are the same.
+ * as its two calls, and the cp.async bit-plane scan; sd_kv4_attend and
+ * sd_kv4_gather_attend take their streaming kernel at every size.  Results are the
+ * same.
  * Returns the previous setting.
  */
 int sd_set_fallback_paths(int on);

@@ -31,11 +31,12 @@
 // instructions (G <= 4; 360 with G = 8), half of them integer operations that issue every
 // second cycle: ~88 to take the codes apart, 64 to scale and centre them, 16 (24) MMAs of
 // 8.4 cycles.  It runs at ~420 cycles (G <= 4).  Measured (GB300): 8 KV heads of 1,048,576
-// tokens, G = 4: 205 us, 5.9 TB/s, 87 % of the copy rate; 512 of 16,384, G = 8: 246 us, 4.9
-// TB/s.  Tried and slower: six warps a CTA (their 168 registers spill; 210 us), scores of
-// the next tile beside the values of this one (219 us), e4m3 MMAs for the scores
-// (converted to f16 by the compiler on this GPU; 284 us), subnormal codes without the
-// multiplication (216 us, but outputs off by up to 1e-2 of themselves).
+// tokens, G = 4: 200 us, 6.0 TB/s, 89 % of the copy rate; 512 of 16,384, G = 8: 242 us, 5.0
+// TB/s.  Tried on the former and slower: six warps a CTA (their 168 registers spill; 5 us
+// more), scores of the next tile beside the values of this one (14), e4m3 MMAs for the
+// scores (converted to f16 by the compiler on this GPU; 35).  Subnormal codes without the
+// multiplication and one running sum on the tensor cores were no faster and took outputs
+// off by up to 1e-2 of themselves.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -56,8 +57,8 @@ constexpr int kKaOffMask = kKaOffS + kKaTile * 2 * kKv4Scales;
 constexpr int kKaOffQ = kKaOffMask + 16;  // the row's queries, where the tile is its first
 template <int G>
 constexpr int kKaStage = kKaOffQ + G * kD * 2;
-// Tiles in a warp's ring (G = 4: 204 us with 3 and 211 with 4 on the longest case above, G
-// = 8: 257 and 252).
+// Tiles in a warp's ring (G = 4: 204 us with 3 when it was 211 with 4, on the longest case
+// above; G = 8: 257 and 252).
 template <int G>
 constexpr int kKaDepth = G == 8 ? 4 : 3;
 template <int G>
