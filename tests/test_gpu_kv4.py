@@ -657,3 +657,65 @@ def test_fallback_switch(sd):
         finally:
             sd.sd_set_fallback_paths(before)
         kv.check(out, lse, ref)
+
+
+def test_order_after_other_work(sd):
+    """Each call follows what its stream holds before it: copies (as memcpy and as kernels),
+    an event of another stream, its own kernels; eagerly and captured, with inputs that
+    change from pass to pass."""
+    rng = np.random.default_rng(43)
+    B, h, G, n = 4, 4, 4, 700
+    shp = sd.make_shape(B, h * G, h, n)
+    src = [dev(kv.tokens(rng, (2, B, h, n))) for _ in range(3)]
+    q = kv.tokens(rng, (B, h * G), spread=False)
+    dq = dev(q)
+    want = []
+    for x in src:
+        b = host(x, np.uint16)
+        k, v, rec = kv.encode(b[0], b[1])
+        want.append((kv.read(k, rec[..., :4]), kv.attend(q, k, v, rec, ranges(B, h, n, None, None),
+                                                         SCALE)))
+    c = sd.Kv4Cache(B, h, n)
+    X = torch.zeros_like(src[0])
+    K2, V2 = torch.zeros_like(X[0]), torch.zeros_like(X[0])
+    out, lse = torch.zeros((B, h * G, 128), device="cuda"), torch.zeros((B, h * G), device="cuda")
+    ws = torch.empty(sd.sd_kv4_attend_workspace_size(shp), dtype=torch.uint8, device="cuda")
+
+    def work():
+        sd.sd_kv4_write(shp, c, X[0], X[1], n)
+        sd.sd_kv4_read(shp, c, K2, V2, n)
+        sd.sd_kv4_attend(shp, dq, c, SCALE, out, lse, ws)
+
+    def check(i):
+        torch.cuda.synchronize()
+        assert same_bits(host(K2, np.uint16), want[i][0]), i
+        kv.check(host(out, np.float32), host(lse, np.float32), want[i][1])
+
+    side = torch.cuda.Stream()
+    for i in (0, 1, 2, 1):
+        torch.cuda._sleep(200000)
+        X.copy_(src[i])                      # a device copy
+        work()
+        check(i)
+        torch.cuda._sleep(200000)
+        torch.add(src[i], 0, out=X)          # a kernel
+        work()
+        check(i)
+        X.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400000)
+            X.copy_(src[i])
+        torch.cuda.current_stream().wait_stream(side)
+        work()
+        check(i)
+    feed = src[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        X.copy_(feed)
+        work()
+    for i in (2, 0, 1):
+        feed.copy_(src[i])
+        graph.replay()
+        graph.replay()
+        check(i)

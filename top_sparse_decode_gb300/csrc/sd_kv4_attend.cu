@@ -66,7 +66,7 @@ constexpr int kKaRing = kKaDepth<G> * kKaStage<G>;
 constexpr float kKaLog2e = 1.4426950408889634f;
 constexpr float kKaLn2 = 0.6931471805599453f;
 constexpr float kKaEmpty = -3e38f;   // m before the first token
-constexpr float kKaPMax = 512.0f;    // a lane's largest sum of four p that leaves m as it is
+constexpr float kKaPMax = 512.0f;    // largest sum of a lane's p that leaves m as it is
 constexpr float kKaWMax = 16384.0f;  // largest w that leaves f as it is (0x7400 in f16)
 constexpr float kKaF0 = 1.2676506e30f;  // 2^100: f before the first token, and its limit
 
