@@ -1000,34 +1000,34 @@ __global__ void __launch_bounds__(kKaThreads, 2) kv4_stream_kernel(const KaArgs 
 
 // Partials i0, i0 + step, .. of the np of one head of a row whose first warp is `first`:
 // their sum over the lanes' four channels each, and (m, l).
-template <int G>
+template <int G, int FLIGHT>
 __device__ __forceinline__ float4 ka_gather_parts(const KaArgs& a, int first, int np, int g, int i0,
                                                   int step, int lane, float& top, float& l) {
   auto at = [&](int i) { return (2 * ((int64_t)first + i) + (i == 0 ? 1 : 0)) * G + g; };
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   top = kKaEmpty;
   l = 0.0f;
-  for (; i0 < np; i0 += 8 * step) {  // eight partials in flight
-    float2 ml[8];
-    float4 v[8];
-    float t8 = top;
+  for (; i0 < np; i0 += FLIGHT * step) {  // so many partials in flight
+    float2 ml[FLIGHT];
+    float4 v[FLIGHT];
+    float tb = top;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < FLIGHT; ++k) {
       const int i = i0 + step * k;
       ml[k] = i < np ? a.part_ml[at(i)] : make_float2(kKaEmpty, 0.0f);
       v[k] = i < np ? reinterpret_cast<const float4*>(a.part_o + at(i) * kD)[lane]
                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      t8 = fmaxf(t8, ml[k].x);
+      tb = fmaxf(tb, ml[k].x);
     }
-    const float f0 = exp2f(top - t8);
-    top = t8;
+    const float f0 = exp2f(top - tb);
+    top = tb;
     l *= f0;
     o.x *= f0;
     o.y *= f0;
     o.z *= f0;
     o.w *= f0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < FLIGHT; ++k) {
       const float f = ka_weight(ml[k], top);
       l = fmaf(ml[k].y, f, l);
       o.x = fmaf(v[k].x, f, o.x);
@@ -1044,7 +1044,10 @@ __device__ __forceinline__ float4 ka_gather_parts(const KaArgs& a, int first, in
 constexpr int kKaJoinWarps = 16;
 constexpr int kKaAlone = 16;
 
-template <int G>
+// FLIGHT: partials that a warp of the latter has in flight.  16 for a few heads (1 us less
+// where 8 rows of 32,768 tokens take 18.5); 8, in 64 registers, for many, whose CTAs then
+// fit beside the last of the streaming kernel's (with 73 they start 2 us later).
+template <int G, int FLIGHT>
 __global__ void __launch_bounds__(32 * kKaJoinWarps) kv4_join_kernel(const KaArgs a, int run) {
   __shared__ float4 so[kKaJoinWarps][32];
   __shared__ float2 sml[kKaJoinWarps];
@@ -1061,7 +1064,7 @@ __global__ void __launch_bounds__(32 * kKaJoinWarps) kv4_join_kernel(const KaArg
       wide = mt.y > kKaAlone;
       if (mt.y > 0 && !wide) {
         float top, l;
-        const float4 o = ka_gather_parts<G>(a, mt.x, mt.y, g, 0, 1, lane, top, l);
+        const float4 o = ka_gather_parts<G, 8>(a, mt.x, mt.y, g, 0, 1, lane, top, l);
         const int64_t bq = (row / a.Hkv) * a.Hq + (row % a.Hkv) * G + g;
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         reinterpret_cast<float4*>(a.out + bq * kD)[lane] =
@@ -1076,7 +1079,7 @@ __global__ void __launch_bounds__(32 * kKaJoinWarps) kv4_join_kernel(const KaArg
       const int2 mt = a.meta[row];
       if (mt.y <= kKaAlone) continue;  // uniform over the CTA
       float top, l;
-      so[warp][lane] = ka_gather_parts<G>(a, mt.x, mt.y, g, warp, kKaJoinWarps, lane, top, l);
+      so[warp][lane] = ka_gather_parts<G, FLIGHT>(a, mt.x, mt.y, g, warp, kKaJoinWarps, lane, top, l);
       if (lane == 0) sml[warp] = make_float2(top, l);
       __syncthreads();
       if (threadIdx.x < kD) {
@@ -1136,8 +1139,8 @@ int ka_launch(const KaArgs& a, int64_t most, cudaStream_t st) {
     const int64_t pairs = a.rows * G, ctas = 2 * device_sm_count();
     const int run = (int)imin64((pairs + ctas - 1) / ctas, kKaJoinWarps);
     const dim3 jgrid((unsigned)imin64((pairs + run - 1) / run, 8 * ctas));
-    return kv4_launch("kv4 attend join", kv4_join_kernel<G>, jgrid, 32 * kKaJoinWarps, 0, 0, st, a,
-                      run);
+    auto join = pairs <= device_sm_count() ? kv4_join_kernel<G, 16> : kv4_join_kernel<G, 8>;
+    return kv4_launch("kv4 attend join", join, jgrid, 32 * kKaJoinWarps, 0, 0, st, a, run);
   }
   const size_t bytes = (size_t)kKaWarps * kKaRing<G>;
   auto kern = kv4_cluster_kernel<G, GATHER>;
