@@ -134,3 +134,34 @@ def test_binding_refusals(sd):
             sd.sd_kv4_write(shp, cache, bad, K, 8, stream=0)
         with pytest.raises(ValueError):
             sd.sd_kv4_read(shp, cache, K, bad, 8, stream=0)
+
+
+def test_binding_refuses_a_shape_beside_the_cache(sd):
+    torch = pytest.importorskip("torch")
+    cache = sd.Kv4Cache(2, 2, 64, device="cpu")
+    K = torch.zeros((2, 2, 8, 128), dtype=torch.bfloat16)
+    i = torch.zeros(64, dtype=torch.int32)
+    for dims in ((3, 4, 2, 64), (2, 4, 1, 64), (2, 4, 4, 64), (2, 4, 2, 63), (2, 4, 2, 128),
+                 (2, 4, 2, 64, 128, 65)):
+        shp = sd.make_shape(*dims)
+        rows = K.new_zeros((dims[0], dims[2], 8, 128))
+        for call in (lambda: sd.sd_kv4_write(shp, cache, rows, rows, 8, stream=0),
+                     lambda: sd.sd_kv4_read(shp, cache, rows, rows, 8, stream=0),
+                     lambda: sd.sd_kv4_attend(shp, K, cache, 0.1, K, stream=0),
+                     lambda: sd.sd_kv4_gather_attend(shp, K, cache, i, 64, i, 64, 0.1, K,
+                                                     stream=0)):
+            with pytest.raises(ValueError, match="do not address"):
+                call()
+    # fewer sequences, and fewer tokens of the same capacity, are addressed (nothing to move)
+    for dims in ((1, 4, 2, 64), (2, 4, 2, 60, 128, 64)):
+        shp = sd.make_shape(*dims)
+        sd.sd_kv4_write(shp, cache, K[:dims[0]], K[:dims[0]], 0, stream=0)
+
+
+def test_binding_refuses_wide_rows(sd):
+    torch = pytest.importorskip("torch")
+    cache = sd.Kv4Cache(1, 2, 64, device="cpu")
+    K = torch.zeros((1, 2, 8, 128))
+    for fn in (sd.sd_kv4_write, sd.sd_kv4_read):
+        with pytest.raises(ValueError, match="bf16"):
+            fn(sd.make_shape(1, 2, 2, 64), cache, K, K, 8, stream=0)

@@ -251,7 +251,17 @@ class Kv4Cache:
         for t, nbytes in ((self.k, 64), (self.v, 64), (self.scale, 16)):
             if t.numel() * t.element_size() != batch * hkv * n_cap * nbytes:
                 raise ValueError("Kv4Cache: an array's size does not match batch, hkv, n_cap")
+        self.dims = dims
         self.c = _abi.SdKv4(_ptr(self.k), _ptr(self.v), _ptr(self.scale))
+
+
+def _kv4(shape: SdShape, cache: Kv4Cache):
+    """The cache's sd_kv4, if the shape addresses it: its first `batch` sequences."""
+    b, h, n_cap = cache.dims
+    if shape.batch > b or shape.hkv != h or (shape.n_cap or shape.n) != n_cap:
+        raise ValueError(f"the shape's batch, hkv, n_cap {shape.batch}, {shape.hkv}, "
+                         f"{shape.n_cap or shape.n} do not address a cache of {cache.dims}")
+    return ctypes.byref(cache.c)
 
 
 def _rows(t, shape: SdShape, m: int):
@@ -264,22 +274,22 @@ def _rows(t, shape: SdShape, m: int):
         raise ValueError(f"expected [{shape.batch}][{shape.hkv}][>= {m}][{shape.d}] rows, "
                          f"got {tuple(t.shape)}")
     sb, sh, st, sd_ = t.stride()
-    if sd_ != 1:
-        raise ValueError("libsd takes rows of consecutive channels")
+    if sd_ != 1 or t.element_size() != 2:
+        raise ValueError("libsd takes bf16 rows of consecutive channels")
     return t.data_ptr(), ctypes.byref(_abi.SdStrides(sb, sh, st))
 
 
 def sd_kv4_write(shape: SdShape, cache: Kv4Cache, K, V, m: int, pos=None, length=None,
                  first: int = 0, stream=None) -> None:
     (k, ks), (v, vs) = _rows(K, shape, m), _rows(V, shape, m)
-    _check(lib().sd_kv4_write(ctypes.byref(shape), ctypes.byref(cache.c), k, ks, v, vs, m, first,
+    _check(lib().sd_kv4_write(ctypes.byref(shape), _kv4(shape, cache), k, ks, v, vs, m, first,
                               _ptr(pos), _ptr(length), _stream(stream)), "sd_kv4_write")
 
 
 def sd_kv4_read(shape: SdShape, cache: Kv4Cache, K, V, m: int, pos=None, length=None,
                 first: int = 0, stream=None) -> None:
     (k, ks), (v, vs) = _rows(K, shape, m), _rows(V, shape, m)
-    _check(lib().sd_kv4_read(ctypes.byref(shape), ctypes.byref(cache.c), k, ks, v, vs, m, first,
+    _check(lib().sd_kv4_read(ctypes.byref(shape), _kv4(shape, cache), k, ks, v, vs, m, first,
                              _ptr(pos), _ptr(length), _stream(stream)), "sd_kv4_read")
 
 
@@ -290,7 +300,7 @@ def sd_kv4_attend_workspace_size(shape: SdShape) -> int:
 def sd_kv4_attend(shape: SdShape, q, cache: Kv4Cache, scale: float, out, lse=None, workspace=None,
                   begin=None, end=None, stream=None) -> None:
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().sd_kv4_attend(ctypes.byref(shape), _ptr(q), ctypes.byref(cache.c), _ptr(begin),
+    _check(lib().sd_kv4_attend(ctypes.byref(shape), _ptr(q), _kv4(shape, cache), _ptr(begin),
                                _ptr(end), float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
                                ws_bytes, _stream(stream)), "sd_kv4_attend")
 
@@ -303,7 +313,7 @@ def sd_kv4_gather_attend(shape: SdShape, q, cache: Kv4Cache, idx, idx_stride: in
                          max_count: int, scale: float, out, lse=None, workspace=None,
                          stream=None) -> None:
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().sd_kv4_gather_attend(ctypes.byref(shape), _ptr(q), ctypes.byref(cache.c),
+    _check(lib().sd_kv4_gather_attend(ctypes.byref(shape), _ptr(q), _kv4(shape, cache),
                                       _ptr(idx), idx_stride, _ptr(count), max_count,
                                       float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
                                       ws_bytes, _stream(stream)), "sd_kv4_gather_attend")
