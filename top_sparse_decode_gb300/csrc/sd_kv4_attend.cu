@@ -34,9 +34,11 @@
 // tokens, G = 4: 200 us, 6.0 TB/s, 89 % of the copy rate; 512 of 16,384, G = 8: 242 us, 5.0
 // TB/s.  Tried on the former and slower: six warps a CTA (their 168 registers spill; 5 us
 // more), scores of the next tile beside the values of this one (14), e4m3 MMAs for the
-// scores (converted to f16 by the compiler on this GPU; 35).  Subnormal codes without the
-// multiplication and one running sum on the tensor cores were no faster and took outputs
-// off by up to 1e-2 of themselves.
+// scores (converted to f16 by the compiler on this GPU; 35), the upper codes of a word taken
+// down by an integer multiplication instead of a shift (24), three CTAs an SM with scale
+// records read twice to save registers (10).  Subnormal codes without the multiplication and
+// one running sum on the tensor cores were no faster and took outputs off by up to 1e-2 of
+// themselves.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
