@@ -55,12 +55,15 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
-// What a lane moves: its half (0: K, 1: V), octet and row, and the tokens [t0, t1) of the
-// row that have a place in the cache.
+// What a lane moves: its half (0: K, 1: V), octet and row, and the `count` tokens of the
+// row that have a place in the cache, numbered from the first of them (tokens that are
+// dropped before it cost nothing).  Both are unsigned and a step is taken only where it
+// stays below count, so that no sum wraps however long the call.
 struct KvLane {
-  int half, l, t, t0, t1;
-  int64_t row, tok;  // tok: token 0's place among the cache's tokens
-  int64_t x;         // offset of token 0's octet in the caller's array
+  int half, l;
+  unsigned t, count;
+  int64_t row, tok;  // tok: the first one's place among the cache's tokens
+  int64_t x;         // offset of its octet in the caller's array
   __device__ __forceinline__ KvLane(const KvMoveArgs& a) {
     const int lane = threadIdx.x & 31;
     half = lane >> 4;
@@ -70,14 +73,12 @@ struct KvLane {
     int64_t len, p0;
     kv_range(a, b, len, p0);
     t = blockIdx.x * kKvStep + (threadIdx.x >> 5) * kKvRun;
-    t0 = (int)imin64(imax64(0, -p0), a.m);
-    t1 = (int)imax64(t0, imin64(len, a.n - p0));
-    tok = row * a.ncap + p0;
-    x = b * a.sb[half] + h * a.sh[half] + 8 * l;
+    const int64_t t0 = imin64(imax64(0, -p0), a.m);
+    count = (unsigned)imax64(0, imin64(len, a.n - p0) - t0);
+    tok = row * a.ncap + p0 + t0;
+    x = b * a.sb[half] + h * a.sh[half] + t0 * a.st[half] + 8 * l;
   }
-  __device__ __forceinline__ bool in(int i) const {
-    return (unsigned)(i - t0) < (unsigned)(t1 - t0);
-  }
+  __device__ __forceinline__ bool in(unsigned i) const { return i < count; }
 };
 
 __global__ void __launch_bounds__(32 * kKvWarps) kv4_write_kernel(const KvMoveArgs a) {
@@ -91,20 +92,21 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv4_write_kernel(const KvMoveAr
   uint32_t* scale = reinterpret_cast<uint32_t*>(a.scale + (L.tok + L.t) * kKv4Scales) +
                     2 * L.half + (L.l >> 3);
   uint4 next[kKvRun];
-  auto fetch = [&](int t) {
+  auto fetch = [&](unsigned t) {
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k)
       next[k] = asked && L.in(t + k) ? __ldcs(reinterpret_cast<const uint4*>(src + k * st))
                                      : make_uint4(0u, 0u, 0u, 0u);
   };
-  const int step = gridDim.x * kKvStep;
+  const unsigned step = gridDim.x * kKvStep;
   fetch(L.t);
-  for (int t = L.t; t < L.t1; t += step) {  // the same for both halves
+  for (unsigned t = L.t, left; t < L.count; t = left > step ? t + step : L.count) {
+    left = L.count - t;  // the same for both halves
     uint4 cur[kKvRun];
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k) cur[k] = next[k];
     src += step * st;
-    if (t < L.t1 - step) fetch(t + step);
+    if (left > step) fetch(t + step);
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k) {
       const uint4 w = cur[k];
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv4_read_kernel(const KvMoveArg
       (L.l >> 3);
   if (!a.x[L.half]) return;  // whole half-warps, which work alone
   uint32_t nw[kKvRun], ns[kKvRun];
-  auto fetch = [&](int t) {
+  auto fetch = [&](unsigned t) {
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k) {
       const bool ok = L.in(t + k);
@@ -152,9 +154,10 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv4_read_kernel(const KvMoveArg
       ns[k] = ok ? __ldcs(scale + k * (kKv4Scales / 2)) : 0u;
     }
   };
-  const int step = gridDim.x * kKvStep;
+  const unsigned step = gridDim.x * kKvStep;
   fetch(L.t);
-  for (int t = L.t; t < L.t1; t += step) {
+  for (unsigned t = L.t, left; t < L.count; t = left > step ? t + step : L.count) {
+    left = L.count - t;
     uint32_t cw[kKvRun], cs[kKvRun];
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k) {
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv4_read_kernel(const KvMoveArg
     }
     code += (int64_t)step * (kKv4Row / 4);
     scale += (int64_t)step * (kKv4Scales / 2);
-    if (t < L.t1 - step) fetch(t + step);
+    if (left > step) fetch(t + step);
 #pragma unroll
     for (int k = 0; k < kKvRun; ++k) {
       if (!L.in(t + k)) continue;
