@@ -1,5 +1,5 @@
 """GPU tests of the 4-bit K/V cache beyond the ordinary sizes and values: calls that are longer
-than the cache."""
+than the cache, values at the ends of their range with the bounds of _kv4_bounds.py."""
 import math
 
 import numpy as np
@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import _kv4 as kv
+import _kv4_bounds as kb
 from _helpers import dev, host
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +65,64 @@ def test_read_in_front_of_the_cache(sd):
     assert bool((out[:, :, :, :m - 7] == 7.0).all())
     for i, x in enumerate((kv.read(k, rec[..., :4]), kv.read(v, rec[..., 4:]))):
         assert np.array_equal(bits(out[i, 0, 0, m - 7:]), x[0, 0, :7])
+
+
+@pytest.fixture(params=[False, True], ids=["chosen", "stream"])
+def path(sd, request):
+    """The kernel the library chooses, then the streaming one for every size."""
+    before = sd.sd_set_fallback_paths(request.param)
+    yield
+    sd.sd_set_fallback_paths(before)
+
+
+def attend_both(sd, q, k, v, rec, scale):
+    """Dense attention and attention over all tokens listed in turn: [(out, lse)] x 2."""
+    B, h, n = k.shape[:3]
+    hq = q.shape[1]
+    shp = sd.make_shape(B, hq, h, n)
+    c = sd.Kv4Cache(B, h, n, k=dev(k), v=dev(v), scale=dev(rec))
+    ws = torch.full((max(sd.sd_kv4_attend_workspace_size(shp),
+                         sd.sd_kv4_gather_attend_workspace_size(shp, n)),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    idx = dev(np.tile(np.arange(n, dtype=np.int32), (B * h, 1)))
+    cnt = dev(np.full(B * h, n, np.int32))
+    res = []
+    for gather in (False, True):
+        out = torch.full((B, hq, 128), 9.0, device="cuda")
+        lse = torch.full((B, hq), 9.0, device="cuda")
+        if gather:
+            sd.sd_kv4_gather_attend(shp, dev(q), c, idx, n, cnt, n, scale, out, lse, ws)
+        else:
+            sd.sd_kv4_attend(shp, dev(q), c, scale, out, lse, ws)
+        torch.cuda.synchronize()
+        res.append((host(out, np.float32), host(lse, np.float32)))
+    return res
+
+
+def check_both(sd, q, k, v, rec, scale, tight=2.0 ** -8):
+    B, h, n = k.shape[:3]
+    ref = kb.attend(q, k, v, rec, [np.arange(n)] * (B * h), scale)
+    for out, lse in attend_both(sd, q, k, v, rec, scale):
+        kb.check(out, lse, ref, tight)
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("below", [20, 60, 83, 300])
+@pytest.mark.parametrize("wide", [1e10, 1e30, 1e38])
+def test_wide_values_of_little_weight(sd, path, G, below, wide):
+    """A group of values that is constant in every token, but for one token of a wide range
+    whose logit is far below the others': first, in the middle, last, or the only one of its
+    tile's second half.  What it adds is tiny or 0, and never NaN."""
+    rng = np.random.default_rng(int(below) + G)
+    B, h, n = 5, 1, 333
+    qf = rng.standard_normal((B, 1, 128)) + 0.05 * rng.standard_normal((B, h * G, 128))
+    K = 0.3 * rng.standard_normal((B, h, n, 128))
+    V = rng.standard_normal((B, h, n, 128))
+    V[:, :, :, 64:] = np.array([0, 2.5, 0, -1, 0]).reshape(B, 1, 1, 1)
+    for b, at in enumerate((0, 100, n - 1, 20, 31)):
+        base = qf[b].mean(0)
+        K[b, :, at] = -below / SCALE / (base @ base) * base
+        V[b, :, at] = rng.uniform(-1, 1, 128) * wide
+    q = kv.bf16_bits(qf.astype(np.float32))
+    k, v, rec = kv.encode(kv.bf16_bits(K.astype(np.float32)), kv.bf16_bits(V.astype(np.float32)))
+    check_both(sd, q, k, v, rec, SCALE, tight=2.0 ** -6)

@@ -537,13 +537,20 @@ __device__ __forceinline__ void ka_weights(KaP& P, KaState& S, const KaScores<G>
   };
   weights(0);
   weights(1);
+  // w = (p f) s, in this order: p f is at most 2^109, where s f would be infinite for a wide
+  // step while f stands at its start, and p = 0 or a small w would become NaN.  p f below
+  // the normal range takes at most 2^-26 from a w.
+  float pf[NR][2][2];  // [token][group][column]
   uint32_t hi[NR][2];  // w's high parts, a pair of columns each
   auto weigh = [&]() {
 #pragma unroll
     for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
-        hi[i][g] = ka_pack(p[i][0] * (sv[i][g] * S.f[0][g]), p[i][1] * (sv[i][g] * S.f[1][g]));
+      for (int g = 0; g < 2; ++g) {
+        pf[i][g][0] = p[i][0] * S.f[0][g];
+        pf[i][g][1] = p[i][1] * S.f[1][g];
+        hi[i][g] = ka_pack(pf[i][g][0] * sv[i][g], pf[i][g][1] * sv[i][g]);
+      }
   };
   weigh();
   __half2 ht = *reinterpret_cast<__half2*>(&hi[0][0]);
@@ -585,8 +592,8 @@ __device__ __forceinline__ void ka_weights(KaP& P, KaState& S, const KaScores<G>
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const float2 h2 = __half22float2(*reinterpret_cast<const __half2*>(&hi[i][g]));
-      const uint32_t lo = ka_pack(fmaf(p[i][0], sv[i][g] * S.f[0][g], -h2.x),
-                                  fmaf(p[i][1], sv[i][g] * S.f[1][g], -h2.y));
+      const uint32_t lo = ka_pack(fmaf(pf[i][g][0], sv[i][g], -h2.x),
+                                  fmaf(pf[i][g][1], sv[i][g], -h2.y));
       if constexpr (G == 8) {
         P.h[i >> 1][g][i & 1] = transpose_8x8(hi[i][g]);
         P.l[i >> 1][g][i & 1] = transpose_8x8(lo);
