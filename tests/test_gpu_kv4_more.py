@@ -126,3 +126,18 @@ def test_wide_values_of_little_weight(sd, path, G, below, wide):
     q = kv.bf16_bits(qf.astype(np.float32))
     k, v, rec = kv.encode(kv.bf16_bits(K.astype(np.float32)), kv.bf16_bits(V.astype(np.float32)))
     check_both(sd, q, k, v, rec, SCALE, tight=2.0 ** -6)
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("wide", [100, 113, 120, 126])
+def test_wide_keys(sd, path, G, wide):
+    """Keys of a range of 2^wide, tiny queries and a small scale: ordinary logits of factors
+    whose products in another order pass the fp32 range."""
+    rng = np.random.default_rng(wide + G)
+    B, h, n = 2, 2, 333
+    qf = rng.uniform(-1, 1, (B, h * G, 128)) * 2.0 ** (27 - wide)
+    K = rng.uniform(-1, 1, (B, h, n, 128)) * 2.0 ** wide
+    V = rng.standard_normal((B, h, n, 128))
+    q = kv.bf16_bits(qf.astype(np.float32))
+    k, v, rec = kv.encode(kv.bf16_bits(K.astype(np.float32)), kv.bf16_bits(V.astype(np.float32)))
+    check_both(sd, q, k, v, rec, SCALE * 2.0 ** -24, tight=2.0 ** -6)

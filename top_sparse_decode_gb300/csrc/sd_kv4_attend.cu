@@ -501,12 +501,14 @@ __device__ __forceinline__ void ka_weights(KaP& P, KaState& S, const KaScores<G>
   const int gid = lane >> 2, tig = lane & 3;
   const int side = G == 8 ? 0 : tig >> 1;  // G <= 4: the half of this lane's tokens
   const int tk = ka_tau(gid);
-  float dot[NR][2], mk[NR][2], sv[NR][2], mv[NR][2];  // [token][column or group]
+  float cq[NR][2][2];  // [token][column][group]: scale log2(e) sum of q c
+  float sk[NR][2], mk[NR][2], sv[NR][2], mv[NR][2];  // [token][group]
   auto token = [&](int i) { return (G == 8 ? 16 * (i >> 1) : 16 * side) + tk + 8 * (i & 1); };
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const uint4 sc = lds128(st + kKaOffS + token(i) * 16);
-    const float sk0 = bf16_lo(sc.x), sk1 = bf16_lo(sc.y);
+    sk[i][0] = bf16_lo(sc.x);
+    sk[i][1] = bf16_lo(sc.y);
     mk[i][0] = bf16_hi(sc.x);
     mk[i][1] = bf16_hi(sc.y);
     sv[i][0] = bf16_lo(sc.z);
@@ -514,13 +516,18 @@ __device__ __forceinline__ void ka_weights(KaP& P, KaState& S, const KaScores<G>
     mv[i][0] = fmaf(7.5f, sv[i][0], bf16_hi(sc.z));  // the middle of the group's range
     mv[i][1] = fmaf(7.5f, sv[i][1], bf16_hi(sc.w));
     const float(&ac)[2][4] = C.c[i >> 1];
+    // out of q's f16 units before the step comes in: a step is up to 2^124, and its product
+    // with a sum in those units (up to 2^16) could pass the fp32 range where a logit does not
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      dot[i][e] = fmaf(sk1, ac[1][2 * (i & 1) + e], sk0 * ac[0][2 * (i & 1) + e]);
+    for (int g = 0; g < 2; ++g)
+      f2_split(f2_mul(f2_make(ac[g][2 * (i & 1)], ac[g][2 * (i & 1) + 1]),
+                      f2_make(Q.ch[0], Q.ch[1])),
+               cq[i][0][g], cq[i][1][g]);
   }
   // log2 of the weight over 2^sub
   auto logit = [&](int i, int e, float sub) {
-    return fmaf(dot[i][e], Q.ch[e], fmaf(mk[i][1], Q.qs[e][1], fmaf(mk[i][0], Q.qs[e][0], -sub)));
+    const float base = fmaf(mk[i][1], Q.qs[e][1], fmaf(mk[i][0], Q.qs[e][0], -sub));
+    return fmaf(sk[i][1], cq[i][e][1], fmaf(sk[i][0], cq[i][e][0], base));
   };
   auto ok = [&](int i) { return valid >> token(i) & 1u; };
   float p[NR][2], sum[2];
