@@ -1,5 +1,6 @@
 """GPU tests of the 4-bit K/V cache beyond the ordinary sizes and values: calls that are longer
-than the cache, values at the ends of their range with the bounds of _kv4_bounds.py."""
+than the cache, values at the ends of their range with the bounds of _kv4_bounds.py, ranges and
+selections that the kernel before writes."""
 import math
 
 import numpy as np
@@ -141,3 +142,61 @@ def test_wide_keys(sd, path, G, wide):
     q = kv.bf16_bits(qf.astype(np.float32))
     k, v, rec = kv.encode(kv.bf16_bits(K.astype(np.float32)), kv.bf16_bits(V.astype(np.float32)))
     check_both(sd, q, k, v, rec, SCALE * 2.0 ** -24, tight=2.0 ** -6)
+
+
+@pytest.mark.parametrize("n,mc", [(300, 64), (4096, 700)])
+def test_ranges_written_by_the_kernel_before(sd, n, mc):
+    """begin, end, count and idx come from the kernel just before the attention (at sizes that
+    take the cluster kernel, which starts while that one runs) and change from pass to pass;
+    eagerly and in a graph."""
+    rng = np.random.default_rng(n)
+    B, h, G = 3, 4, 4
+    shp = sd.make_shape(B, h * G, h, n)
+    q = kv.tokens(rng, (B, h * G), spread=False)
+    k, v, rec = kv.encode(kv.tokens(rng, (B, h, n)), kv.tokens(rng, (B, h, n)))
+    c = sd.Kv4Cache(B, h, n, k=dev(k), v=dev(v), scale=dev(rec))
+    passes = []
+    for _ in range(4):
+        begin = rng.integers(0, n // 2, B).astype(np.int32)
+        end = (begin + rng.integers(1, n // 2, B)).astype(np.int32)
+        idx = rng.integers(0, n, (B * h, mc)).astype(np.int32)
+        cnt = rng.integers(1, mc + 1, B * h).astype(np.int32)
+        dense = [np.arange(begin[b], end[b]) for b in range(B) for _ in range(h)]
+        passes.append(([dev(x) for x in (begin, end, idx, cnt)],
+                       kv.attend(q, k, v, rec, dense, SCALE),
+                       kv.attend(q, k, v, rec, [idx[r, :cnt[r]] for r in range(B * h)], SCALE)))
+    feed = [torch.zeros_like(x) for x in passes[0][0]]
+    now = [torch.zeros_like(x) for x in feed]
+    dq = dev(q)
+    outs = [torch.zeros((B, h * G, 128), device="cuda") for _ in range(2)]
+    lses = [torch.zeros((B, h * G), device="cuda") for _ in range(2)]
+    ws = torch.empty(max(sd.sd_kv4_attend_workspace_size(shp),
+                         sd.sd_kv4_gather_attend_workspace_size(shp, mc)), dtype=torch.uint8,
+                     device="cuda")
+
+    def work():
+        torch._foreach_copy_(now[:2], feed[:2])
+        sd.sd_kv4_attend(shp, dq, c, SCALE, outs[0], lses[0], ws, begin=now[0], end=now[1])
+        torch.add(feed[2], 0, out=now[2])
+        torch.add(feed[3], 0, out=now[3])
+        sd.sd_kv4_gather_attend(shp, dq, c, now[2], mc, now[3], mc, SCALE, outs[1], lses[1], ws)
+
+    def check(i):
+        torch.cuda.synchronize()
+        for j in range(2):
+            kv.check(host(outs[j], np.float32), host(lses[j], np.float32), passes[i][1 + j])
+
+    for i in (0, 1, 2, 3, 1):
+        for to, x in zip(feed, passes[i][0]):
+            to.copy_(x)
+        torch.cuda._sleep(200000)
+        work()
+        check(i)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for i in (2, 0, 3, 1):
+        for to, x in zip(feed, passes[i][0]):
+            to.copy_(x)
+        graph.replay()
+        check(i)

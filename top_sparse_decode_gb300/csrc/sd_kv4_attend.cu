@@ -96,15 +96,25 @@ struct KaArgs {
 struct KaRow {
   int t0, len;
 };
+// An ordinary load of a count, a range or an index: a kernel that is launched early lives
+// while the one before it may still write them, so a read-only load (of data that do not
+// change while its kernel lives) is not for them.  volatile keeps it behind the wait; the
+// compiler may move the others past it, as it may not past a plain load here (199 us; 203
+// with *p or __ldcg, 8 KV heads of 1,048,576 tokens).
+__device__ __forceinline__ int ka_load(const int32_t* p) {
+  int x;
+  asm volatile("ld.global.s32 %0, [%1];\n" : "=r"(x) : "l"(p));
+  return x;
+}
 template <bool GATHER>
 __device__ __forceinline__ KaRow ka_row(const KaArgs& a, int64_t row, int b) {
   KaRow r;
   if (GATHER) {
     r.t0 = 0;
-    r.len = max(min(__ldg(a.count + row), a.max_count), 0);
+    r.len = max(min(ka_load(a.count + row), a.max_count), 0);
   } else {
-    r.t0 = a.begin ? max(__ldg(a.begin + b), 0) : 0;
-    const int e = a.end ? min(__ldg(a.end + b), a.n) : a.n;
+    r.t0 = a.begin ? max(ka_load(a.begin + b), 0) : 0;
+    const int e = a.end ? min(ka_load(a.end + b), a.n) : a.n;
     r.len = e > r.t0 ? e - r.t0 : 0;
   }
   return r;
@@ -171,7 +181,7 @@ struct KaSrc {
   int left;                 // tokens of the row from the tile on
   int tok;                  // gathered: this lane's index, requested a tile ahead
   __device__ __forceinline__ void fetch(int lane) {
-    if (GATHER) tok = lane < left ? __ldg(idx) : -1;
+    if (GATHER) tok = lane < left ? ka_load(idx) : -1;
   }
   __device__ __forceinline__ void set(const KaArgs& a, int64_t row, const KaRow& r, int tile,
                                       int lane) {
