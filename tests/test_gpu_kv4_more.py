@@ -1,7 +1,10 @@
 """GPU tests of the 4-bit K/V cache beyond the ordinary sizes and values: calls that are longer
 than the cache, values at the ends of their range with the bounds of _kv4_bounds.py, ranges and
-selections that the kernel before writes."""
+selections that the kernel before writes, calls captured first."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -200,3 +203,35 @@ def test_ranges_written_by_the_kernel_before(sd, n, mc):
             to.copy_(x)
         graph.replay()
         check(i)
+
+
+FIRST = """
+import torch, top_sparse_decode_gb300 as sd
+B, h, G, n = 2, 2, 4, {n}
+shp, c = sd.make_shape(B, h * G, h, n), sd.Kv4Cache(B, h, n)
+x = torch.randn((B, h, n, 128), device="cuda").bfloat16()
+q = torch.randn((B, h * G, 128), device="cuda").bfloat16()
+out, lse = torch.zeros((B, h * G, 128), device="cuda"), torch.zeros((B, h * G), device="cuda")
+ws = torch.empty(sd.sd_kv4_attend_workspace_size(shp), dtype=torch.uint8, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    sd.sd_kv4_write(shp, c, x, x, n)
+    sd.sd_kv4_attend(shp, q, c, 0.08, out, lse, ws)
+graph.replay()
+torch.cuda.synchronize()
+got = out.clone(), lse.clone()
+sd.sd_kv4_attend(shp, q, c, 0.08, out, lse, ws)
+torch.cuda.synchronize()
+assert torch.equal(got[0], out) and torch.equal(got[1], lse) and bool((out != 0).any())
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("n", [500, 40000])
+def test_first_calls_captured(sd, n):
+    """The library's very first calls are made inside a capture (what it asks the device once
+    it asks there)."""
+    r = subprocess.run([sys.executable, "-c", FIRST.format(n=n)], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr

@@ -44,6 +44,7 @@
 
 #include "sd_internal.cuh"
 #include "sd_kv4.cuh"
+#include "sd_kv4_plan.cuh"
 #include "sd_mma.cuh"
 
 namespace sd {
@@ -51,8 +52,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kKaTile = 32;    // tokens per tile
-constexpr int kKaWarps = 4;    // warps per CTA
 constexpr int kKaThreads = 32 * kKaWarps;
 constexpr int kKaOffV = kKaTile * kKv4Row, kKaOffS = 2 * kKaOffV;
 constexpr int kKaOffMask = kKaOffS + kKaTile * 2 * kKv4Scales;
@@ -1128,33 +1127,44 @@ __global__ void __launch_bounds__(32 * kKaJoinWarps) kv4_join_kernel(const KaArg
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// The largest cluster of the cluster kernel that this device runs (cached per device); 0:
+// none, not even of one CTA.
+template <int G, bool GATHER>
+int ka_max_cluster() {
+  static std::atomic<int> most[kMaxDev];
+  return per_device_cached(most, [] {
+    auto kern = kv4_cluster_kernel<G, GATHER>;
+    const size_t bytes = (size_t)kKaWarps * kKaRing<G>;
+    if (set_smem_limit((const void*)kern, bytes, "kv4 attend") != SD_OK) return 0;
+    int c = 8;
+    for (; c > 0; c >>= 1) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(c, 1, 1);
+      cfg.blockDim = dim3(kKaThreads, 1, 1);
+      cfg.dynamicSmemBytes = bytes;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = c;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int nc = 0;
+      if (cudaOccupancyMaxActiveClusters(&nc, kern, &cfg) == cudaSuccess && nc > 0) break;
+      cudaGetLastError();
+    }
+    return c;
+  });
+}
+
 template <int G, bool GATHER>
 int ka_launch(const KaArgs& a, int64_t most, cudaStream_t st) {
   const int64_t tiles = (most + kKaTile - 1) / kKaTile;
-  // Which kernel, by tiles in a row of work (t), each ~0.6 to 1 us, with what a launch adds
-  // in the same units.  Clusters: the tiles of a warp, 4 for every wave of CTAs, and what
-  // joining c CTAs adds; c > 1 only where all CTAs run at once.  Stream: an even share,
-  // and 12 for finding it and joining.  Measured (us, clusters / stream): 8 rows of 8,192
-  // tokens 11.8 / 13.2, of 16,384 16.8 / 15.3; 128 rows of 4,096 24.1 / 26.5, of 16,384
-  // 66 / 62; 512 rows of 128 10.7 / 12.7, of 2,064 46 / 42.
-  const int64_t slots = 2 * device_sm_count();
-  constexpr int kJoin[4] = {0, 4, 3, 4};  // c = 1, 2, 4, 8
-  int64_t best = 0;
-  int cs = 1;
-  for (int i = 0; i < 4; ++i) {
-    const int64_t c = 1 << i, w = c * kKaWarps;
-    if (i && a.rows * c > slots) break;
-    const int64_t waves = (a.rows * c + slots - 1) / slots;
-    const int64_t t = (tiles + w - 1) / w + kJoin[i];
-    const int64_t cost = waves > 1 ? waves * (t + 4) : t;
-    if (i == 0 || cost <= best) {
-      best = cost;
-      cs = (int)c;
-    }
-  }
-  const bool bal = fallback_forced() || best > a.rows * tiles / (slots * kKaWarps) + 12;
-  if (bal) {
-    const size_t bytes = (size_t)kKaWarps * kKaRing<G>;
+  const int cs = fallback_forced() ? 0
+                                   : kv4_cluster_of(a.rows, tiles, device_sm_count(),
+                                                    ka_max_cluster<G, GATHER>());
+  const size_t bytes = (size_t)kKaWarps * kKaRing<G>;
+  if (cs == 0) {
     auto kern = kv4_stream_kernel<G, GATHER>;
     if (int rc = set_smem_limit((const void*)kern, bytes, "kv4 attend")) return rc;
     const int grid = (int)imin64(2 * device_sm_count(), kKaMaxWarps / kKaWarps);
@@ -1168,7 +1178,6 @@ int ka_launch(const KaArgs& a, int64_t most, cudaStream_t st) {
     auto join = pairs <= device_sm_count() ? kv4_join_kernel<G, 16> : kv4_join_kernel<G, 8>;
     return kv4_launch("kv4 attend join", join, jgrid, 32 * kKaJoinWarps, 0, 0, st, a, run);
   }
-  const size_t bytes = (size_t)kKaWarps * kKaRing<G>;
   auto kern = kv4_cluster_kernel<G, GATHER>;
   if (int rc = set_smem_limit((const void*)kern, bytes, "kv4 attend")) return rc;
   return kv4_launch("kv4 attend", kern, dim3(cs, (unsigned)a.rows), kKaThreads, bytes, cs, st, a);
