@@ -239,7 +239,8 @@ def sd_gather_attend_noalloc(shape: SdShape, q, K, V, idx, idx_stride: int, coun
 
 class Kv4Cache:
     """A 4-bit K/V cache on the device (sd_kv4): k, v uint8 [B][hkv][n_cap][64] and
-    scale bf16 [B][hkv][n_cap][8], given or allocated (zeros: every token stands for 0)."""
+    scale bf16 [B][hkv][n_cap][8], given (also flat, or as bytes or bit patterns) or
+    allocated (zeros: every token stands for 0)."""
 
     def __init__(self, batch: int, hkv: int, n_cap: int, device="cuda", k=None, v=None,
                  scale=None):
@@ -248,49 +249,107 @@ class Kv4Cache:
         self.v = torch.zeros((*dims, 64), dtype=torch.uint8, device=device) if v is None else v
         self.scale = (torch.zeros((*dims, 8), dtype=torch.bfloat16, device=device)
                       if scale is None else scale)
-        for t, nbytes in ((self.k, 64), (self.v, 64), (self.scale, 16)):
+        for name, t, last, nbytes in (("k", self.k, 64, 64), ("v", self.v, 64, 64),
+                                      ("scale", self.scale, 8, 16)):
             if t.numel() * t.element_size() != batch * hkv * n_cap * nbytes:
                 raise ValueError("Kv4Cache: an array's size does not match batch, hkv, n_cap")
+            if t.dim() == 4 and tuple(t.shape[:3]) != dims:
+                raise ValueError(f"Kv4Cache: {name} is {tuple(t.shape)}, expected "
+                                 f"{(*dims, last)}")
+            if name != "scale" and (t.is_floating_point() or t.dtype == torch.bool):
+                raise ValueError(f"Kv4Cache: {name} is {t.dtype}, expected code bytes (uint8)")
+            if name == "scale" and t.dtype not in _BF16:
+                raise ValueError(f"Kv4Cache: scale is {t.dtype}, expected bf16")
+            if t.device != self.k.device:
+                raise ValueError("Kv4Cache: arrays on different devices")
         self.dims = dims
         self.c = _abi.SdKv4(_ptr(self.k), _ptr(self.v), _ptr(self.scale))
 
 
-def _kv4(shape: SdShape, cache: Kv4Cache):
-    """The cache's sd_kv4, if the shape addresses it: its first `batch` sequences."""
-    b, h, n_cap = cache.dims
-    if shape.batch > b or shape.hkv != h or (shape.n_cap or shape.n) != n_cap:
-        raise ValueError(f"the shape's batch, hkv, n_cap {shape.batch}, {shape.hkv}, "
-                         f"{shape.n_cap or shape.n} do not address a cache of {cache.dims}")
-    return ctypes.byref(cache.c)
+# What may hold bf16 values: the type, its bit patterns, raw bytes.
+_BF16 = frozenset((torch.bfloat16, torch.int16, torch.uint16, torch.uint8))
+_INT32, _FLOAT32, _BFLOAT16 = torch.int32, torch.float32, torch.bfloat16
 
 
-def _rows(t, shape: SdShape, m: int):
-    """(pointer, strides) of a [B][hkv][>= m][128] tensor of any strides with consecutive
-    channels; other contiguous tensors and addresses are taken as [B][hkv][m][128]."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+def _kv4(shape: SdShape, B: int, hkv: int, cache: Kv4Cache):
+    """The cache's sd_kv4, if the shape addresses it: its first B sequences."""
+    n_cap = shape.n_cap or shape.n
+    if (hkv, n_cap) != cache.dims[1:] or B > cache.dims[0]:
+        raise ValueError(f"the shape's batch, hkv, n_cap {B}, {hkv}, {n_cap} do not address a "
+                         f"cache of {cache.dims}")
+    return cache.c
+
+
+def _values(t, name: str, dtype, n: int) -> Optional[int]:
+    """The address of a contiguous tensor of at least n values of dtype; None and addresses
+    pass.  (Indices and lengths are int64 by torch's default, whose words would be taken
+    as pairs of int32.)"""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is dtype and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected at least {n} contiguous values of {dtype}, got "
+                     f"{tuple(t.shape)} of {t.dtype}")
+
+
+def _bf16(t, name: str, n: int) -> Optional[int]:
+    """... of at least n bf16 values, their bit patterns or bytes."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is _BFLOAT16 and t.numel() >= n:
+        return _ptr(t)
+    if t.dtype not in _BF16 or t.numel() * t.element_size() < 2 * n:
+        raise ValueError(f"{name}: expected at least {n} bf16 values, got {tuple(t.shape)} of "
+                         f"{t.dtype}")
+    return _ptr(t)
+
+
+def _rows(t, dims, m: int):
+    """(pointer, strides) of a [B][hkv][>= m][128] bf16 tensor of any strides with
+    consecutive channels, dims = (B, hkv, 128); a contiguous tensor of another rank that
+    holds exactly B * hkv * m rows, a flat one of at least as many, and addresses are taken
+    as [B][hkv][m][128]."""
+    if t is None or type(t) is int:
+        return t, None
+    if t.dtype not in _BF16:
+        raise ValueError(f"libsd takes bf16 rows, got {t.dtype}")
+    if t.dim() != 4:
+        have, need = t.numel() * t.element_size(), 2 * dims[0] * dims[1] * m * dims[2]
+        if have < need or (have > need and t.dim() != 1):
+            raise ValueError(f"expected {m} rows of {dims}, got {tuple(t.shape)}")
         return _ptr(t), None
     b, h, n, d = t.shape
-    if b != shape.batch or h != shape.hkv or n < m or d != shape.d:
-        raise ValueError(f"expected [{shape.batch}][{shape.hkv}][>= {m}][{shape.d}] rows, "
+    if (b, h, d) != dims or n < m:
+        raise ValueError(f"expected [{dims[0]}][{dims[1]}][>= {m}][{dims[2]}] rows, "
                          f"got {tuple(t.shape)}")
     sb, sh, st, sd_ = t.stride()
     if sd_ != 1 or t.element_size() != 2:
         raise ValueError("libsd takes bf16 rows of consecutive channels")
+    if n == m and st == d and sh == m * d and sb == h * sh:
+        return t.data_ptr(), None  # contiguous
     return t.data_ptr(), ctypes.byref(_abi.SdStrides(sb, sh, st))
 
 
 def sd_kv4_write(shape: SdShape, cache: Kv4Cache, K, V, m: int, pos=None, length=None,
                  first: int = 0, stream=None) -> None:
-    (k, ks), (v, vs) = _rows(K, shape, m), _rows(V, shape, m)
-    _check(lib().sd_kv4_write(ctypes.byref(shape), _kv4(shape, cache), k, ks, v, vs, m, first,
-                              _ptr(pos), _ptr(length), _stream(stream)), "sd_kv4_write")
+    B, hkv = shape.batch, shape.hkv
+    dims = (B, hkv, shape.d)
+    (k, ks), (v, vs) = _rows(K, dims, m), _rows(V, dims, m)
+    _check(lib().sd_kv4_write(shape, _kv4(shape, B, hkv, cache), k, ks, v, vs, m,
+                              first, _values(pos, "pos", _INT32, B),
+                              _values(length, "length", _INT32, B), _stream(stream)),
+           "sd_kv4_write")
 
 
 def sd_kv4_read(shape: SdShape, cache: Kv4Cache, K, V, m: int, pos=None, length=None,
                 first: int = 0, stream=None) -> None:
-    (k, ks), (v, vs) = _rows(K, shape, m), _rows(V, shape, m)
-    _check(lib().sd_kv4_read(ctypes.byref(shape), _kv4(shape, cache), k, ks, v, vs, m, first,
-                             _ptr(pos), _ptr(length), _stream(stream)), "sd_kv4_read")
+    B, hkv = shape.batch, shape.hkv
+    dims = (B, hkv, shape.d)
+    (k, ks), (v, vs) = _rows(K, dims, m), _rows(V, dims, m)
+    _check(lib().sd_kv4_read(shape, _kv4(shape, B, hkv, cache), k, ks, v, vs, m,
+                             first, _values(pos, "pos", _INT32, B),
+                             _values(length, "length", _INT32, B), _stream(stream)),
+           "sd_kv4_read")
 
 
 def sd_kv4_attend_workspace_size(shape: SdShape) -> int:
@@ -300,9 +359,14 @@ def sd_kv4_attend_workspace_size(shape: SdShape) -> int:
 def sd_kv4_attend(shape: SdShape, q, cache: Kv4Cache, scale: float, out, lse=None, workspace=None,
                   begin=None, end=None, stream=None) -> None:
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().sd_kv4_attend(ctypes.byref(shape), _ptr(q), _kv4(shape, cache), _ptr(begin),
-                               _ptr(end), float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
-                               ws_bytes, _stream(stream)), "sd_kv4_attend")
+    B, hq = shape.batch, shape.hq
+    c, n = _kv4(shape, B, shape.hkv, cache), B * hq * shape.d
+    _check(lib().sd_kv4_attend(shape, _bf16(q, "q", n), c,
+                               _values(begin, "begin", _INT32, B),
+                               _values(end, "end", _INT32, B), float(scale),
+                               _values(out, "out", _FLOAT32, n),
+                               _values(lse, "lse", _FLOAT32, B * hq), _ptr(workspace), ws_bytes,
+                               _stream(stream)), "sd_kv4_attend")
 
 
 def sd_kv4_gather_attend_workspace_size(shape: SdShape, max_count: int) -> int:
@@ -313,9 +377,15 @@ def sd_kv4_gather_attend(shape: SdShape, q, cache: Kv4Cache, idx, idx_stride: in
                          max_count: int, scale: float, out, lse=None, workspace=None,
                          stream=None) -> None:
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().sd_kv4_gather_attend(ctypes.byref(shape), _ptr(q), _kv4(shape, cache),
-                                      _ptr(idx), idx_stride, _ptr(count), max_count,
-                                      float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+    B, hq, hkv = shape.batch, shape.hq, shape.hkv
+    c, n, rows = _kv4(shape, B, hkv, cache), B * hq * shape.d, B * hkv
+    # the last row's entries end at max_count
+    idx = _values(idx, "idx", _INT32, (rows - 1) * idx_stride + max_count)
+    _check(lib().sd_kv4_gather_attend(shape, _bf16(q, "q", n), c, idx, idx_stride,
+                                      _values(count, "count", _INT32, rows), max_count,
+                                      float(scale),
+                                      _values(out, "out", _FLOAT32, n),
+                                      _values(lse, "lse", _FLOAT32, B * hq), _ptr(workspace),
                                       ws_bytes, _stream(stream)), "sd_kv4_gather_attend")
 
 
