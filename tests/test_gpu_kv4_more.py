@@ -235,3 +235,26 @@ def test_first_calls_captured(sd, n):
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                        timeout=300)
     assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("G", [4, 8])
+@pytest.mark.parametrize("small", [0, -40, -60])
+def test_small_values_after_wide_ones(sd, path, G, small):
+    """The first tile's values have a range of 2^100 and its logits lie 400 below those of
+    all that follow, whose values are of size 2^small: a warp that has met the wide ones
+    weighs the others as exactly as any."""
+    rng = np.random.default_rng(G)
+    B, h, n = 20, 8, 1000  # several tiles a warp with either kernel
+    some = 2
+    qf = rng.standard_normal((B, h, 1, 128)) + 0.05 * rng.standard_normal((B, h, G, 128))
+    K = 0.3 * rng.standard_normal((B, h, n, 128)).astype(np.float32)
+    V = rng.standard_normal((B, h, n, 128)).astype(np.float32) * np.float32(2.0 ** small)
+    base = qf.mean(2)
+    K[:, :, :32] = (-400 / SCALE / (base * base).sum(-1, keepdims=True) * base)[:, :, None]
+    V[:, :, :32] = rng.uniform(-1, 1, (B, h, 32, 128)) * 2.0 ** 100
+    q = kv.bf16_bits(qf.reshape(B, h * G, 128).astype(np.float32))
+    k, v, rec = kv.encode(kv.bf16_bits(K), kv.bf16_bits(V))
+    ref = kb.attend(q[:some], k[:some], v[:some], rec[:some], [np.arange(n)] * (some * h), SCALE)
+    for out, lse in attend_both(sd, q, k, v, rec, SCALE):
+        kb.check(out[:some], lse[:some], ref, tight=2.0 ** -6)
+        assert np.isfinite(out).all()

@@ -417,9 +417,14 @@ __device__ __forceinline__ void ka_raise_m(KaState& S, int e, float top) {
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     S.mo[e][g] *= al;
-    // what was summed weighs 2^-d now: f takes up the factor, o stays, up to f's limit
-    const float fn = fminf(S.f[e][g] * ka_exp2(fminf(d, 126.0f)), kKaF0);
-    const float r = (fn / S.f[e][g]) * al;
+    // what was summed weighs 2^-d now: f takes up the factor, o stays, up to f's limit.  In
+    // exponents, as 2^d alone may pass the fp32 range (f then stayed where wide values had
+    // left it, and small ones after them became 0).  1 / f is as exact; r is 0 below 2^-49,
+    // where f is at its limit and an old sum below 2^-135 of no account.
+    const uint32_t fb = __float_as_uint(S.f[e][g]);
+    const float fn = __uint_as_float(
+        min(fb + ((uint32_t)fminf(d, 217.0f) << 23), __float_as_uint(kKaF0)));
+    const float r = fn * (al * __uint_as_float(0x7F000000u - fb));
     S.f[e][g] = fn;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
