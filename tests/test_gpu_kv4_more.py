@@ -1,6 +1,6 @@
 """GPU tests of the 4-bit K/V cache beyond the ordinary sizes and values: calls that are longer
-than the cache, values at the ends of their range with the bounds of _kv4_bounds.py, ranges and
-selections that the kernel before writes, calls captured first."""
+than the cache, values and queries at the ends of their range with the bounds of _kv4_bounds.py,
+ranges and selections that the kernel before writes, calls captured first, every step."""
 import math
 import os
 import subprocess
@@ -258,3 +258,100 @@ def test_small_values_after_wide_ones(sd, path, G, small):
     for out, lse in attend_both(sd, q, k, v, rec, SCALE):
         kb.check(out[:some], lse[:some], ref, tight=2.0 ** -6)
         assert np.isfinite(out).all()
+
+
+@pytest.mark.parametrize("G", [1, 4, 8])
+@pytest.mark.parametrize("below", [10, 20, 28])
+def test_wide_queries(sd, path, G, below):
+    """Query channels of up to `below` powers of two under the head's largest, with a key that
+    shows only them: exact all the same (the keys are 0 and their group's minimum in the
+    large channels, so that a logit holds nothing else)."""
+    rng = np.random.default_rng(below + G)
+    B, h, n = 2, 2, 333
+    big = np.arange(128) % 16 == 3
+    qf = np.where(big, 1.5, rng.uniform(1, 2, (B, h * G, 128)) * 2.0 ** -below)
+    K = np.where(big, 0, rng.uniform(0, 4, (B, h, n, 128)))
+    V = rng.standard_normal((B, h, n, 128))
+    q = kv.bf16_bits(qf.astype(np.float32))
+    k, v, rec = kv.encode(kv.bf16_bits(K.astype(np.float32)), kv.bf16_bits(V.astype(np.float32)))
+    assert not kv.bf16_val(rec[..., 1:4:2]).any()  # the minima
+    check_both(sd, q, k, v, rec, 2.0 ** (below - 4), tight=2.0 ** -7)
+
+
+@pytest.mark.parametrize("G", [4, 8])
+def test_huge_values_of_no_weight(sd, path, G):
+    """Ordinary tokens, and three of enormous values and a weight of 0 at the front."""
+    rng = np.random.default_rng(G)
+    B, h, n = 2, 2, 900
+    qf = np.repeat(rng.standard_normal((B, h, 128)), G, 1)
+    K, V = rng.standard_normal((2, B, h, n, 128))
+    K[:, :, :3] = -40 * qf[:, ::G, None]
+    V[:, :, :3] *= 1e30
+    q = kv.bf16_bits(qf.astype(np.float32))
+    k, v, rec = kv.encode(kv.bf16_bits(K.astype(np.float32)), kv.bf16_bits(V.astype(np.float32)))
+    check_both(sd, q, k, v, rec, SCALE, tight=2.0 ** -6)
+
+
+@pytest.mark.parametrize("G", [4, 8])
+def test_long_flat_tail(sd, G):
+    """One token of a wide step that carries half of the mass, then thousands of equal ones
+    that carry the rest, in rows that a warp works on alone: the smallest weights that count
+    against a large one (their 22 bits end at 2^-25 / 2^7 of it)."""
+    g = torch.Generator(device="cuda").manual_seed(G)
+    B, h, n = 400, 8, 4096      # rows in plenty for the streaming kernel
+    some = [0, 1, 133, B - 1]
+    c = sd.Kv4Cache(B, h, n)
+    shp = sd.make_shape(B, h * G, h, n)
+    base = torch.randn(128, device="cuda", generator=g)
+    first = base * (math.log(n) / SCALE / float(base @ base))  # logit log(n), the others 0
+    for t in range(0, n, 512):
+        V = torch.randn((B, h, 512, 128), device="cuda", generator=g)
+        K = torch.zeros_like(V)
+        if t == 0:
+            K[:, :, 0] = first
+            V[:, :, 0] *= 4
+        sd.sd_kv4_write(shp, c, K.bfloat16(), V.bfloat16(), 512, first=t)
+        del K, V
+    qb = base.bfloat16().expand(B, h * G, 128).contiguous()
+    out, lse = torch.empty((B, h * G, 128), device="cuda"), torch.empty((B, h * G), device="cuda")
+    ws = torch.empty(sd.sd_kv4_attend_workspace_size(shp), dtype=torch.uint8, device="cuda")
+    sd.sd_kv4_attend(shp, qb, c, SCALE, out, lse, ws)
+    torch.cuda.synchronize()
+    s = torch.tensor(some, device="cuda")
+    q, k, v = bits(qb[s]), host(c.k[s], np.uint8), host(c.v[s], np.uint8)
+    ref = kb.attend(q, k, v, bits(c.scale[s]), [np.arange(n)] * (len(some) * h), SCALE)
+    kb.check(host(out[s], np.float32), host(lse[s], np.float32), ref)
+
+
+def test_steps_of_every_significand(sd):
+    """Steps s of all 128 bf16 significands and of exponents over the whole range, with channels
+    on, next to and between the borders of codes (m + (c + 1/2) s): the quotients are
+    rounded as an IEEE division's, so every code is that of the plain format."""
+    rng = np.random.default_rng(5)
+    sig = np.arange(128, 256)
+    ex = np.concatenate((np.arange(-100, 118, 7), [117]))
+    s = (sig[:, None] * 2.0 ** (ex[None] - 7.0)).reshape(-1)              # [groups]
+    off = rng.integers(0, 16, s.size)                                     # m = -off s / 4 or so
+    lo = kv.bf16_val(kv.bf16_bits((-off * s / 4).astype(np.float32))).astype(np.float64)
+    x = np.empty((s.size, 64))
+    x[:] = lo[:, None] + (rng.integers(0, 15, x.shape) + 0.5 + rng.choice(
+        [0, 2.0 ** -9, -2.0 ** -9, 2.0 ** -7, -2.0 ** -7], x.shape)) * s[:, None]
+    x[:, 0] = lo
+    x[:, 1] = lo + 15 * s                                                 # the group's largest
+    x = kv.bf16_bits(x.astype(np.float32))
+    n = s.size // 2
+    rows = x.reshape(n, 128)
+    codes, steps, _ = kv.quantise(rows)
+    got = kv.bf16_bits(steps.reshape(-1)) & 0x7F
+    assert set(got.tolist()) == set(range(128)) and (steps > 0).all()
+    # ties are among them: a quotient that is not the division's would show there
+    d = kv.bf16_val(rows).astype(np.float64).reshape(n, 2, 64)
+    qt = (d - d.min(-1, keepdims=True)) / steps[..., None]
+    assert ((qt - np.floor(qt)) == 0.5).sum() > 1000
+    c = sd.Kv4Cache(1, 1, n)
+    t = dev(rows).view(1, 1, n, 128)
+    sd.sd_kv4_write(sd.make_shape(1, 1, 1, n), c, t, t, n)
+    torch.cuda.synchronize()
+    assert np.array_equal(host(c.k, np.uint8)[0, 0], kv.pack(codes))
+    assert np.array_equal(host(c.v, np.uint8)[0, 0], kv.pack(codes))
+    assert np.array_equal(bits(c.scale)[0, 0, :, 0:4:2], kv.bf16_bits(steps))

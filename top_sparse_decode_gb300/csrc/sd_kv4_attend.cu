@@ -16,7 +16,10 @@
 //  * PV: O^T = V^T P^T, 16 channels as rows, heads as columns, 16 tokens deep.  w = p s f is
 //    split in two f16 parts (22 bits: one rounding to 11 would cost 2^-12 of an output; f
 //    a power of two per head and group that holds the largest w in [2^7, 2^14], raised and
-//    lowered as an online softmax moves its maximum).  With G <= 4 columns 0..3 take the
+//    lowered as an online softmax moves its maximum).  22 bits hold down to 2^-10 of the
+//    largest w that the warp has met; below, a w is off by at most 2^-25, 2^-32 of that one,
+//    so that a tail of many small weights is off by 2^-32 per token of the warp, where its
+//    sum in fp32 may be by 2^-27 (chains of an eighth of the tokens).  With G <= 4 columns 0..3 take the
 //    high parts and 4..7 the low ones (8 MMAs per 16 tokens), with G = 8 the low parts are
 //    8 more.
 //  * p = 2^(z log2 e - m); m, a whole number per head, is raised only when weights
