@@ -456,8 +456,14 @@ int sd_kv4_read(const sd_shape* shape, const sd_kv4* cache, void* K, const sd_st
  *   q bf16 [B][hq][d]; begin, end: int32 [B] (device), NULL meaning 0 and n; out fp32
  *   [B][hq][d]; lse fp32 [B][hq] or NULL.  An empty range gives out = 0, lse = -inf.
  *   Cache contents outside the range reach no output.  q is finite.
- *   Workspace: sd_kv4_attend_workspace_size() bytes (device, 16-byte aligned),
- *   contents need not be initialised; calls sharing a workspace must not overlap.
+ *   A finite cache gives finite results as long as fp32 holds what they are made of:
+ *   scale log2(e) times a group's sum of q_j and of q_j c_j, and these times its m and
+ *   s; and e^{z_i - m'} |v_i| summed over the tokens that were met, m' the largest logit
+ *   met so far, less 9 log(2) at most (a token's weight may stand at 2^9 for a while, and
+ *   one that later ones make vanish has counted in full).
+ *   Workspace: sd_kv4_attend_workspace_size() bytes (device, 16-byte aligned; at most 11.2
+ *   MB, whatever n), contents need not be initialised; every call asks for it, also one
+ *   that is small enough to leave it alone; calls sharing a workspace must not overlap.
  *   Errors: SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED (shape), SD_ERR_WORKSPACE,
  *   SD_ERR_CUDA.
  */
@@ -474,7 +480,8 @@ int sd_kv4_attend(const sd_shape* shape, const void* q, const sd_kv4* cache,
  *   order; entries outside [0, n) are skipped, an index listed twice counts twice; a
  *   count below 1 is an empty row: out = 0, lse = -inf).  Other arguments and errors
  *   as sd_kv4_attend; 0 <= max_count <= idx_stride, max_count < 2^31.
- *   Workspace: sd_kv4_gather_attend_workspace_size() bytes (device).
+ *   Workspace: sd_kv4_gather_attend_workspace_size() bytes (device), as many as
+ *   sd_kv4_attend's for any max_count >= 0.
  */
 size_t sd_kv4_gather_attend_workspace_size(const sd_shape* shape, int64_t max_count);
 int sd_kv4_gather_attend(const sd_shape* shape, const void* q, const sd_kv4* cache,

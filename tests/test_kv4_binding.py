@@ -100,3 +100,14 @@ def test_cache_arrays(sd):
     sd.Kv4Cache(B, H, N, device="cpu", k=k, v=k.view(torch.int8), scale=s.view(torch.int16))
     sd.Kv4Cache(B, H, N, device="cpu", k=k.flatten(), v=k.flatten().view(torch.int32),
                 scale=s.flatten().view(torch.uint8))
+
+
+def test_workspace_sizes(sd):
+    """One size for both calls, whatever n and max_count, and at most what the header says."""
+    for b, hq, hkv in ((1, 1, 1), (2, 8, 2), (5000, 16, 2), (65535, 8, 1)):
+        size = sd.sd_kv4_attend_workspace_size(sd.make_shape(b, hq, hkv, 1))
+        assert 0 < size <= 11_200_000
+        for n, mc in ((1, 0), (4096, 7), (2 ** 31 - 1, 2 ** 31 - 1)):
+            shp = sd.make_shape(b, hq, hkv, n)
+            assert sd.sd_kv4_attend_workspace_size(shp) == size
+            assert sd.sd_kv4_gather_attend_workspace_size(shp, mc) == size

@@ -611,7 +611,7 @@ static int check_kv4_attend(const char* fn, const Dims& s, const void* q, const 
 size_t sd_kv4_attend_workspace_size(const sd_shape* shape) {
   Dims s;
   if (check_shape(shape, &s)) return 0;
-  return kv4_attend_workspace_bytes(s, s.n);
+  return kv4_attend_workspace_bytes(s);
 }
 
 int sd_kv4_attend(const sd_shape* shape, const void* q, const sd_kv4* cache,
@@ -621,7 +621,7 @@ int sd_kv4_attend(const sd_shape* shape, const void* q, const sd_kv4* cache,
   int rc = check_shape(shape, &s);
   if (rc) return rc;
   if ((rc = check_kv4_attend("sd_kv4_attend", s, q, cache, out, lse, workspace, ws_bytes,
-                             kv4_attend_workspace_bytes(s, s.n))))
+                             kv4_attend_workspace_bytes(s))))
     return rc;
   if ((uintptr_t)begin % 4 || (uintptr_t)end % 4)
     return fail(SD_ERR_INVALID_ARG, "sd_kv4_attend: begin and end must be 4-byte aligned");
@@ -632,7 +632,7 @@ int sd_kv4_attend(const sd_shape* shape, const void* q, const sd_kv4* cache,
 size_t sd_kv4_gather_attend_workspace_size(const sd_shape* shape, int64_t max_count) {
   Dims s;
   if (check_shape(shape, &s) || max_count < 0) return 0;
-  return kv4_attend_workspace_bytes(s, max_count);
+  return kv4_attend_workspace_bytes(s);
 }
 
 int sd_kv4_gather_attend(const sd_shape* shape, const void* q, const sd_kv4* cache,
@@ -649,7 +649,7 @@ int sd_kv4_gather_attend(const sd_shape* shape, const void* q, const sd_kv4* cac
   if (max_count < 0 || max_count >= (int64_t)1 << 31 || idx_stride < max_count)
     return fail(SD_ERR_INVALID_ARG, "sd_kv4_gather_attend: bad max_count / idx_stride");
   if ((rc = check_kv4_attend("sd_kv4_gather_attend", s, q, cache, out, lse, workspace, ws_bytes,
-                             kv4_attend_workspace_bytes(s, max_count))))
+                             kv4_attend_workspace_bytes(s))))
     return rc;
   return launch_kv4_attend(s, (const uint16_t*)q, *cache, idx, idx_stride, count, max_count,
                            nullptr, nullptr, scale, out, lse, workspace, (cudaStream_t)stream);

@@ -204,7 +204,7 @@ int launch_attend_combine(int S, int64_t BH, const float* outs, const float* lse
 int launch_kv4_move(bool write, const Dims& s, const sd_kv4& c, void* K, const sd_strides& ks,
                     void* V, const sd_strides& vs, int64_t m, int64_t first, const int32_t* pos,
                     const int32_t* length, cudaStream_t st);
-size_t kv4_attend_workspace_bytes(const Dims& s, int64_t max_tokens);
+size_t kv4_attend_workspace_bytes(const Dims& s);
 int launch_kv4_attend(const Dims& s, const uint16_t* q, const sd_kv4& c, const int32_t* idx,
                       int64_t idx_stride, const int32_t* count, int64_t max_count,
                       const int32_t* begin, const int32_t* end, float scale, float* out,

@@ -1198,7 +1198,7 @@ int ka_pick(const KaArgs& a, int64_t most, cudaStream_t st) {
 
 }  // namespace
 
-size_t kv4_attend_workspace_bytes(const Dims& s, int64_t) {
+size_t kv4_attend_workspace_bytes(const Dims& s) {
   return align256(sizeof(int2) * s.B * s.Hkv) +
          (size_t)2 * kKaMaxWarps * s.G * (sizeof(float) * kD + sizeof(float2));
 }
