@@ -12,8 +12,8 @@
 // 16-byte access of bf16, one 32-bit word of codes) per lane, 8 lanes per group; four
 // tokens at a time, the next four requested before the current ones are worked on.
 //
-// The read is bound by HBM: 4 x 8 x 131,072 tokens, 2.75 GB, in 421 us (6.5 TB/s, 96 % of
-// the copy rate).  The write moves the same bytes in 443 us (6.2 TB/s): its ~100
+// The read is bound by HBM: 4 x 8 x 131,072 tokens, 2.75 GB, in 423 us (6.5 TB/s, 96 % of
+// the copy rate).  The write moves the same bytes in 440 us (6.3 TB/s): its ~100
 // instructions a token (quotients rounded as a division's, in pairs of fp32) nearly fill
 // the schedulers.  With one token a warp and plain divisions the two took 1.87 ms together.
 #include "sd_internal.cuh"

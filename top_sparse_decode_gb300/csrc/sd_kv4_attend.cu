@@ -19,9 +19,9 @@
 //    lowered as an online softmax moves its maximum).  22 bits hold down to 2^-10 of the
 //    largest w that the warp has met; below, a w is off by at most 2^-25, 2^-32 of that one,
 //    so that a tail of many small weights is off by 2^-32 per token of the warp, where its
-//    sum in fp32 may be by 2^-27 (chains of an eighth of the tokens).  With G <= 4 columns 0..3 take the
-//    high parts and 4..7 the low ones (8 MMAs per 16 tokens), with G = 8 the low parts are
-//    8 more.
+//    sum in fp32 may be by 2^-27 (chains of an eighth of the tokens).  With G <= 4 columns
+//    0..3 take the high parts and 4..7 the low ones (8 MMAs per 16 tokens), with G = 8 the
+//    low parts are 8 more.
 //  * p = 2^(z log2 e - m); m, a whole number per head, is raised only when weights
 //    exceed 2^8 or so.
 //
@@ -30,11 +30,11 @@
 // without bank conflicts.  No warp waits for another while it works.
 //
 // What bounds it: 144 bytes a token and KV head from HBM are 397 cycles of an SM's four
-// schedulers per 16 tokens at the measured copy rate; the work on them is ~311
+// schedulers per 16 tokens at the measured copy rate; the work on them is ~307
 // instructions (G <= 4; 360 with G = 8), half of them integer operations that issue every
 // second cycle: ~88 to take the codes apart, 64 to scale and centre them, 16 (24) MMAs of
 // 8.4 cycles.  It runs at ~420 cycles (G <= 4).  Measured (GB300): 8 KV heads of 1,048,576
-// tokens, G = 4: 200 us, 6.0 TB/s, 89 % of the copy rate; 512 of 16,384, G = 8: 242 us, 5.0
+// tokens, G = 4: 199 us, 6.1 TB/s, 89 % of the copy rate; 512 of 16,384, G = 8: 244 us, 5.0
 // TB/s.  Tried on the former and slower: six warps a CTA (their 168 registers spill; 5 us
 // more), scores of the next tile beside the values of this one (14), e4m3 MMAs for the
 // scores (converted to f16 by the compiler on this GPU; 35), the upper codes of a word taken
@@ -787,9 +787,9 @@ __device__ __forceinline__ void ka_write(const KaArgs& a, int64_t bq, int j, flo
 }
 
 // Few tiles: one cluster of CTAs per row, tiles dealt to its warps in turn, the states joined
-// through shared and distributed shared memory.  One launch and no workspace: a call of
-// one 4,096-token KV head takes 9 us as a graph node (10.3 with the streaming kernel), of
-// which an empty one is 4.8.
+// through shared and distributed shared memory.  One launch, and the workspace that every
+// call brings is left alone: a call of one 4,096-token KV head takes 8.2 us as a graph node
+// (9.3 with the streaming kernel), one of a single tile 4.4.
 template <int G, bool GATHER>
 __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];

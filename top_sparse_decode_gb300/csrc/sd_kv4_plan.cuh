@@ -16,9 +16,10 @@ constexpr int kKaWarps = 4;  // warps per CTA
 // By tiles in a row of work (t), each ~0.6 to 1 us, with what a launch adds in the same
 // units.  Clusters: the tiles of a warp, 4 for every wave of CTAs, and what joining c CTAs
 // adds; c > 1 only where all CTAs run at once.  Stream: an even share, and 12 for finding
-// it and joining.  Measured (us, clusters / stream): 8 rows of 8,192 tokens 11.8 / 13.2, of
-// 16,384 16.8 / 15.3; 128 rows of 4,096 24.1 / 26.5, of 16,384 66 / 62; 512 rows of 128
-// 10.7 / 12.7, of 2,064 46 / 42.
+// it and joining.  Measured (us, clusters / stream): 8 rows of 8,192 tokens 11.1 / 11.5, of
+// 16,384 16.0 / 13.5; 128 rows of 4,096 22.6 / 23.8, of 16,384 64.0 / 59.9; 512 rows of 128
+// 10.1 / 11.5, of 2,064 39.4 / 35.9.  Where it is wrong it costs little: 512 rows of 32
+// 8.8 / 7.8, of 1,024 24.7 / 23.5 (clusters taken).
 inline int kv4_cluster_of(int64_t rows, int64_t tiles, int sms, int max_cluster) {
   const int64_t slots = 2 * (int64_t)sms;
   constexpr int kJoin[4] = {0, 4, 3, 4};  // c = 1, 2, 4, 8
