@@ -18,8 +18,9 @@ constexpr int kKaWarps = 4;  // warps per CTA
 // adds; c > 1 only where all CTAs run at once.  Stream: an even share, and 12 for finding
 // it and joining.  Measured (us, clusters / stream): 8 rows of 8,192 tokens 11.1 / 11.5, of
 // 16,384 16.0 / 13.5; 128 rows of 4,096 22.6 / 23.8, of 16,384 64.0 / 59.9; 512 rows of 128
-// 10.1 / 11.5, of 2,064 39.4 / 35.9.  Where it is wrong it costs little: 512 rows of 32
-// 8.8 / 7.8, of 1,024 24.7 / 23.5 (clusters taken).
+// 10.1 / 11.5, of 2,064 39.4 / 35.9.  Next to its border it takes clusters where the other
+// is up to 8 to 13 % faster: 512 rows of 32 8.8 / 7.8, of 1,024 24.7 / 23.5; 256 rows of
+// 8,192, G = 8, 75.4 / 69.6.
 inline int kv4_cluster_of(int64_t rows, int64_t tiles, int sms, int max_cluster) {
   const int64_t slots = 2 * (int64_t)sms;
   constexpr int kJoin[4] = {0, 4, 3, 4};  // c = 1, 2, 4, 8
