@@ -460,7 +460,8 @@ int sd_kv4_read(const sd_shape* shape, const sd_kv4* cache, void* K, const sd_st
  *   scale log2(e) times a group's sum of q_j and of q_j c_j, and these times its m and
  *   s; and e^{z_i - m'} |v_i| summed over the tokens that were met, m' the largest logit
  *   met so far, less 9 log(2) at most (a token's weight may stand at 2^9 for a while, and
- *   one that later ones make vanish has counted in full).
+ *   one that later ones make vanish has counted in full).  Weights e^{z_i - m} below about
+ *   2^-126 count as 0.
  *   Workspace: sd_kv4_attend_workspace_size() bytes (device, 16-byte aligned; at most 11.2
  *   MB, whatever n), contents need not be initialised; every call asks for it, also one
  *   that is small enough to leave it alone; calls sharing a workspace must not overlap.
