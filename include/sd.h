@@ -491,6 +491,111 @@ int sd_kv4_gather_attend(const sd_shape* shape, const void* q, const sd_kv4* cac
                          void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * The bf16 K/V cache around the sparse step: how rows get into it, the attention of
+ * prompts and of layers that keep a window (HashAttention 2.1 starts from the attention
+ * over every cached token; 3.1 keeps the first and the latest tokens), and decode over a
+ * prefix that a batch shares.
+ *
+ * sd_rope -- norm and rotation of query and key heads.
+ *   q_weight, k_weight: fp32 [d] (device) or NULL; with a weight, a head's row x becomes
+ *     x / sqrt(mean(x^2) + eps) * weight, without one it is not normed.
+ *   inv_freq: double [rot / 2] (device), radians per position; channel pair j is turned
+ *     by the angle a = position * inv_freq[j] (a formed and reduced in 64 bits, so far
+ *     positions keep their phase): (x, y) -> (x cos a - y sin a, y cos a + x sin a).
+ *   rot: rotated channels, the first of the head; a multiple of 16 in [0, d] (0: no
+ *     rotation, inv_freq not read).
+ *   pairs: 0: pair j is channels j and j + rot / 2; 1: channels 2j and 2j + 1.
+ */
+typedef struct sd_rope {
+  const float* q_weight;
+  const float* k_weight;
+  const double* inv_freq;
+  float eps;
+  int32_t rot;
+  int32_t pairs;
+} sd_rope;
+
+/*
+ * sd_qk_norm_rope -- queries and keys of m new tokens per sequence, normed and rotated on
+ * their way from the projection: queries to q_out, keys and values into the cache (fp32
+ * arithmetic, one rounding to bf16 at the end; values are copied).
+ *   q, q_out: bf16, token t of (sequence b, query head h) at b * seq + h * head + t *
+ *   token (q_strides, q_out_strides; NULL: contiguous [B][hq][m][d]); k, v: the same over
+ *   the KV heads (a fused projection's output is one array seen three ways).  Input
+ *   strides may be 0; rows of q_out must not overlap; q_out may be q with its strides.
+ *   K, V: the caches, bf16 [B][hkv][n_cap][d]; token t < min(m, length[b]) of sequence b
+ *   goes to position first + pos[b] + t; keys and values whose position is outside [0, n)
+ *   are dropped (queries are not).  q and q_out, k and K, v and V: both or neither, at
+ *   least one of the three.
+ *   pos, length, rotary: int32 [B] (device), NULL meaning 0, m and first + pos[b]:
+ *   rotary[b] + t is the position that token t is rotated by (other than its place in the
+ *   cache when the cache holds a piece of the sequence, or is a buffer of m tokens on the
+ *   way to sd_kv4_write).  What is not written keeps what it holds.
+ *   Errors: SD_ERR_INVALID_ARG for a NULL or misaligned pointer (16 bytes; 8 for inv_freq,
+ *   4 for int32; weights 16), rot, eps (finite, >= 0) or strides out of range, m outside
+ *   [0, 2^31) or first outside [0, n].  m = 0 does nothing.
+ */
+int sd_qk_norm_rope(const sd_shape* shape, const sd_rope* rope, const void* q,
+                    const sd_strides* q_strides, void* q_out, const sd_strides* q_out_strides,
+                    const void* k, const sd_strides* k_strides, const void* v,
+                    const sd_strides* v_strides, void* K, void* V, int64_t m, int64_t first,
+                    const int32_t* pos, const int32_t* length, const int32_t* rotary,
+                    void* stream);
+
+/*
+ * sd_window_attend -- softmax attention with a sliding window and a few first tokens that
+ * stay visible, over the bf16 cache: prompts, chunks of them, and single tokens.
+ *   Query token t < min(m, length[b]) of sequence b stands at p = first + pos[b] + t and
+ *   sees the cached tokens i of [0, n) with i <= p and (i < sink or i > p - window); its
+ *   own key and those before it are in the cache already.  window >= n gives causal
+ *   attention over everything.  z_i = scale * <q, k_i>, out = sum_i e^{z_i - m} v_i /
+ *   sum_i e^{z_i - m}, lse = m + log(sum_i e^{z_i - m}); a token that sees nothing (p < 0)
+ *   gives out = 0, lse = -inf.
+ *   q: bf16, strides as sd_qk_norm_rope's q; K, V: bf16 [B][hkv][n_cap][d]; out: bf16
+ *   with strides of its own, rows apart; lse: fp32 [B][hq][m] or NULL.  pos, length: int32
+ *   [B] (device), NULL meaning 0 and m.  Rows of tokens t >= length[b] are not written.
+ *   scale >= 0.  Scores, sums and the softmax are fp32; the weights e^{z - m'} (m' at most
+ *   8 log 2 below the row's largest score so far) are rounded to bf16 for the product with
+ *   V, and lse comes from the sums before that.
+ *   A token that a query does not see reaches nothing of it, whatever its K and V hold
+ *   (infinities and NaN included).
+ *   Workspace: sd_window_attend_workspace_size() bytes (device, 16-byte aligned; 0 where
+ *   none is needed), contents need not be initialised; calls sharing a workspace must not
+ *   overlap.
+ *   Errors: SD_ERR_INVALID_ARG for a NULL or misaligned pointer (16 bytes; 4 for lse, pos,
+ *   length), bad strides, m outside [0, 2^31), first outside [0, n], window < 1, sink < 0,
+ *   a scale that is negative or not finite; SD_ERR_UNSUPPORTED for n >= 2^31 or m * hq *
+ *   B >= 2^31 (shape); SD_ERR_WORKSPACE; SD_ERR_CUDA.  m = 0 does nothing.
+ */
+size_t sd_window_attend_workspace_size(const sd_shape* shape, int64_t m, int64_t window,
+                                       int64_t sink);
+int sd_window_attend(const sd_shape* shape, const void* q, const sd_strides* q_strides,
+                     const void* K, const void* V, int64_t m, int64_t first, const int32_t* pos,
+                     const int32_t* length, int64_t window, int64_t sink, float scale, void* out,
+                     const sd_strides* out_strides, float* lse, void* workspace,
+                     size_t ws_bytes, void* stream);
+
+/*
+ * sd_prefix_attend -- decode attention of a batch that shares a prefix: one query token
+ * per sequence over the prefix's p tokens, whose K and V are read once for all sequences,
+ * and over its own tokens [0, min(end[b], n)) of the cache; one softmax over both.
+ *   q: bf16 [B][hq][d]; K_prefix, V_prefix: bf16 [hkv][p_cap][d] (p_cap >= p; 0: p); K, V:
+ *   bf16 [B][hkv][n_cap][d], or both NULL (no own tokens; the shape's n is then not used);
+ *   end: int32 [B] (device), NULL meaning n; out: bf16 [B][hq][d]; lse: fp32 [B][hq] or
+ *   NULL.  p may be 0 (K_prefix, V_prefix not read).  A sequence with no token at all
+ *   gives out = 0, lse = -inf.  scale, arithmetic and roundings as sd_window_attend; cache
+ *   contents outside the ranges reach no output.
+ *   Workspace: sd_prefix_attend_workspace_size() bytes, as sd_window_attend's.
+ *   Errors: SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED (p or n >= 2^31, B * hq >= 2^24),
+ *   SD_ERR_WORKSPACE, SD_ERR_CUDA.
+ */
+size_t sd_prefix_attend_workspace_size(const sd_shape* shape, int64_t p);
+int sd_prefix_attend(const sd_shape* shape, const void* q, const void* K_prefix,
+                     const void* V_prefix, int64_t p, int64_t p_cap, const void* K,
+                     const void* V, const int32_t* end, float scale, void* out, float* lse,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * sd_offload_gather -- copy each (sequence, KV head, channel j)'s planned
  * prefix (the first plan_j planes, contiguous in the channel-major layout)
  * and channel j's scales from pinned host memory into HBM, with device loads
@@ -700,7 +805,8 @@ const char* sd_last_error(void);
  * sd_device_status, sd_set_fallback_paths and sd_debug_set_device_error; 103 adds
  * SD_PLAN_SPLIT, sd_shard_candidates, sd_topk_merge, sd_shard_select and
  * sd_attend_combine; 104 adds sd_copy.  The sd_kv4_* entry points came later under
- * the same number (nothing else changed): look them up by name. */
+ * the same number, and so did sd_qk_norm_rope, sd_window_attend and sd_prefix_attend
+ * (nothing else changed): look them up by name. */
 int sd_version(void);
 
 /*

@@ -24,6 +24,8 @@ from ._abi import (SD_ERR_CUDA, SD_ERR_INVALID_ARG, SD_ERR_TIMEOUT, SD_ERR_UNSUP
                    SD_SCORE_F32, SD_SCORE_I32, SdEncoder, SdSelect, SdShape)
 
 __all__ = [
+    "make_rope", "sd_qk_norm_rope", "sd_window_attend_workspace_size", "sd_window_attend",
+    "sd_prefix_attend_workspace_size", "sd_prefix_attend",
     "SdError", "make_shape", "make_encoder", "make_select", "lib",
     "sd_build_index", "sd_append_index", "sd_encode_query", "sd_plan", "sd_score",
     "sd_topk_workspace_size", "sd_topk", "sd_gather_attend_workspace_size", "sd_gather_attend",
@@ -387,6 +389,78 @@ def sd_kv4_gather_attend(shape: SdShape, q, cache: Kv4Cache, idx, idx_stride: in
                                       _values(out, "out", _FLOAT32, n),
                                       _values(lse, "lse", _FLOAT32, B * hq), _ptr(workspace),
                                       ws_bytes, _stream(stream)), "sd_kv4_gather_attend")
+
+
+class _Rope:
+    """sd_rope plus references that keep its tensors alive."""
+
+    def __init__(self, inv_freq, rot: int, q_weight, k_weight, eps: float, pairs: bool):
+        self.tensors = (inv_freq, q_weight, k_weight)
+        self.c = _abi.SdRope(_values(q_weight, "q_weight", _FLOAT32, 128),
+                             _values(k_weight, "k_weight", _FLOAT32, 128),
+                             _values(inv_freq, "inv_freq", torch.float64, rot // 2),
+                             float(eps), rot, 1 if pairs else 0)
+
+
+def make_rope(inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+              pairs: bool = False) -> _Rope:
+    """Norm and rotation of query and key heads (sd_rope), device tensors: inv_freq float64
+    [rot / 2] in radians per position (None: no rotation), q_weight and k_weight float32
+    [128] (None: that side is not normed)."""
+    return _Rope(inv_freq, 0 if inv_freq is None else 2 * inv_freq.numel(), q_weight, k_weight,
+                 eps, pairs)
+
+
+def sd_qk_norm_rope(shape: SdShape, rope: _Rope, q, q_out, k, v, K, V, m: int, pos=None,
+                    length=None, rotary=None, first: int = 0, stream=None) -> None:
+    B, hq, hkv, d = shape.batch, shape.hq, shape.hkv, shape.d
+    cap = B * hkv * (shape.n_cap or shape.n) * d
+    (qi, qs), (qo, qos) = _rows(q, (B, hq, d), m), _rows(q_out, (B, hq, d), m)
+    (ki, ks), (vi, vs) = _rows(k, (B, hkv, d), m), _rows(v, (B, hkv, d), m)
+    _check(lib().sd_qk_norm_rope(shape, rope.c, qi, qs, qo, qos, ki, ks, vi, vs,
+                                 _bf16(K, "K", cap), _bf16(V, "V", cap), m, first,
+                                 _values(pos, "pos", _INT32, B),
+                                 _values(length, "length", _INT32, B),
+                                 _values(rotary, "rotary", _INT32, B), _stream(stream)),
+           "sd_qk_norm_rope")
+
+
+def sd_window_attend_workspace_size(shape: SdShape, m: int, window: int, sink: int = 0) -> int:
+    return int(lib().sd_window_attend_workspace_size(shape, m, window, sink))
+
+
+def sd_window_attend(shape: SdShape, q, K, V, m: int, window: int, sink: int, scale: float, out,
+                     lse=None, workspace=None, pos=None, length=None, first: int = 0,
+                     stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    B, hq, d = shape.batch, shape.hq, shape.d
+    cap = B * shape.hkv * (shape.n_cap or shape.n) * d
+    (qi, qs), (oo, os_) = _rows(q, (B, hq, d), m), _rows(out, (B, hq, d), m)
+    _check(lib().sd_window_attend(shape, qi, qs, _bf16(K, "K", cap), _bf16(V, "V", cap), m, first,
+                                  _values(pos, "pos", _INT32, B),
+                                  _values(length, "length", _INT32, B), window, sink,
+                                  float(scale), oo, os_,
+                                  _values(lse, "lse", _FLOAT32, B * hq * m), _ptr(workspace),
+                                  ws_bytes, _stream(stream)), "sd_window_attend")
+
+
+def sd_prefix_attend_workspace_size(shape: SdShape, p: int) -> int:
+    return int(lib().sd_prefix_attend_workspace_size(shape, p))
+
+
+def sd_prefix_attend(shape: SdShape, q, K_prefix, V_prefix, p: int, K, V, scale: float, out,
+                     lse=None, workspace=None, end=None, p_cap: int = 0, stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    B, hq, hkv, d = shape.batch, shape.hq, shape.hkv, shape.d
+    n, cap = B * hq * d, B * hkv * (shape.n_cap or shape.n) * d
+    pre = hkv * (p_cap or p) * d
+    _check(lib().sd_prefix_attend(shape, _bf16(q, "q", n), _bf16(K_prefix, "K_prefix", pre),
+                                  _bf16(V_prefix, "V_prefix", pre), p, p_cap,
+                                  _bf16(K, "K", cap), _bf16(V, "V", cap),
+                                  _values(end, "end", _INT32, B), float(scale),
+                                  _bf16(out, "out", n), _values(lse, "lse", _FLOAT32, B * hq),
+                                  _ptr(workspace), ws_bytes, _stream(stream)),
+           "sd_prefix_attend")
 
 
 def sd_offload_gather(shape: SdShape, host_planes, host_scales, plan, dev_planes, dev_scales,

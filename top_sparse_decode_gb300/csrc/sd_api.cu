@@ -655,6 +655,156 @@ int sd_kv4_gather_attend(const sd_shape* shape, const void* q, const sd_kv4* cac
                            nullptr, nullptr, scale, out, lse, workspace, (cudaStream_t)stream);
 }
 
+// The strides of a [B][heads][m][d] array (null: contiguous).
+static int row_strides(const char* fn, Dims s, int heads, int64_t m, const sd_strides* in,
+                       bool apart, sd_strides* out) {
+  s.Hkv = heads;
+  return resolve_strides(fn, s, m, in, apart, out);
+}
+static bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+int sd_qk_norm_rope(const sd_shape* shape, const sd_rope* rope, const void* q,
+                    const sd_strides* q_strides, void* q_out, const sd_strides* q_out_strides,
+                    const void* k, const sd_strides* k_strides, const void* v,
+                    const sd_strides* v_strides, void* K, void* V, int64_t m, int64_t first,
+                    const int32_t* pos, const int32_t* length, const int32_t* rotary,
+                    void* stream) {
+  const char* fn = "sd_qk_norm_rope";
+  Dims s;
+  int rc = check_shape(shape, &s);
+  if (rc) return rc;
+  if (!rope) return fail(SD_ERR_INVALID_ARG, "%s: rope is NULL", fn);
+  if (rope->rot < 0 || rope->rot > kD || rope->rot % 16)
+    return fail(SD_ERR_INVALID_ARG, "%s: rot = %d (a multiple of 16 in [0, %d])", fn, rope->rot,
+                kD);
+  if (rope->rot && (!rope->inv_freq || (uintptr_t)rope->inv_freq % 8))
+    return fail(SD_ERR_INVALID_ARG, "%s: inv_freq is NULL or not 8-byte aligned", fn);
+  if (!(rope->eps >= 0.0f) || rope->eps > 3.4e38f)
+    return fail(SD_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
+  if (!aligned16(rope->q_weight) || !aligned16(rope->k_weight))
+    return fail(SD_ERR_INVALID_ARG, "%s: the weights must be 16-byte aligned", fn);
+  if (!q != !q_out || !k != !K || !v != !V || !(q || k || v))
+    return fail(SD_ERR_INVALID_ARG, "%s: q and q_out, k and K, v and V go together, and one of "
+                "them is needed", fn);
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(K) ||
+      !aligned16(V))
+    return fail(SD_ERR_INVALID_ARG, "%s: rows and caches must be 16-byte aligned", fn);
+  if (!aligned4(pos) || !aligned4(length) || !aligned4(rotary))
+    return fail(SD_ERR_INVALID_ARG, "%s: pos, length and rotary must be 4-byte aligned", fn);
+  if (m < 0 || m >= (int64_t)1 << 31 || first < 0 || first > s.n)
+    return fail(SD_ERR_INVALID_ARG, "%s: m = %lld or first = %lld out of range", fn,
+                (long long)m, (long long)first);
+  if (m == 0) return SD_OK;
+  sd_strides qs, qos, ks, vs;
+  if ((rc = row_strides(fn, s, s.Hq, m, q ? q_strides : nullptr, false, &qs))) return rc;
+  if ((rc = row_strides(fn, s, s.Hq, m, q ? q_out_strides : nullptr, true, &qos))) return rc;
+  if ((rc = row_strides(fn, s, s.Hkv, m, k ? k_strides : nullptr, false, &ks))) return rc;
+  if ((rc = row_strides(fn, s, s.Hkv, m, v ? v_strides : nullptr, false, &vs))) return rc;
+  return launch_norm_rope(s, *rope, (const uint16_t*)q, qs, (uint16_t*)q_out, qos,
+                          (const uint16_t*)k, ks, (const uint16_t*)v, vs, (uint16_t*)K,
+                          (uint16_t*)V, m, first, pos, length, rotary, (cudaStream_t)stream);
+}
+
+// What the window and prefix calls share: scale, workspace.
+static int check_dense(const char* fn, float scale, const float* lse, void* ws, size_t ws_bytes,
+                       size_t need) {
+  if (!(scale >= 0.0f) || scale > 3.4e38f)
+    return fail(SD_ERR_INVALID_ARG, "%s: scale must be finite and not negative", fn);
+  if (!aligned4(lse)) return fail(SD_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", fn);
+  if (need && (!ws || ws_bytes < need))
+    return fail(SD_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+  if (need && !aligned16(ws))
+    return fail(SD_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+  return SD_OK;
+}
+
+static bool window_fits(const Dims& s, int64_t m, int64_t window, int64_t sink) {
+  return m >= 0 && m < (int64_t)1 << 31 && window >= 1 && sink >= 0 &&
+         (int64_t)s.B * s.Hq * m < (int64_t)1 << 31;
+}
+
+size_t sd_window_attend_workspace_size(const sd_shape* shape, int64_t m, int64_t window,
+                                       int64_t sink) {
+  Dims s;
+  if (check_shape(shape, &s) || !window_fits(s, m, window, sink) || m == 0) return 0;
+  return window_attend_workspace_bytes(s, m, window, sink);
+}
+
+int sd_window_attend(const sd_shape* shape, const void* q, const sd_strides* q_strides,
+                     const void* K, const void* V, int64_t m, int64_t first, const int32_t* pos,
+                     const int32_t* length, int64_t window, int64_t sink, float scale, void* out,
+                     const sd_strides* out_strides, float* lse, void* workspace,
+                     size_t ws_bytes, void* stream) {
+  const char* fn = "sd_window_attend";
+  Dims s;
+  int rc = check_shape(shape, &s);
+  if (rc) return rc;
+  if (!q || !K || !V || !out) return fail(SD_ERR_INVALID_ARG, "%s: NULL input", fn);
+  if (!aligned16(q) || !aligned16(K) || !aligned16(V) || !aligned16(out))
+    return fail(SD_ERR_INVALID_ARG, "%s: q, K, V and out must be 16-byte aligned", fn);
+  if (!aligned4(pos) || !aligned4(length))
+    return fail(SD_ERR_INVALID_ARG, "%s: pos and length must be 4-byte aligned", fn);
+  if (m < 0 || m >= (int64_t)1 << 31 || first < 0 || first > s.n)
+    return fail(SD_ERR_INVALID_ARG, "%s: m = %lld or first = %lld out of range", fn,
+                (long long)m, (long long)first);
+  if (window < 1 || sink < 0)
+    return fail(SD_ERR_INVALID_ARG, "%s: window = %lld or sink = %lld out of range", fn,
+                (long long)window, (long long)sink);
+  if (!window_fits(s, m, window, sink))
+    return fail(SD_ERR_UNSUPPORTED, "%s: batch * hq * m >= 2^31", fn);
+  if (m == 0) return SD_OK;
+  sd_strides qs, os;
+  if ((rc = row_strides(fn, s, s.Hq, m, q_strides, false, &qs))) return rc;
+  if ((rc = row_strides(fn, s, s.Hq, m, out_strides, true, &os))) return rc;
+  // ranges beyond the cache are the whole of it
+  window = imin64(window, (int64_t)1 << 32);
+  sink = imin64(sink, s.n);
+  if ((rc = check_dense(fn, scale, lse, workspace, ws_bytes,
+                        window_attend_workspace_bytes(s, m, window, sink))))
+    return rc;
+  return launch_window_attend(s, (const uint16_t*)q, qs, (const uint16_t*)K, (const uint16_t*)V,
+                              m, first, pos, length, window, sink, scale, (uint16_t*)out, os, lse,
+                              workspace, (cudaStream_t)stream);
+}
+
+static bool prefix_fits(const Dims& s, int64_t p) {
+  return p < (int64_t)1 << 31 && (int64_t)s.B * s.Hq < (int64_t)1 << 24;
+}
+
+size_t sd_prefix_attend_workspace_size(const sd_shape* shape, int64_t p) {
+  Dims s;
+  if (check_shape(shape, &s) || p < 0 || !prefix_fits(s, p)) return 0;
+  return prefix_attend_workspace_bytes(s, p);
+}
+
+int sd_prefix_attend(const sd_shape* shape, const void* q, const void* K_prefix,
+                     const void* V_prefix, int64_t p, int64_t p_cap, const void* K,
+                     const void* V, const int32_t* end, float scale, void* out, float* lse,
+                     void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "sd_prefix_attend";
+  Dims s;
+  int rc = check_shape(shape, &s);
+  if (rc) return rc;
+  if (p_cap == 0) p_cap = p;
+  if (p < 0 || p_cap < p)
+    return fail(SD_ERR_INVALID_ARG, "%s: p = %lld or p_cap = %lld out of range", fn,
+                (long long)p, (long long)p_cap);
+  if (!prefix_fits(s, p) || p_cap >= (int64_t)1 << 31)
+    return fail(SD_ERR_UNSUPPORTED, "%s: p_cap >= 2^31 or batch * hq >= 2^24", fn);
+  if (!q || !out || (p && (!K_prefix || !V_prefix)) || !K != !V)
+    return fail(SD_ERR_INVALID_ARG, "%s: NULL input", fn);
+  if (!aligned16(q) || !aligned16(out) || !aligned16(K_prefix) || !aligned16(V_prefix) ||
+      !aligned16(K) || !aligned16(V))
+    return fail(SD_ERR_INVALID_ARG, "%s: q, out, K and V must be 16-byte aligned", fn);
+  if (!aligned4(end)) return fail(SD_ERR_INVALID_ARG, "%s: end must be 4-byte aligned", fn);
+  if ((rc = check_dense(fn, scale, lse, workspace, ws_bytes, prefix_attend_workspace_bytes(s, p))))
+    return rc;
+  return launch_prefix_attend(s, (const uint16_t*)q, (const uint16_t*)K_prefix,
+                              (const uint16_t*)V_prefix, p, p_cap, (const uint16_t*)K,
+                              (const uint16_t*)V, end, scale, (uint16_t*)out, lse, workspace,
+                              (cudaStream_t)stream);
+}
+
 int sd_delta_select(const sd_shape* shape, const sd_select* sel, const float* scores,
                     const int32_t* idx, int64_t idx_stride, const int32_t* count,
                     int32_t admit_cap, int32_t step, const sd_resident* res,

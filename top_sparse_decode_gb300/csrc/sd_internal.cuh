@@ -209,6 +209,23 @@ int launch_kv4_attend(const Dims& s, const uint16_t* q, const sd_kv4& c, const i
                       int64_t idx_stride, const int32_t* count, int64_t max_count,
                       const int32_t* begin, const int32_t* end, float scale, float* out,
                       float* lse, void* ws, cudaStream_t st);
+// The bf16 cache around the sparse step (sd_rope.cu, sd_dense_attend.cu), strides resolved.
+int launch_norm_rope(const Dims& s, const sd_rope& rope, const uint16_t* q, const sd_strides& qs,
+                     uint16_t* qo, const sd_strides& qos, const uint16_t* k,
+                     const sd_strides& ks, const uint16_t* v, const sd_strides& vs, uint16_t* K,
+                     uint16_t* V, int64_t m, int64_t first, const int32_t* pos,
+                     const int32_t* length, const int32_t* rotary, cudaStream_t st);
+size_t window_attend_workspace_bytes(const Dims& s, int64_t m, int64_t window, int64_t sink);
+int launch_window_attend(const Dims& s, const uint16_t* q, const sd_strides& qs,
+                         const uint16_t* K, const uint16_t* V, int64_t m, int64_t first,
+                         const int32_t* pos, const int32_t* length, int64_t window, int64_t sink,
+                         float scale, uint16_t* out, const sd_strides& os, float* lse, void* ws,
+                         cudaStream_t st);
+size_t prefix_attend_workspace_bytes(const Dims& s, int64_t p);
+int launch_prefix_attend(const Dims& s, const uint16_t* q, const uint16_t* Kp,
+                         const uint16_t* Vp, int64_t p, int64_t pcap, const uint16_t* K,
+                         const uint16_t* V, const int32_t* end, float scale, uint16_t* out,
+                         float* lse, void* ws, cudaStream_t st);
 int launch_offload_gather(const Dims& s, const uint32_t* host_planes, const uint16_t* host_scales,
                           const uint8_t* plan, uint32_t* dev_planes, uint16_t* dev_scales,
                           cudaStream_t st);
