@@ -955,8 +955,14 @@ int sd_set_fallback_paths(int on) {
 }
 
 int sd_device_status(void* stream) {
-  unsigned word = 0;
+  unsigned word = 0, tile = 0;
   if (int rc = scan_error_take((cudaStream_t)stream, &word)) return rc;
+  if (int rc = tile_error_take((cudaStream_t)stream, &tile)) return rc;
+  if (tile)
+    return fail(SD_ERR_TIMEOUT,
+                "sd_device_status: a bounded wait inside a window or prefix attention ran out "
+                "since the last check; it stopped early and its results are incomplete%s",
+                word ? ", and so did a bit-plane scan" : "");
   if (word)
     return fail(SD_ERR_TIMEOUT,
                 "sd_device_status: a bounded wait inside a bit-plane scan ran out since the last "

@@ -79,4 +79,12 @@ __device__ __forceinline__ void dn_row_end(const DnRow& r, uint16_t* out, float*
   if (lse && lane == 0) *lse = r.l == 0.0f ? -INFINITY : (r.m + log2f(r.l)) * kDnLn2;
 }
 
+// sd_dense_stream.cu: one query token per sequence.
+int64_t window_stream_parts(const Dims& s, int64_t tokens);
+int launch_window_stream(const Dims& s, const uint16_t* q, const sd_strides& qs,
+                         const uint16_t* K, const uint16_t* V, const DnWindow& w, bool own,
+                         const int32_t* end, int64_t tokens, float scale, const float* pre_o,
+                         const float2* pre_ml, int pre, uint16_t* out, const sd_strides& os,
+                         float* lse, float* cut_o, float2* cut_ml, int* cut, cudaStream_t st);
+
 }  // namespace sd

@@ -1,0 +1,409 @@
+// Decode attention of one query token per sequence over ranges of its bf16 cache
+// (HashAttention: Semantic Sparsity for Faster Inference, 2.1; 3.1, the first and the latest
+// tokens kept): single tokens under a window with first tokens, and a sequence's own tokens
+// behind a prefix that the batch shares.
+//
+// Bound by HBM: 512 bytes a token and KV head against 4 G products of 128.  A row, a
+// (sequence, KV head) pair, is cut into `parts` CTAs of four warps; warp w takes every fourth
+// group of 16 tokens.  Warps work alone: each keeps a ring of kSwStages groups in shared
+// memory, filled by 16-byte asynchronous copies (chunks XOR-swizzled by token, so that the
+// matrix loads meet no bank twice), 16 KB of a warp in flight, which 8 warps of an SM make
+// 128 KB.  S = Q K^T as m16n8k16 bf16 products (M: the group's heads), p = 2^(s - m) in fp32
+// with the reference m raised only when a group's maximum exceeds it by more than 2^8, O^T +=
+// V^T P^T with p rounded to bf16 and V^T read by transposing matrix loads.
+//
+// Warps of a CTA join through shared memory, CTAs of a row through the cluster's (up to
+// eight), longer cuts through a workspace (dense_join_kernel).  A prefix's partial results
+// (sd_dense_tile.cu) join in the same place.
+#include <atomic>
+
+#include "sd_dense.cuh"
+#include "sd_dense_plan.cuh"
+#include "sd_mma.cuh"
+
+namespace sd {
+namespace {
+
+constexpr int kSwGrp = 16;     // tokens per group
+constexpr int kSwWarps = 4;    // warps per CTA
+constexpr int kSwThreads = 32 * kSwWarps;
+constexpr int kSwStages = 3;
+constexpr uint32_t kSwRow = kD * 2;
+constexpr uint32_t kSwHalf = kSwGrp * kSwRow;  // a group's K: 4 KB; V behind it
+constexpr uint32_t kSwStage = 2 * kSwHalf;
+constexpr size_t kSwSmem = (size_t)kSwWarps * kSwStages * kSwStage;  // 96 KB
+constexpr float kSwSlack = 8.0f;
+
+struct SwArgs {
+  const uint16_t* q;
+  const uint16_t* K;
+  const uint16_t* V;
+  uint16_t* out;
+  float* lse;
+  float* part_o;      // cut through the workspace: [row][head][parts][d], not divided by l
+  float2* part_ml;
+  const float* pre_o; // a prefix's parts: [KV head][sequence][head][pre][d]
+  const float2* pre_ml;
+  int pre;
+  int64_t qseq, qhead, oseq, ohead;
+  DnWindow w;
+  const int32_t* end; // own tokens [0, min(end, n)) instead of a window (own = 1)
+  int own;
+  int B, Hkv, parts, cut;  // cut: parts joined by dense_join_kernel
+  int64_t ncap;
+  float sl2;
+};
+
+__device__ __forceinline__ uint32_t sw_su32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void sw_ldm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void sw_ldmt(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void sw_cp16(uint32_t dst, const uint16_t* src, bool v) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+               "r"(v ? 16 : 0)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void sw_cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t sw_rank_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float sw_ld_rank(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sw_cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;\n" ::
+          : "memory");
+}
+
+template <int G>
+__global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(const SwArgs a) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float2 wml[kSwWarps][8];  // a warp's (m, l) of each head
+  __shared__ float2 cml[8];            // the CTA's
+  __shared__ float co[8][kD];          // and its O
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+  const bool real = gid < G;
+  const int64_t row = blockIdx.x / a.parts;
+  const int part = (int)(blockIdx.x - row * a.parts);
+  const int b = (int)(row / a.Hkv), h = (int)(row - (int64_t)b * a.Hkv);
+
+  DnRanges r;
+  if (a.own) {
+    r = DnRanges{0, 0, a.end ? imax64(0, imin64(a.w.n, a.end[b])) : a.w.n};
+  } else {
+    if (a.w.len(b) < 1) return;  // every CTA of the row
+    const int64_t p = a.w.at(b);
+    r = dn_ranges(a.w, p, p);
+  }
+  const int na = (int)((r.s1 + kSwGrp - 1) / kSwGrp);
+  const int all = na + (int)((r.w1 - r.w0 + kSwGrp - 1) / kSwGrp);
+  const int g0 = (int)((int64_t)all * part / a.parts) + warp;
+  const int g1 = (int)((int64_t)all * (part + 1) / a.parts);
+
+  const uint32_t mine = sw_su32(ring) + warp * kSwStages * kSwStage;
+  const int64_t base = row * a.ncap * kD;
+  const int lr = lane >> 4, lc = lane & 15;
+  auto fetch = [&](int i, int slot) {
+    if (i < g1) {
+      const int64_t c0 = i < na ? (int64_t)i * kSwGrp : r.w0 + (int64_t)(i - na) * kSwGrp;
+      const int have = (int)imin64(kSwGrp, (i < na ? r.s1 : r.w1) - c0);
+      const int64_t at = base + c0 * kD + 8 * lc;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int t = 2 * k + lr;
+        const uint32_t dst = mine + slot * kSwStage + t * kSwRow + ((lc ^ (t & 7)) << 4);
+        const int64_t src = at + (t < have ? t : 0) * kD;
+        sw_cp16(dst, a.K + src, t < have);
+        sw_cp16(dst + kSwHalf, a.V + src, t < have);
+      }
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < kSwStages - 1; ++s) fetch(g0 + s * kSwWarps, s);
+
+  uint32_t qa[8][2];
+  {
+    const uint32_t* q =
+        reinterpret_cast<const uint32_t*>(a.q + b * a.qseq + (h * G + (real ? gid : 0)) * a.qhead);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      qa[kk][0] = real ? q[8 * kk + tig] : 0u;
+      qa[kk][1] = real ? q[8 * kk + 4 + tig] : 0u;
+    }
+  }
+  float o[8][4];
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.0f;
+  float m = -INFINITY, l = 0.0f;
+
+  int slot = 0;
+  for (int i = g0; i < g1; i += kSwWarps) {
+    __syncwarp();  // the slot filled next is read by all
+    fetch(i + (kSwStages - 1) * kSwWarps, slot == 0 ? kSwStages - 1 : slot - 1);
+    sw_cp_wait<kSwStages - 1>();
+    __syncwarp();
+    const uint32_t at = mine + slot * kSwStage;
+    slot = slot == kSwStages - 1 ? 0 : slot + 1;
+    const int64_t c0 = i < na ? (int64_t)i * kSwGrp : r.w0 + (int64_t)(i - na) * kSwGrp;
+    const int have = (int)imin64(kSwGrp, (i < na ? r.s1 : r.w1) - c0);
+    float sc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int t = 8 * n + (lane & 7);
+#pragma unroll
+      for (int kp = 0; kp < 4; ++kp) {
+        uint32_t k[4];
+        sw_ldm(k, at + t * kSwRow + (((4 * kp + (lane >> 3)) ^ (t & 7)) << 4));
+        mma_bf16(sc[n], qa[2 * kp][0], 0u, qa[2 * kp][1], 0u, k[0], k[1]);
+        mma_bf16(sc[n], qa[2 * kp + 1][0], 0u, qa[2 * kp + 1][1], 0u, k[2], k[3]);
+      }
+    }
+    float x[2][2], top = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        x[n][e] = real && 8 * n + 2 * tig + e < have ? sc[n][e] * a.sl2 : -INFINITY;
+        top = fmaxf(top, x[n][e]);
+      }
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const bool need = top > m + kSwSlack;
+    if (__any_sync(0xFFFFFFFFu, need)) {
+      const float f = need ? exp2f(m - top) : 1.0f;  // m = -inf: 0
+      // O^T's columns 2tig, 2tig + 1 are heads whose factors the lanes of S's rows hold
+      const float fa = __shfl_sync(0xFFFFFFFFu, f, 8 * tig);
+      const float fb = __shfl_sync(0xFFFFFFFFu, f, 8 * tig + 4);
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        o[mt][0] *= fa;
+        o[mt][1] *= fb;
+        o[mt][2] *= fa;
+        o[mt][3] *= fb;
+      }
+      l *= f;
+      if (need) m = top;
+    }
+    const float mu = m == -INFINITY ? 0.0f : m;
+    uint32_t p[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const float u = exp2f(x[n][0] - mu), v = exp2f(x[n][1] - mu);
+      l += u + v;
+      p[n] = dn_pack(u, v);
+    }
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      const int t = (lane & 7) + 8 * (lane >> 4);
+      uint32_t v[4];
+      sw_ldmt(v, at + kSwHalf + t * kSwRow + (((2 * mt + ((lane >> 3) & 1)) ^ (t & 7)) << 4));
+      mma_bf16(o[mt], v[0], v[1], v[2], v[3], p[0], p[1]);
+    }
+  }
+  sw_cp_wait<0>();
+
+  // the warp's (m, l, O) into its own part of the ring
+  l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+  l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+  if (tig == 0) wml[warp][gid] = make_float2(m, l);
+  __syncwarp();
+  float* wo = reinterpret_cast<float*>(ring + warp * kSwStages * kSwStage);
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int head = 2 * tig + (e & 1);
+      if (head < G) wo[head * kD + 16 * mt + 8 * (e >> 1) + gid] = o[mt][e];
+    }
+  __syncthreads();
+  const bool joined = a.parts > 1 && !a.cut;
+  const float* all_o = reinterpret_cast<const float*>(ring);
+  constexpr int kStep = kSwStages * kSwStage / sizeof(float);
+#pragma unroll 1
+  for (int g = 0; g < G; ++g) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kSwWarps; ++w) top = fmaxf(top, wml[w][g].x);
+    const float mu = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, acc = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSwWarps; ++w) {
+      const float f = exp2f(wml[w][g].x - mu);
+      sum = fmaf(wml[w][g].y, f, sum);
+      acc = fmaf(all_o[w * kStep + g * kD + tid], f, acc);
+    }
+    if (a.cut) {
+      const int64_t at = (row * G + g) * a.parts + part;
+      a.part_o[at * kD + tid] = acc;
+      if (tid == 0) a.part_ml[at] = make_float2(top, sum);
+    } else {
+      co[g][tid] = acc;
+      if (tid == 0) cml[g] = make_float2(top, sum);
+    }
+  }
+  if (a.cut) return;
+  if (joined)
+    sw_cluster_sync();
+  else
+    __syncthreads();
+  // each CTA of the row finishes its share of the heads
+  const uint32_t ml_at = sw_su32(cml), o_at = sw_su32(co);
+  for (int g = part; g < G; g += a.parts) {
+    const int head = h * G + g;
+    const int64_t pr = ((int64_t)h * a.B + b) * G + g;
+    float top = -INFINITY;
+    for (int s = 0; s < a.parts; ++s)
+      top = fmaxf(top, joined ? sw_ld_rank(sw_rank_addr(ml_at + 8 * g, s)) : cml[g].x);
+    for (int s = 0; s < a.pre; ++s) top = fmaxf(top, a.pre_ml[pr * a.pre + s].x);
+    const float mu = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, acc = 0.0f;
+    for (int s = 0; s < a.parts; ++s) {
+      float mm, ll, oo;
+      if (joined) {
+        mm = sw_ld_rank(sw_rank_addr(ml_at + 8 * g, s));
+        ll = sw_ld_rank(sw_rank_addr(ml_at + 8 * g + 4, s));
+        oo = sw_ld_rank(sw_rank_addr(o_at + 4 * (g * kD + tid), s));
+      } else {
+        mm = cml[g].x, ll = cml[g].y, oo = co[g][tid];
+      }
+      const float f = exp2f(mm - mu);
+      sum = fmaf(ll, f, sum);
+      acc = fmaf(oo, f, acc);
+    }
+#pragma unroll 4
+    for (int s = 0; s < a.pre; ++s) {
+      const float2 y = a.pre_ml[pr * a.pre + s];
+      const float f = exp2f(y.x - mu);
+      sum = fmaf(y.y, f, sum);
+      acc = fmaf(a.pre_o[(pr * a.pre + s) * kD + tid], f, acc);
+    }
+    const float res = sum == 0.0f ? 0.0f : acc / sum;
+    const float next = __shfl_down_sync(0xFFFFFFFFu, res, 1);
+    if (!(tid & 1))
+      *reinterpret_cast<uint32_t*>(a.out + b * a.oseq + head * a.ohead + tid) = dn_pack(res, next);
+    if (a.lse && tid == 0)
+      a.lse[(int64_t)b * a.Hkv * G + head] =
+          sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kDnLn2;
+  }
+  if (joined) sw_cluster_sync();  // the others' shared memory is read
+}
+
+// The largest cluster that this device runs of the kernel (cached per device).
+template <int G>
+int sw_max_cluster() {
+  static std::atomic<int> most[kMaxDev];
+  return per_device_cached(most, [] {
+    if (set_smem_limit((const void*)dense_stream_kernel<G>, kSwSmem, "stream attention") != SD_OK)
+      return 0;
+    int c = 8;
+    for (; c > 1; c >>= 1) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(c, 1, 1);
+      cfg.blockDim = dim3(kSwThreads, 1, 1);
+      cfg.dynamicSmemBytes = kSwSmem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = c;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int nc = 0;
+      if (cudaOccupancyMaxActiveClusters(&nc, dense_stream_kernel<G>, &cfg) == cudaSuccess &&
+          nc > 0)
+        break;
+      cudaGetLastError();
+    }
+    return c;
+  });
+}
+
+template <int G>
+int sw_launch(SwArgs& a, int64_t tokens, float* cut_o, float2* cut_ml, int* cut,
+              cudaStream_t st) {
+  const int64_t rows = (int64_t)a.B * a.Hkv;
+  const SwPlan p = sw_plan(rows, tokens, device_sm_count(),
+                           fallback_forced() ? 1 : sw_max_cluster<G>());
+  a.parts = p.parts;
+  a.cut = p.cut;
+  if (p.cut) {
+    a.part_o = cut_o;
+    a.part_ml = cut_ml;
+  }
+  *cut = p.cut ? p.parts : 0;
+  if (int rc = set_smem_limit((const void*)dense_stream_kernel<G>, kSwSmem, "stream attention"))
+    return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * p.parts), 1, 1);
+  cfg.blockDim = dim3(kSwThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSwSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.parts;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.parts > 1 && !p.cut ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, dense_stream_kernel<G>, (const SwArgs)a) != cudaSuccess)
+    return check_launch("stream attention");
+  note_launches(1);
+  return check_launch("stream attention");
+}
+
+int sw_dispatch(SwArgs& a, int G, int64_t tokens, float* cut_o, float2* cut_ml, int* cut,
+                cudaStream_t st) {
+  // (scale 0 as in the tile kernel: unseen tokens' -inf must stay)
+  switch (G) {
+    case 1: return sw_launch<1>(a, tokens, cut_o, cut_ml, cut, st);
+    case 2: return sw_launch<2>(a, tokens, cut_o, cut_ml, cut, st);
+    case 4: return sw_launch<4>(a, tokens, cut_o, cut_ml, cut, st);
+    default: return sw_launch<8>(a, tokens, cut_o, cut_ml, cut, st);
+  }
+}
+
+}  // namespace
+
+int64_t window_stream_parts(const Dims& s, int64_t tokens) {
+  return (int64_t)s.B * s.Hq * sw_cut((int64_t)s.B * s.Hkv, tokens, device_sm_count());
+}
+
+// One query token per sequence: under the window, or (own) over [0, min(end, n)) with a
+// prefix's parts joined in.  tokens: what a row may see.  *cut: parts left for
+// dense_join_kernel in cut_o, cut_ml (0: out and lse are written).
+int launch_window_stream(const Dims& s, const uint16_t* q, const sd_strides& qs,
+                         const uint16_t* K, const uint16_t* V, const DnWindow& w, bool own,
+                         const int32_t* end, int64_t tokens, float scale, const float* pre_o,
+                         const float2* pre_ml, int pre, uint16_t* out, const sd_strides& os,
+                         float* lse, float* cut_o, float2* cut_ml, int* cut, cudaStream_t st) {
+  SwArgs a = {};
+  a.q = q, a.K = K, a.V = V, a.out = out, a.lse = lse;
+  a.pre_o = pre_o, a.pre_ml = pre_ml, a.pre = pre;
+  a.qseq = qs.seq, a.qhead = qs.head, a.oseq = os.seq, a.ohead = os.head;
+  a.w = w, a.own = own, a.end = end, a.B = s.B, a.Hkv = s.Hkv, a.ncap = s.ncap;
+  a.sl2 = scale * kDnLog2e;
+  return sw_dispatch(a, s.G, tokens, cut_o, cut_ml, cut, st);
+}
+
+}  // namespace sd

@@ -1,0 +1,1060 @@
+// Softmax attention of many query rows over ranges of the bf16 cache on the 5th-generation
+// tensor cores (HashAttention: Semantic Sparsity for Faster Inference, 2.1, the attention
+// over every cached token; 3.1, the first and the latest tokens kept): prompts and chunks
+// under a window with first tokens, and a batch's rows over the prefix that it shares.
+//
+// Rows.  A KV head's query heads share its K and V, so a row is a (token, head of the group)
+// pair, token by token: 256 rows, two tiles of 128, span 256 / G tokens, and what they see is
+// little more than the window.  A work item is two row tiles against the token tiles that
+// any of their rows sees -- [0, s1) and [w0, w1), each cut into tiles of 128 from its start
+// (a TMA load may start at any token) -- or a part of these, whose results join later.  With
+// at most 128 rows (`dual`) both softmax groups take the same rows and every second token
+// tile each, so that one's softmax hides behind the other's products.
+//
+// Per token tile and row tile: S = Q K^T (128 x 128 x 128, both operands from shared memory,
+// fp32 in tensor memory), p = 2^(s - m) by the softmax group whose thread owns the row, p
+// rounded to bf16 into the columns that S held, O += P V (P from tensor memory, V as it
+// lies).  The reference m is raised only when a tile's maximum exceeds it by more than 2^8,
+// and only then O is rescaled (weights are at most 2^8, and exact in their scale).
+//
+// Roles (384 threads, one CTA per SM, persistent over items): warps 0-3 and 4-7 softmax and
+// output of the two row tiles, warp 8 issues the products, warp 9 the TMA loads, warps 10
+// and 11 load Q.  Products are issued PV(0), QK(0) of the next tile, PV(1), QK(1): while one
+// group's scores are in its softmax the tensor cores work for the other.  S and P share
+// columns: QK of the next tile follows PV of this one in the tensor cores' queue.
+//
+// Shared memory: Q 64 KB, a ring of five 32 KB stages for K and V tiles, all in the 128-byte
+// swizzle that the TMA writes.  Tensor memory: S 2 x 128 and O 2 x 128 columns, all 512.
+//
+// What a row does not see reaches nothing of it: scores by selection; V rows behind a
+// range's end are set to zero in shared memory; and where a tile's rows differ in what they
+// see, V is searched for values that are not finite (0 x inf is not 0), and an item that
+// holds one is computed again row by row.
+//
+// Every wait is bounded: one that runs out sets the library's error word (sd_device_status)
+// and ends the CTA's work.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "sd_dense.cuh"
+#include "sd_dense_plan.cuh"
+
+namespace sd {
+
+__device__ unsigned int g_tile_timeout = 0;  // set when a bounded wait of a tile kernel ran out
+
+namespace {
+
+constexpr int kTlThreads = 384;
+constexpr int kTlStages = 5;
+constexpr uint32_t kTlTile = kDtKeys * kD * 2;  // bytes of a K, V or Q tile: 32 KB
+constexpr uint32_t kTlHalf = kTlTile / 2;       // 64 channels of it
+constexpr uint32_t kTlSpin = 1u << 22;          // try_wait rounds before a wait gives up
+constexpr float kTlSlack = 8.0f;                // log2 headroom before m is raised
+
+struct TlSmem {
+  uint8_t q[2][kTlTile];
+  uint8_t ring[kTlStages][kTlTile];
+  unsigned long long full[kTlStages], empty[kTlStages];
+  unsigned long long qfull, qempty;
+  unsigned long long sfull[2], pfull[2], pvdone[2], oempty[2], mlfull, drain;
+  float2 ml[kDtRows];   // dual: the second group's (m, l)
+  int bad[2][2];        // [group][item of the group & 1]: the last such item (counted from 1)
+                        // whose V held a value that is not finite
+  uint32_t tmem;
+  int abort;
+};
+constexpr size_t kTlSmemBytes = sizeof(TlSmem) + 1024;  // the tiles start on 1 KB
+
+struct TlArgs {
+  const uint16_t* q;
+  const uint16_t* K;
+  const uint16_t* V;
+  uint16_t* out;      // splits == 1: the result
+  float* lse;
+  float* part_o;      // parts: [row][splits][d], not divided by l
+  float2* part_ml;    // [row][splits]: (m in log2 units, l)
+  sd_strides qs, os;
+  DnWindow w;         // m: query tokens per sequence
+  int causal;         // 0: every row sees [0, w.n)
+  int Hkv, G, lg;     // lg: log2 G
+  int64_t ncap;
+  float sl2;          // scale * log2(e), above 0
+  int dual, splits, wide;  // wide: rows of out on 32 bytes
+  int parts_only;          // splits == 1 leaves a partial result, too
+  int64_t per, items, bh;
+};
+
+// ---- PTX ---------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t tl_su32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void tl_init(unsigned long long* b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(tl_su32(b)), "r"(count)
+               : "memory");
+}
+__device__ __forceinline__ void tl_arrive(unsigned long long* b) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n" ::"r"(tl_su32(b))
+               : "memory");
+}
+__device__ __forceinline__ bool tl_try(unsigned long long* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(tl_su32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for the phase of the given parity to complete; false once the rounds ran out or
+// another thread of the CTA gave up.
+__device__ __forceinline__ bool tl_wait(int* abort, unsigned long long* b, uint32_t parity) {
+  for (uint32_t i = 0; i < kTlSpin; ++i) {
+    if (tl_try(b, parity)) return true;
+    if (*(volatile int*)abort) return false;
+  }
+  *(volatile int*)abort = 1;
+  atomicOr(&g_tile_timeout, 1u);
+  return false;
+}
+// ... by a whole warp, with one answer.
+__device__ __forceinline__ bool tl_wait_warp(int* abort, unsigned long long* b, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, tl_wait(abort, b, parity));
+}
+// The same without a look at the others: for copies in flight when the CTA gives up.
+__device__ __forceinline__ void tl_drain(unsigned long long* b, uint32_t parity) {
+  for (uint32_t i = 0; i < kTlSpin && !tl_try(b, parity); ++i) {
+  }
+}
+__device__ __forceinline__ void tl_tma(void* dst, const CUtensorMap* map, int c, int tok, int row,
+                                       unsigned long long* b) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(tl_su32(dst)),
+      "l"(map), "r"(c), "r"(tok), "r"(row), "r"(tl_su32(b))
+      : "memory");
+}
+__device__ __forceinline__ void tl_commit(unsigned long long* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(
+                   tl_su32(b))
+               : "memory");
+}
+__device__ __forceinline__ void tl_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+}
+__device__ __forceinline__ void tl_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+}
+// What was loaded may be used (tl_use32: these 32 registers, none earlier than here).
+__device__ __forceinline__ void tl_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void tl_use32(uint32_t* r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+               :: "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]) :: "memory");
+}
+__device__ __forceinline__ void tl_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+// 32 columns of the thread's lane
+__device__ __forceinline__ void tl_ld32(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tl_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31, %32};\n" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// Shared-memory operand in the 128-byte swizzle: 8-row groups 1 KB apart; lbo: for an operand
+// whose rows are the product's inner dimension (V), its next 64 columns.
+__device__ __forceinline__ uint64_t tl_desc(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
+         ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// bf16 x bf16 -> fp32, 128 x 128; bit 16: B's rows are the inner dimension
+constexpr uint32_t kTlInstr = (1u << 4) | (1u << 7) | (1u << 10) | ((128u / 8) << 17) |
+                              ((128u / 16) << 24);
+constexpr uint32_t kTlInstrV = kTlInstr | (1u << 16);
+
+__device__ __forceinline__ void tl_qk(uint32_t s, uint32_t q, uint32_t k) {
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {  // 16 channels each: 32 bytes of a 64-channel half
+    const uint32_t off = (kk >> 2) * kTlHalf + (kk & 3) * 32;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(s),
+        "l"(tl_desc(q + off, 16)), "l"(tl_desc(k + off, 16)), "r"(kTlInstr), "r"((uint32_t)(kk > 0))
+        : "memory");
+  }
+}
+__device__ __forceinline__ void tl_pv(uint32_t o, uint32_t p, uint32_t v, bool add) {
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {  // 16 tokens each: two 8-row groups; 8 columns of P
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(o),
+        "r"(p + 8 * kk), "l"(tl_desc(v + 2048 * kk, kTlHalf)), "r"(kTlInstrV),
+        "r"((uint32_t)(add || kk > 0))
+        : "memory");
+  }
+}
+// Pairs of fp32 values, one instruction for both.
+__device__ __forceinline__ uint64_t tl_two(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void tl_of(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t tl_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t tl_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float tl_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---- work --------------------------------------------------------------------------------
+// One item: rows [r0, r0 + rows) of (sequence, KV head) bh, token tiles [ta, tb) of the
+// item's list (tiles of [0, s1), then of [w0, w1)).
+struct TlItem {
+  int64_t bh, r0;
+  int b, h, rows, split;
+  int64_t p0;        // position of query token 0
+  DnRanges r;
+  int na, ta, tb;    // tiles of [0, s1); this part's tiles
+  int t[2];          // token tiles of each softmax group
+  int nq;            // row tiles (dual: 2 groups of one)
+};
+
+__device__ __forceinline__ TlItem tl_item(const TlArgs& a, int64_t id) {
+  TlItem x;
+  x.split = (int)(id % a.splits);
+  const int64_t rest = id / a.splits;
+  x.bh = rest % a.bh;
+  // the last rows first: under a causal mask they see most
+  const int64_t tile = a.per - 1 - rest / a.bh;
+  x.b = (int)(x.bh / a.Hkv);
+  x.h = (int)(x.bh - (int64_t)x.b * a.Hkv);
+  const int64_t len = a.causal ? a.w.len(x.b) : a.w.m;
+  x.r0 = tile * (a.dual ? kDtRows : kDtPair);
+  x.rows = (int)imax64(0, imin64(a.dual ? kDtRows : kDtPair, len * a.G - x.r0));
+  x.p0 = a.causal ? a.w.at(x.b) : 0;
+  x.ta = x.tb = x.na = 0;
+  x.t[0] = x.t[1] = 0;
+  x.nq = a.dual || x.rows > kDtRows ? 2 : 1;
+  if (!x.rows) return x;
+  if (a.causal) {
+    const int64_t pa = x.p0 + (x.r0 >> a.lg), pb = x.p0 + ((x.r0 + x.rows - 1) >> a.lg);
+    // [0, s1) and [w0, w1) of all rows: the first row's window start, the last row's end
+    DnRanges& r = x.r;
+    r.w1 = imax64(0, imin64(a.w.n, pb + 1));
+    r.w0 = imax64(0, imin64(pa - a.w.window + 1, r.w1));
+    r.s1 = imin64(imin64(a.w.sink, a.w.n), r.w1);
+    if (r.s1 >= r.w0) r.s1 = 0, r.w0 = 0;
+  } else {
+    x.r = DnRanges{0, 0, a.w.n};
+  }
+  x.na = (int)((x.r.s1 + kDtKeys - 1) / kDtKeys);
+  const int all = x.na + (int)((x.r.w1 - x.r.w0 + kDtKeys - 1) / kDtKeys);
+  x.ta = (int)((int64_t)all * x.split / a.splits);
+  x.tb = (int)((int64_t)all * (x.split + 1) / a.splits);
+  const int t = x.tb - x.ta;
+  if (a.dual) {
+    x.t[0] = (t + 1) / 2;
+    x.t[1] = t / 2;
+  } else {
+    x.t[0] = t;
+    x.t[1] = x.nq == 2 ? t : 0;
+  }
+  return x;
+}
+// Tile i of the list: its first token and its range's end.
+__device__ __forceinline__ void tl_tile(const TlItem& x, int i, int64_t& c0, int64_t& end) {
+  if (i < x.na) {
+    c0 = (int64_t)i * kDtKeys;
+    end = x.r.s1;
+  } else {
+    c0 = x.r.w0 + (int64_t)(i - x.na) * kDtKeys;
+    end = x.r.w1;
+  }
+}
+// The list's tile that group g takes j-th.
+__device__ __forceinline__ int tl_index(const TlArgs& a, const TlItem& x, int g, int j) {
+  return x.ta + (a.dual ? 2 * j + g : j);
+}
+// Ring positions (counted from the item's first) of group g's j-th K and V.  Loads go K, V,
+// K, V, ..; dual: K0, K1, V0, V1, ...
+__device__ __forceinline__ uint32_t tl_kpos(const TlArgs& a, int g, int j) {
+  return a.dual ? 4u * j + g : 2u * j;
+}
+__device__ __forceinline__ uint32_t tl_vpos(const TlArgs& a, const TlItem& x, int g, int j) {
+  return a.dual ? 4u * j + (j < x.t[1] ? 2 : 1) + g : 2u * j + 1;
+}
+__device__ __forceinline__ uint32_t tl_loads(const TlArgs& a, const TlItem& x) {
+  return 2u * (a.dual ? x.t[0] + x.t[1] : x.t[0]);
+}
+
+// A row's own (m, l, O) from the cache, its warp together: the tokens of the part's tiles
+// that it sees.  For items whose V holds values that are not finite.
+__device__ __noinline__ void tl_row_again(const TlArgs& a, const TlItem& x, int64_t row, DnRow& r,
+                                          int lane) {
+  const int64_t t = row >> a.lg;
+  const int g = (int)(row & (a.G - 1));
+  dn_row_begin(r, a.q + x.b * a.qs.seq + (int64_t)(x.h * a.G + g) * a.qs.head + t * a.qs.token,
+               a.sl2, lane);
+  const int64_t base = x.bh * a.ncap * kD, p = x.p0 + t;
+  for (int i = x.ta; i < x.tb; ++i) {
+    int64_t c0, end;
+    tl_tile(x, i, c0, end);
+    end = imin64(end, c0 + kDtKeys);
+    if (a.causal) {
+      end = imin64(end, p + 1);
+      const int64_t w = imax64(c0, p - a.w.window + 1);
+      const int64_t s = imin64(imin64(end, a.w.sink), w);  // first tokens before the window
+      dn_row_over(r, a.K + base, a.V + base, c0, s, lane);
+      c0 = imax64(c0, w);
+    }
+    dn_row_over(r, a.K + base, a.V + base, c0, end, lane);
+  }
+}
+
+// Softmax of the item's row tile `g` (dual: of every second token tile), and its result.
+__device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, uint32_t tmem) {
+  const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
+  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+  const uint32_t s_at = tmem + lanes + 128 * g, o_at = tmem + lanes + 256 + 128 * g;
+  uint32_t base = 0;   // ring position of the item's first load
+  uint32_t done = 0;   // tiles of this group so far
+  uint32_t done1 = 0;  // dual: tiles of the second group up to this item's end
+  int mine_n = 0;      // items in which this group had tiles
+  int other_n = 0;     // dual: items in which the second group had
+  for (int64_t id = blockIdx.x; id < a.items; id += gridDim.x) {
+    const TlItem x = tl_item(a, id);
+    if (!x.rows) continue;
+    const int T = x.t[g];
+    const int local = (a.dual ? 0 : kDtRows * g) + tid;  // row of the item
+    const int64_t row = x.r0 + local;
+    const bool mine = local < x.rows;
+    const bool warp_on = (a.dual ? 0 : kDtRows * g) + 32 * warp < x.rows;
+    const int64_t p = x.p0 + ((x.r0 + min(local, x.rows - 1)) >> a.lg);
+    // positions of this row tile's first and last row
+    const int64_t pa = x.p0 + ((x.r0 + (a.dual ? 0 : kDtRows * g)) >> a.lg);
+    const int64_t pb =
+        x.p0 + ((x.r0 + min((a.dual ? 0 : kDtRows * g) + kDtRows, x.rows) - 1) >> a.lg);
+    float m = -INFINITY, l = 0.0f;
+    if (g == 1 && (x.nq == 1 || (a.dual && T == 0))) {  // nothing of the item is this group's
+      base += tl_loads(a, x);
+      continue;
+    }
+    if (T > 0) ++mine_n;
+    if (a.dual && x.t[1] > 0) ++other_n;
+    if (a.dual) done1 += x.t[1];
+    for (int j = 0; j < T; ++j) {
+      int64_t c0, end;
+      tl_tile(x, tl_index(a, x, g, j), c0, end);
+      const int have = (int)imin64(kDtKeys, end - c0);
+      // whether all rows of the tile see all that it holds
+      const bool same = !a.causal || (c0 + have - 1 <= pa &&
+                                      (c0 + have <= a.w.sink || c0 > pb - a.w.window));
+      if (!tl_wait_warp(&sm.abort, &sm.sfull[g], done & 1)) return;
+      tl_fence_after();
+      if (warp_on) {
+        uint32_t sr[kDtKeys];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tl_ld32(sr + 32 * c, s_at + 32 * c);
+        tl_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tl_use32(sr + 32 * c);
+        float s[kDtKeys];
+#pragma unroll
+        for (int i = 0; i < kDtKeys; ++i) s[i] = __uint_as_float(sr[i]);
+        if (!same || have < kDtKeys) {
+          int hi = have, lo = -1, sk = kDtKeys;
+          if (a.causal) {
+            hi = (int)imax64(0, imin64(hi, p + 1 - c0));
+            sk = (int)imax64(0, imin64(kDtKeys, a.w.sink - c0));
+            lo = (int)imax64(-1, imin64(kDtKeys, p - a.w.window - c0));
+          }
+#pragma unroll
+          for (int i = 0; i < kDtKeys; ++i)
+            if (i >= hi || (i <= lo && i >= sk)) s[i] = -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kDtKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sl2;
+        const bool need = top > m + kTlSlack;
+        if (__any_sync(0xFFFFFFFFu, need)) {
+          const float f = need ? tl_exp2(m - top) : 1.0f;  // m = -inf: 0
+          if (j > 0) {
+            if (!tl_wait_warp(&sm.abort, &sm.pvdone[g], (done - 1) & 1)) return;
+            tl_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tl_ld32(o, o_at + 32 * c);
+              tl_wait_ld();
+              tl_use32(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tl_st32(o_at + 32 * c, o);
+            }
+          }
+          l *= f;
+          if (need) m = top;
+        }
+        const float mu = m == -INFINITY ? 0.0f : m;
+        const uint64_t sl = tl_two(a.sl2, a.sl2), mm = tl_two(-mu, -mu);
+        uint64_t sum0 = 0, sum1 = 0;  // pairs of +0
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int k = 64 * c + 2 * i;
+            float u, v;
+            tl_of(tl_fma2(tl_two(s[k], s[k + 1]), sl, mm), u, v);
+            u = tl_exp2(u);
+            v = tl_exp2(v);
+            if (i & 1)
+              sum1 = tl_add2(sum1, tl_two(u, v));
+            else
+              sum0 = tl_add2(sum0, tl_two(u, v));
+            pk[i] = dn_pack(u, v);
+          }
+          tl_st32(s_at + 32 * c, pk);
+        }
+        float u, v;
+        tl_of(tl_add2(sum0, sum1), u, v);
+        l += u + v;
+        tl_wait_st();
+      }
+      if (have < kDtKeys || !same) {
+        // V rows behind the range's end become zero; rows that some do not see are searched
+        // for values that are not finite
+        const uint32_t pos = base + tl_vpos(a, x, g, j);
+        const uint32_t st = pos % kTlStages;
+        if (!tl_wait_warp(&sm.abort, &sm.full[st], (pos / kTlStages) & 1)) return;
+        uint4* v = reinterpret_cast<uint4*>(sm.ring[st]) + tid;
+        uint32_t worst = 0;  // largest magnitude bits of a half (exponent all ones: not finite)
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+          if ((((tid >> 3) + 16 * k) & 127) >= have) {
+            v[128 * k] = make_uint4(0u, 0u, 0u, 0u);
+          } else if (!same) {
+            const uint4 y = v[128 * k];
+            worst = __vmaxu2(worst, y.x & 0x7FFF7FFFu);
+            worst = __vmaxu2(worst, y.y & 0x7FFF7FFFu);
+            worst = __vmaxu2(worst, y.z & 0x7FFF7FFFu);
+            worst = __vmaxu2(worst, y.w & 0x7FFF7FFFu);
+          }
+        }
+        if ((worst & 0xFFFFu) >= 0x7F80u || (worst >> 16) >= 0x7F80u)
+          *(volatile int*)&sm.bad[g][mine_n & 1] = mine_n;
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      }
+      tl_fence_before();
+      tl_arrive(&sm.pfull[g]);
+      ++done;
+    }
+    base += tl_loads(a, x);
+    if (T > 0) {
+      if (!tl_wait_warp(&sm.abort, &sm.pvdone[g], (done - 1) & 1)) return;
+      tl_fence_after();
+    }
+    if (a.dual && g == 1) {
+      sm.ml[tid] = make_float2(m, l);
+      // read by the first group before it gives O back, which this group's next item needs
+      tl_arrive(&sm.mlfull);
+      continue;
+    }
+    if (a.dual && x.t[1] > 0) {
+      if (!tl_wait_warp(&sm.abort, &sm.mlfull, (other_n - 1) & 1)) return;
+      if (!tl_wait_warp(&sm.abort, &sm.pvdone[1], (done1 - 1) & 1)) return;
+      tl_fence_after();
+    }
+    // all threads of a group have searched their parts of V before its last product
+    bool again = T > 0 && *(volatile int*)&sm.bad[g][mine_n & 1] == mine_n;
+    if (a.dual && x.t[1] > 0)
+      again = again || *(volatile int*)&sm.bad[1][other_n & 1] == other_n;
+    float f0 = 1.0f, f1 = 0.0f;
+    if (a.dual && x.t[1] > 0) {
+      const float2 y = sm.ml[tid];
+      const float top = fmaxf(m, y.x), mu = top == -INFINITY ? 0.0f : top;
+      f0 = exp2f(m - mu);
+      f1 = exp2f(y.x - mu);
+      l = l * f0 + y.y * f1;
+      m = top;
+    }
+    const int64_t t = row >> a.lg;
+    const int head = x.h * a.G + (int)(row & (a.G - 1));
+    const int64_t prow = (x.bh * a.w.m * a.G + row) * a.splits + x.split;
+    const int64_t orow = x.b * a.os.seq + head * a.os.head + t * a.os.token;
+    if (!again) {
+      const bool final = a.splits == 1 && !a.parts_only;
+      if (final) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        f0 *= inv;
+        f1 *= inv;
+      }
+      if (warp_on) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          if (x.t[0] > 0) {
+            tl_ld32(o, o_at + 32 * c);
+            tl_wait_ld();
+            tl_use32(o);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = x.t[0] > 0 ? __float_as_uint(__uint_as_float(o[i]) * f0) : 0u;
+          if (a.dual && x.t[1] > 0) {
+            uint32_t o1[32];
+            tl_ld32(o1, o_at + 128 + 32 * c);
+            tl_wait_ld();
+            tl_use32(o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o[i])));
+          }
+          if (mine && final) {
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              y[i] = l == 0.0f ? 0u
+                               : dn_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            uint16_t* dst = a.out + orow + 32 * c;
+            if (a.wide) {  // whole 32-byte sectors
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(
+                                 dst + 16 * i),
+                             "r"(y[8 * i]), "r"(y[8 * i + 1]), "r"(y[8 * i + 2]), "r"(y[8 * i + 3]),
+                             "r"(y[8 * i + 4]), "r"(y[8 * i + 5]), "r"(y[8 * i + 6]),
+                             "r"(y[8 * i + 7])
+                             : "memory");
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(dst + 8 * i) =
+                    make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            }
+          } else if (mine) {
+            float* dst = a.part_o + prow * kD + 32 * c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(
+                               dst + 8 * i),
+                           "r"(o[8 * i]), "r"(o[8 * i + 1]), "r"(o[8 * i + 2]), "r"(o[8 * i + 3]),
+                           "r"(o[8 * i + 4]), "r"(o[8 * i + 5]), "r"(o[8 * i + 6]),
+                           "r"(o[8 * i + 7])
+                           : "memory");
+          }
+        }
+      }
+      if (mine) {
+        if (!final)
+          a.part_ml[prow] = make_float2(m, l);
+        else if (a.lse)
+          a.lse[((int64_t)x.b * a.Hkv * a.G + head) * a.w.m + t] =
+              l == 0.0f ? -INFINITY : (m + log2f(l)) * kDnLn2;
+      }
+    } else {
+      for (int i = 0; i < 32; ++i) {
+        const int li = (a.dual ? 0 : kDtRows * g) + 32 * warp + i;
+        if (li >= x.rows) break;
+        const int64_t rw = x.r0 + li;
+        DnRow r;
+        tl_row_again(a, x, rw, r, lane);
+        const int hd = x.h * a.G + (int)(rw & (a.G - 1));
+        const int64_t tt = rw >> a.lg;
+        if (a.splits == 1 && !a.parts_only) {
+          dn_row_end(r, a.out + x.b * a.os.seq + hd * a.os.head + tt * a.os.token,
+                     a.lse ? a.lse + ((int64_t)x.b * a.Hkv * a.G + hd) * a.w.m + tt : nullptr,
+                     lane);
+        } else {
+          const int64_t pr = (x.bh * a.w.m * a.G + rw) * a.splits + x.split;
+          reinterpret_cast<float4*>(a.part_o + pr * kD)[lane] = r.o;
+          if (lane == 0) a.part_ml[pr] = make_float2(r.m, r.l);
+        }
+      }
+    }
+    tl_fence_before();
+    if (T > 0) tl_arrive(&sm.oempty[g]);
+    if (a.dual && x.t[1] > 0) tl_arrive(&sm.oempty[1]);
+  }
+}
+
+// One thread issues every product of the CTA.
+__device__ __forceinline__ bool tl_products(TlSmem& sm, const TlArgs& a, uint32_t tmem) {
+  uint32_t base = 0, items = 0, tiles[2] = {0, 0}, outs[2] = {0, 0};
+  const uint32_t q_at = tl_su32(sm.q[0]), ring = tl_su32(sm.ring[0]);
+  auto stage = [&](uint32_t pos) { return ring + (pos % kTlStages) * kTlTile; };
+  auto loaded = [&](uint32_t pos) {
+    return tl_wait(&sm.abort, &sm.full[pos % kTlStages], (pos / kTlStages) & 1);
+  };
+  for (int64_t id = blockIdx.x; id < a.items; id += gridDim.x) {
+    const TlItem x = tl_item(a, id);
+    if (x.tb == x.ta) continue;
+    if (!tl_wait(&sm.abort, &sm.qfull, items & 1)) return false;
+    int left = x.t[0] + x.t[1];  // score products still to issue
+    for (int g = 0; g < 2; ++g) {
+      if (x.t[g] == 0) continue;
+      const uint32_t kp = base + tl_kpos(a, g, 0);
+      if (!loaded(kp)) return false;
+      tl_fence_after();
+      tl_qk(tmem + 128 * g, q_at + (a.dual ? 0 : g * kTlTile), stage(kp));
+      tl_commit(&sm.sfull[g]);
+      --left;
+      if (a.dual || g == x.nq - 1) tl_commit(&sm.empty[kp % kTlStages]);
+    }
+    if (left == 0) tl_commit(&sm.qempty);
+    for (int j = 0; j < x.t[0]; ++j) {
+      for (int g = 0; g < 2; ++g) {
+        if (j >= x.t[g]) continue;
+        const bool last = a.dual || g == x.nq - 1;  // the stage's last reader
+        const uint32_t vp = base + tl_vpos(a, x, g, j);
+        if (!loaded(vp)) return false;
+        if (!tl_wait(&sm.abort, &sm.pfull[g], tiles[g] & 1)) return false;
+        ++tiles[g];
+        if (j == 0) {  // O of the item before is read
+          if (outs[g] && !tl_wait(&sm.abort, &sm.oempty[g], (outs[g] - 1) & 1)) return false;
+          ++outs[g];
+        }
+        tl_fence_after();
+        tl_pv(tmem + 256 + 128 * g, tmem + 128 * g, stage(vp), j > 0);
+        tl_commit(&sm.pvdone[g]);
+        if (last) tl_commit(&sm.empty[vp % kTlStages]);
+        if (j + 1 < x.t[g]) {
+          const uint32_t kp = base + tl_kpos(a, g, j + 1);
+          if (!loaded(kp)) return false;
+          tl_fence_after();
+          tl_qk(tmem + 128 * g, q_at + (a.dual ? 0 : g * kTlTile), stage(kp));
+          tl_commit(&sm.sfull[g]);
+          if (last) tl_commit(&sm.empty[kp % kTlStages]);
+          if (--left == 0) tl_commit(&sm.qempty);
+        }
+      }
+    }
+    base += tl_loads(a, x);
+    ++items;
+  }
+  // arrivals of the last commits are in before the CTA ends
+  return !items || tl_wait(&sm.abort, &sm.qempty, (items - 1) & 1);
+}
+
+// One thread issues every K and V load of the CTA.
+__device__ __forceinline__ void tl_loader(TlSmem& sm, const TlArgs& a, const CUtensorMap* mk,
+                                          const CUtensorMap* mv) {
+  uint32_t n = 0;
+  bool ok = true;
+  auto load = [&](const CUtensorMap* map, const TlItem& x, int tile) {
+    const uint32_t st = n % kTlStages, round = n / kTlStages;
+    if (round && !tl_wait(&sm.abort, &sm.empty[st], (round - 1) & 1)) return false;
+    int64_t c0, end;
+    tl_tile(x, tile, c0, end);
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n" ::"r"(
+                     tl_su32(&sm.full[st])),
+                 "r"(kTlTile)
+                 : "memory");
+    tl_tma(sm.ring[st], map, 0, (int)c0, (int)x.bh, &sm.full[st]);
+    tl_tma(sm.ring[st] + kTlHalf, map, 64, (int)c0, (int)x.bh, &sm.full[st]);
+    ++n;
+    return true;
+  };
+  for (int64_t id = blockIdx.x; ok && id < a.items; id += gridDim.x) {
+    const TlItem x = tl_item(a, id);
+    if (x.tb == x.ta) continue;
+    for (int j = 0; ok && j < x.t[0]; ++j) {
+      if (!a.dual) {
+        ok = load(mk, x, x.ta + j) && load(mv, x, x.ta + j);
+      } else {
+        const int i = x.ta + 2 * j;
+        const bool two = j < x.t[1];
+        ok = load(mk, x, i) && (!two || load(mk, x, i + 1)) && load(mv, x, i) &&
+             (!two || load(mv, x, i + 1));
+      }
+    }
+  }
+  // every load has landed and every stage is released before the CTA ends
+  const uint32_t first = n > kTlStages ? n - kTlStages : 0;
+  for (uint32_t i = first; i < n; ++i) {
+    const uint32_t st = i % kTlStages, par = (i / kTlStages) & 1;
+    if (ok) ok = tl_wait(&sm.abort, &sm.empty[st], par);
+    if (!ok) tl_drain(&sm.full[st], par);
+  }
+}
+
+// Two warps load each item's query rows, in the swizzle of the products.
+__device__ __forceinline__ void tl_queries(TlSmem& sm, const TlArgs& a) {
+  const int tid = threadIdx.x - 320;
+  uint32_t items = 0;
+  for (int64_t id = blockIdx.x; id < a.items; id += gridDim.x) {
+    const TlItem x = tl_item(a, id);
+    if (x.tb == x.ta) continue;
+    if (items && !tl_wait_warp(&sm.abort, &sm.qempty, (items - 1) & 1)) return;
+    const int rows = a.dual ? kDtRows : x.nq * kDtRows;
+    const int c = tid & 15;
+    for (int r = tid >> 4; r < rows; r += 4) {
+      const int64_t row = x.r0 + min(r, x.rows - 1);
+      const int64_t t = row >> a.lg;
+      const int head = x.h * a.G + (int)(row & (a.G - 1));
+      const uint16_t* src = a.q + x.b * a.qs.seq + head * a.qs.head + t * a.qs.token + 8 * c;
+      const uint32_t dst = tl_su32(sm.q[r >> 7]) + (c >> 3) * kTlHalf + (r & 127) * 128 +
+                           (((c & 7) ^ (r & 7)) << 4);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+                   "r"(r < x.rows ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;\n" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    tl_arrive(&sm.qfull);
+    ++items;
+  }
+}
+
+__global__ void __launch_bounds__(kTlThreads, 1)
+    dense_tile_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                      const __grid_constant__ TlArgs a) {
+  extern __shared__ uint8_t raw[];
+  TlSmem& sm = *reinterpret_cast<TlSmem*>(raw + ((1024u - (tl_su32(raw) & 1023u)) & 1023u));
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTlStages; ++i) {
+      tl_init(&sm.full[i], 1);
+      tl_init(&sm.empty[i], 1);
+    }
+    tl_init(&sm.qfull, 64);
+    tl_init(&sm.qempty, 1);
+    for (int g = 0; g < 2; ++g) {
+      tl_init(&sm.sfull[g], 1);
+      tl_init(&sm.pfull[g], 128);
+      tl_init(&sm.pvdone[g], 1);
+      tl_init(&sm.oempty[g], 128);
+      sm.bad[g][0] = sm.bad[g][1] = 0;
+    }
+    tl_init(&sm.mlfull, 128);
+    tl_init(&sm.drain, 1);
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
+                     tl_su32(&sm.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  tl_fence_before();
+  __syncthreads();
+  tl_fence_after();
+  const uint32_t tmem = sm.tmem;
+  // 384 x 168 registers at launch: 256 x 208 + 128 x 80
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+    tl_softmax(sm, a, warp >> 2, tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+    if (warp == 8) {
+      if ((threadIdx.x & 31) == 0 && !tl_products(sm, a, tmem)) {
+        tl_commit(&sm.drain);  // gave up: the products in flight end before tensor memory goes
+        tl_drain(&sm.drain, 0);
+      }
+    } else if (warp == 9) {
+      if ((threadIdx.x & 31) == 0) tl_loader(sm, a, &mk, &mv);
+    } else {
+      tl_queries(sm, a);
+    }
+    __syncwarp();
+  }
+  tl_fence_before();
+  __syncthreads();
+  tl_fence_after();
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+}
+
+// ---- joining parts -----------------------------------------------------------------------
+// A warp per row: out and lse of up to two sets of partial results (m, l, O).
+struct TlJoin {
+  const float* ao;
+  const float2* aml;
+  const float* bo;
+  const float2* bml;
+  int na, nb;
+  uint16_t* out;
+  float* lse;
+  sd_strides os;
+  DnWindow w;
+  int causal;        // rows of tokens behind a sequence's length are left alone
+  int Hq, Hkv, G;
+  int64_t B, rows;   // rows: B * Hq * m
+};
+
+__global__ void __launch_bounds__(128) dense_join_kernel(TlJoin a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (i >= a.rows) return;
+  const int64_t m = a.w.m, bhq = i / m, t = i - bhq * m;
+  const int64_t b = bhq / a.Hq;
+  const int h = (int)(bhq - b * a.Hq), kv = h / a.G, g = h - kv * a.G;
+  if (a.causal && t >= a.w.len((int)b)) return;
+  // set A's rows: (sequence, KV head, token, head of the group), or, for a prefix, (KV head,
+  // sequence, head); set B's: (sequence, KV head, head)
+  const int64_t ra = a.causal ? ((b * a.Hkv + kv) * m + t) * a.G + g : (kv * a.B + b) * a.G + g;
+  const int64_t rb = (b * a.Hkv + kv) * a.G + g;
+  const int n = a.na + a.nb;
+  auto ml = [&](int p) {
+    return p < a.na ? a.aml[ra * a.na + p] : a.bml[rb * a.nb + p - a.na];
+  };
+  float top = -INFINITY;
+  for (int p = lane; p < n; p += 32) top = fmaxf(top, ml(p).x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const float mu = top == -INFINITY ? 0.0f : top;
+  float l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int p0 = 0; p0 < n; p0 += 32) {
+    float f = 0.0f, fl = 0.0f;
+    if (p0 + lane < n) {
+      const float2 x = ml(p0 + lane);
+      f = exp2f(x.x - mu);  // an empty part: 0
+      fl = x.x == -INFINITY && x.y == 0.0f ? 0.0f : f * x.y;
+    }
+    l += fl;
+#pragma unroll 4
+    for (int p = p0; p < min(n, p0 + 32); ++p) {
+      const float w = __shfl_sync(0xFFFFFFFFu, f, p - p0);
+      const float* src = p < a.na ? a.ao + (ra * a.na + p) * kD : a.bo + (rb * a.nb + p - a.na) * kD;
+      const float4 v = reinterpret_cast<const float4*>(src)[lane];
+      o.x = fmaf(v.x, w, o.x);
+      o.y = fmaf(v.y, w, o.y);
+      o.z = fmaf(v.z, w, o.z);
+      o.w = fmaf(v.w, w, o.w);
+    }
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
+  DnRow r;
+  r.o = o, r.m = top, r.l = l;
+  dn_row_end(r, a.out + b * a.os.seq + h * a.os.head + t * a.os.token, a.lse ? a.lse + i : nullptr,
+             lane);
+}
+
+// ---- host --------------------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The tensor map of a cache [rows][ncap][d] whose first n tokens exist: boxes of 64 channels
+// x 128 tokens, zeros behind n.
+int tl_map(CUtensorMap* map, const uint16_t* base, int64_t n, int64_t ncap, int64_t rows) {
+  static std::atomic<EncodeFn> known{nullptr};
+  EncodeFn fn = known.load(std::memory_order_acquire);
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult res;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &res) != cudaSuccess ||
+        res != cudaDriverEntryPointSuccess || !p) {
+      cudaGetLastError();
+      return fail(SD_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    }
+    fn = reinterpret_cast<EncodeFn>(p);
+    known.store(fn, std::memory_order_release);
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)n, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {kD * 2, (cuuint64_t)ncap * kD * 2};
+  const cuuint32_t box[3] = {64, kDtKeys, 1}, one[3] = {1, 1, 1};
+  const CUresult rc =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box,
+         one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (rc != CUDA_SUCCESS) return fail(SD_ERR_CUDA, "cuTensorMapEncodeTiled: %d", (int)rc);
+  return SD_OK;
+}
+
+int tl_launch(TlArgs& a, int64_t rows_bh, const DtPlan& p, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (int rc = tl_map(&mk, a.K, a.w.n, a.ncap, rows_bh)) return rc;
+  if (int rc = tl_map(&mv, a.V, a.w.n, a.ncap, rows_bh)) return rc;
+  a.lg = a.G == 8 ? 3 : a.G == 4 ? 2 : a.G - 1;
+  // scale 0: every score 0, as a product with a factor this small gives (0 would turn the
+  // -inf of unseen tokens into NaN)
+  a.sl2 = fmaxf(a.sl2, 1e-36f);
+  a.dual = p.dual;
+  a.splits = p.splits;
+  a.per = p.per;
+  a.items = p.items;
+  a.bh = rows_bh;
+  a.wide = ((uintptr_t)a.out & 31) == 0 && a.os.seq % 16 == 0 && a.os.head % 16 == 0 &&
+           a.os.token % 16 == 0;
+  if (int rc = set_smem_limit((const void*)dense_tile_kernel, kTlSmemBytes, "tile attention"))
+    return rc;
+  const unsigned grid = (unsigned)imin64(p.items, device_sm_count());
+  dense_tile_kernel<<<grid, kTlThreads, kTlSmemBytes, st>>>(mk, mv, a);
+  note_launches(1);
+  return check_launch("tile attention");
+}
+
+int tl_join(const TlJoin& j, cudaStream_t st) {
+  dense_join_kernel<<<(unsigned)((j.rows + 3) / 4), 128, 0, st>>>(j);
+  note_launches(1);
+  return check_launch("attention join");
+}
+
+// Partial results in a workspace: O first, then (m, l).
+constexpr size_t kTlPart = kD * sizeof(float) + sizeof(float2);
+
+}  // namespace
+
+// Sets the word as a kernel whose bounded wait ran out would have, reads and clears it.
+int tile_error_take(cudaStream_t st, unsigned* word) {
+  *word = 0;
+  unsigned zero = 0;
+  if (cudaMemcpyFromSymbolAsync(word, g_tile_timeout, sizeof(unsigned), 0, cudaMemcpyDeviceToHost,
+                                st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return check_launch("device status: read");
+  if (*word &&
+      (cudaMemcpyToSymbolAsync(g_tile_timeout, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice,
+                               st) != cudaSuccess ||
+       cudaStreamSynchronize(st) != cudaSuccess))
+    return check_launch("device status: clear");
+  return SD_OK;
+}
+
+static DtPlan window_plan(const Dims& s, int64_t m, int64_t window, int64_t sink) {
+  const int64_t rows = m * s.G;
+  const int64_t span = imin64(m, (rows <= kDtRows ? kDtRows : kDtPair) / s.G);
+  const int64_t keys = imin64(s.n, imin64(sink, s.n) + imin64(window, s.n) + span - 1);
+  return dt_plan((int64_t)s.B * s.Hkv, rows, keys, device_sm_count());
+}
+// Tokens that a single query token may see.
+static int64_t window_tokens(const Dims& s, int64_t window, int64_t sink) {
+  return imin64(s.n, imin64(sink, s.n) + imin64(window, s.n));
+}
+
+size_t window_attend_workspace_bytes(const Dims& s, int64_t m, int64_t window, int64_t sink) {
+  if (m == 1) {
+    const int64_t parts = window_stream_parts(s, window_tokens(s, window, sink));
+    return parts == (int64_t)s.B * s.Hq ? 0 : parts * kTlPart;
+  }
+  const DtPlan p = window_plan(s, m, window, sink);
+  return p.splits == 1 ? 0 : (size_t)s.B * s.Hq * m * p.splits * kTlPart;
+}
+
+int launch_window_attend(const Dims& s, const uint16_t* q, const sd_strides& qs,
+                         const uint16_t* K, const uint16_t* V, int64_t m, int64_t first,
+                         const int32_t* pos, const int32_t* length, int64_t window, int64_t sink,
+                         float scale, uint16_t* out, const sd_strides& os, float* lse, void* ws,
+                         cudaStream_t st) {
+  const DnWindow w{pos, length, first, m, s.n, window, sink};
+  const int64_t rows = (int64_t)s.B * s.Hq * m;
+  TlJoin j = {};
+  j.out = out, j.lse = lse, j.os = os, j.w = w, j.causal = 1;
+  j.Hq = s.Hq, j.Hkv = s.Hkv, j.G = s.G, j.B = s.B, j.rows = rows;
+  if (m == 1) {
+    const int64_t tokens = window_tokens(s, window, sink);
+    j.ao = (float*)ws;
+    j.aml = (float2*)((float*)ws + window_stream_parts(s, tokens) * kD);
+    if (int rc = launch_window_stream(s, q, qs, K, V, w, false, nullptr, tokens, scale, nullptr,
+                                      nullptr, 0, out, os, lse, (float*)ws, (float2*)j.aml, &j.na,
+                                      st))
+      return rc;
+    return j.na ? tl_join(j, st) : SD_OK;
+  }
+  const DtPlan p = window_plan(s, m, window, sink);
+  TlArgs a = {};
+  a.q = q, a.K = K, a.V = V, a.out = out, a.lse = lse, a.qs = qs, a.os = os, a.w = w;
+  a.causal = 1, a.Hkv = s.Hkv, a.G = s.G, a.ncap = s.ncap, a.sl2 = scale * kDnLog2e;
+  a.part_o = (float*)ws;
+  a.part_ml = (float2*)(a.part_o + rows * p.splits * kD);
+  if (int rc = tl_launch(a, (int64_t)s.B * s.Hkv, p, st)) return rc;
+  if (p.splits == 1) return SD_OK;
+  j.ao = a.part_o, j.aml = a.part_ml, j.na = p.splits;
+  return tl_join(j, st);
+}
+
+static DtPlan prefix_plan(const Dims& s, int64_t p) {
+  return dt_plan(s.Hkv, (int64_t)s.B * s.G, p, device_sm_count());
+}
+
+size_t prefix_attend_workspace_bytes(const Dims& s, int64_t p) {
+  const int64_t rows = (int64_t)s.B * s.Hq;
+  const int64_t pre = p ? rows * prefix_plan(s, p).splits : 0;
+  return (pre + window_stream_parts(s, s.n)) * kTlPart;
+}
+
+int launch_prefix_attend(const Dims& s, const uint16_t* q, const uint16_t* Kp,
+                         const uint16_t* Vp, int64_t p, int64_t pcap, const uint16_t* K,
+                         const uint16_t* V, const int32_t* end, float scale, uint16_t* out,
+                         float* lse, void* ws, cudaStream_t st) {
+  const int64_t rows = (int64_t)s.B * s.Hq;
+  const sd_strides qs{(int64_t)s.Hq * kD, kD, 0};
+  TlJoin j = {};
+  j.out = out, j.lse = lse, j.os = qs, j.w.m = 1, j.Hq = s.Hq, j.Hkv = s.Hkv, j.G = s.G;
+  j.B = s.B, j.rows = rows;
+  const DtPlan plan = p ? prefix_plan(s, p) : DtPlan{};
+  const int64_t pre = p ? rows * plan.splits : 0, own = window_stream_parts(s, s.n);
+  float* ao = (float*)ws;
+  float* bo = ao + pre * kD;
+  float2* aml = (float2*)(bo + own * kD);
+  float2* bml = aml + pre;
+  if (p) {
+    // the batch's rows as the tokens of one sequence, every one seeing the whole prefix
+    TlArgs a = {};
+    a.q = q, a.K = Kp, a.V = Vp, a.qs = sd_strides{0, kD, (int64_t)s.Hq * kD};
+    a.w.m = s.B, a.w.n = p, a.Hkv = s.Hkv, a.G = s.G, a.ncap = pcap;
+    a.sl2 = scale * kDnLog2e, a.part_o = ao, a.part_ml = aml, a.parts_only = 1;
+    if (int rc = tl_launch(a, s.Hkv, plan, st)) return rc;
+  }
+  j.ao = ao, j.aml = aml, j.na = p ? plan.splits : 0;
+  if (K) {
+    DnWindow w = {};
+    w.n = s.n;
+    if (int rc = launch_window_stream(s, q, qs, K, V, w, true, end, s.n, scale, ao, aml, j.na, out,
+                                      qs, lse, bo, bml, &j.nb, st))
+      return rc;
+    if (!j.nb) return SD_OK;
+    j.bo = bo, j.bml = bml;
+  }
+  return tl_join(j, st);
+}
+
+}  // namespace sd

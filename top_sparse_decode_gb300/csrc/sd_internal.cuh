@@ -60,6 +60,8 @@ inline int per_device_cached(std::atomic<int> (&tab)[kMaxDev], F compute) {
 // setter for testing the report without making a wait run out.
 int scan_error_take(cudaStream_t st, unsigned* word);
 int scan_error_set(unsigned word, cudaStream_t st);
+// The tile attention's (sd_dense_tile.cu).
+int tile_error_take(cudaStream_t st, unsigned* word);
 // The current device's SM count (cached per device; 152 if it cannot be read).
 int device_sm_count();
 
@@ -209,7 +211,7 @@ int launch_kv4_attend(const Dims& s, const uint16_t* q, const sd_kv4& c, const i
                       int64_t idx_stride, const int32_t* count, int64_t max_count,
                       const int32_t* begin, const int32_t* end, float scale, float* out,
                       float* lse, void* ws, cudaStream_t st);
-// The bf16 cache around the sparse step (sd_rope.cu, sd_dense_attend.cu), strides resolved.
+// The bf16 cache around the sparse step (sd_rope.cu, sd_dense_tile.cu), strides resolved.
 int launch_norm_rope(const Dims& s, const sd_rope& rope, const uint16_t* q, const sd_strides& qs,
                      uint16_t* qo, const sd_strides& qos, const uint16_t* k,
                      const sd_strides& ks, const uint16_t* v, const sd_strides& vs, uint16_t* K,
