@@ -190,37 +190,61 @@ __device__ __forceinline__ void tl_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 // Shared-memory operand in the 128-byte swizzle: 8-row groups 1 KB apart; lbo: for an operand
-// whose rows are the product's inner dimension (V), its next 64 columns.
-__device__ __forceinline__ uint64_t tl_desc(uint32_t addr, uint32_t lbo) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
-         ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// whose rows are the product's inner dimension (V), its next 64 columns.  The low word moves
+// with the address, the high word stands.
+__device__ __forceinline__ uint32_t tl_desc(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
+constexpr uint32_t kTlDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 // bf16 x bf16 -> fp32, 128 x 128; bit 16: B's rows are the inner dimension
 constexpr uint32_t kTlInstr = (1u << 4) | (1u << 7) | (1u << 10) | ((128u / 8) << 17) |
                               ((128u / 16) << 24);
 constexpr uint32_t kTlInstrV = kTlInstr | (1u << 16);
 
+template <bool ADD>
+__device__ __forceinline__ void tl_mma_qk(uint32_t s, uint32_t q, uint32_t k) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %3};\n\t"
+      "mov.b64 db, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(s),
+      "r"(q), "r"(k), "r"(kTlDescHi), "r"(kTlInstr), "n"(ADD ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void tl_mma_pv(uint32_t o, uint32_t p, uint32_t v, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}\n" ::"r"(o),
+      "r"(p), "r"(v), "r"(kTlDescHi), "r"(kTlInstrV), "r"(add)
+      : "memory");
+}
+// S = Q K^T by one thread: 16 channels a product, 32 bytes of a 64-channel half.
 __device__ __forceinline__ void tl_qk(uint32_t s, uint32_t q, uint32_t k) {
+  const uint32_t dq = tl_desc(q, 16), dk = tl_desc(k, 16);
+  tl_mma_qk<false>(s, dq, dk);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {  // 16 channels each: 32 bytes of a 64-channel half
-    const uint32_t off = (kk >> 2) * kTlHalf + (kk & 3) * 32;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(s),
-        "l"(tl_desc(q + off, 16)), "l"(tl_desc(k + off, 16)), "r"(kTlInstr), "r"((uint32_t)(kk > 0))
-        : "memory");
+  for (int kk = 1; kk < 8; ++kk) {
+    const uint32_t off = ((kk >> 2) * kTlHalf + (kk & 3) * 32) >> 4;
+    tl_mma_qk<true>(s, dq + off, dk + off);
   }
 }
+// O += P V: 16 tokens a product, two 8-row groups; 8 columns of P.
 __device__ __forceinline__ void tl_pv(uint32_t o, uint32_t p, uint32_t v, bool add) {
+  const uint32_t dv = tl_desc(v, kTlHalf);
+  tl_mma_pv(o, p, dv, add);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {  // 16 tokens each: two 8-row groups; 8 columns of P
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(o),
-        "r"(p + 8 * kk), "l"(tl_desc(v + 2048 * kk, kTlHalf)), "r"(kTlInstrV),
-        "r"((uint32_t)(add || kk > 0))
-        : "memory");
-  }
+  for (int kk = 1; kk < 8; ++kk) tl_mma_pv(o, p + 8 * kk, dv + ((2048 * kk) >> 4), 1u);
+}
+__device__ __forceinline__ bool tl_elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+               : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ float tl_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 // Pairs of fp32 values, one instruction for both.
 __device__ __forceinline__ uint64_t tl_two(float x, float y) {
@@ -316,11 +340,8 @@ __device__ __forceinline__ void tl_tile(const TlItem& x, int i, int64_t& c0, int
 __device__ __forceinline__ int tl_index(const TlArgs& a, const TlItem& x, int g, int j) {
   return x.ta + (a.dual ? 2 * j + g : j);
 }
-// Ring positions (counted from the item's first) of group g's j-th K and V.  Loads go K, V,
-// K, V, ..; dual: K0, K1, V0, V1, ...
-__device__ __forceinline__ uint32_t tl_kpos(const TlArgs& a, int g, int j) {
-  return a.dual ? 4u * j + g : 2u * j;
-}
+// Ring position (counted from the item's first) of group g's j-th V.  Loads go K, V, K, V, ..;
+// dual: K0, K1, V0, V1, ...
 __device__ __forceinline__ uint32_t tl_vpos(const TlArgs& a, const TlItem& x, int g, int j) {
   return a.dual ? 4u * j + (j < x.t[1] ? 2 : 1) + g : 2u * j + 1;
 }
@@ -415,8 +436,10 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < kDtKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sl2;
+        for (int i = 0; i < kDtKeys; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = tl_max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
+        const float top = fmaxf(tl_max3(mx[0], mx[1], mx[2]), mx[3]) * a.sl2;
         const bool need = top > m + kTlSlack;
         if (__any_sync(0xFFFFFFFFu, need)) {
           const float f = need ? tl_exp2(m - top) : 1.0f;  // m = -inf: 0
@@ -488,7 +511,8 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       }
       tl_fence_before();
-      tl_arrive(&sm.pfull[g]);
+      __syncwarp();
+      if (lane == 0) tl_arrive(&sm.pfull[g]);
       ++done;
     }
     base += tl_loads(a, x);
@@ -499,7 +523,8 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
     if (a.dual && g == 1) {
       sm.ml[tid] = make_float2(m, l);
       // read by the first group before it gives O back, which this group's next item needs
-      tl_arrive(&sm.mlfull);
+      __syncwarp();
+      if (lane == 0) tl_arrive(&sm.mlfull);
       continue;
     }
     if (a.dual && x.t[1] > 0) {
@@ -615,67 +640,104 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
       }
     }
     tl_fence_before();
-    if (T > 0) tl_arrive(&sm.oempty[g]);
-    if (a.dual && x.t[1] > 0) tl_arrive(&sm.oempty[1]);
+    __syncwarp();
+    if (lane == 0) {
+      if (T > 0) tl_arrive(&sm.oempty[g]);
+      if (a.dual && x.t[1] > 0) tl_arrive(&sm.oempty[1]);
+    }
   }
 }
 
-// One thread issues every product of the CTA.
+// A ring position as stage and round.
+struct TlPos {
+  uint32_t stage, par;
+  __device__ __forceinline__ void next() {
+    if (++stage == kTlStages) {
+      stage = 0;
+      par ^= 1;
+    }
+  }
+  __device__ __forceinline__ TlPos ahead(uint32_t n) const {  // n <= kTlStages
+    TlPos p = {stage + n, par};
+    if (p.stage >= kTlStages) {
+      p.stage -= kTlStages;
+      p.par ^= 1;
+    }
+    return p;
+  }
+};
+
+// One warp issues every product of the CTA; it stays together (so that addresses and
+// descriptors live in uniform registers: issued by one diverged thread, a tile's eight
+// products took 700 to 800 cycles) and elects the thread that issues.
 __device__ __forceinline__ bool tl_products(TlSmem& sm, const TlArgs& a, uint32_t tmem) {
-  uint32_t base = 0, items = 0, tiles[2] = {0, 0}, outs[2] = {0, 0};
+  const bool leader = tl_elect();
+  uint32_t items = 0, par_p[2] = {0, 0}, outs[2] = {0, 0};
   const uint32_t q_at = tl_su32(sm.q[0]), ring = tl_su32(sm.ring[0]);
-  auto stage = [&](uint32_t pos) { return ring + (pos % kTlStages) * kTlTile; };
-  auto loaded = [&](uint32_t pos) {
-    return tl_wait(&sm.abort, &sm.full[pos % kTlStages], (pos / kTlStages) & 1);
+  TlPos at = {0, 0};
+  auto loaded = [&](const TlPos& p) {
+    return tl_wait_warp(&sm.abort, &sm.full[p.stage], p.par);
   };
   for (int64_t id = blockIdx.x; id < a.items; id += gridDim.x) {
     const TlItem x = tl_item(a, id);
-    if (x.tb == x.ta) continue;
-    if (!tl_wait(&sm.abort, &sm.qfull, items & 1)) return false;
-    int left = x.t[0] + x.t[1];  // score products still to issue
-    for (int g = 0; g < 2; ++g) {
-      if (x.t[g] == 0) continue;
-      const uint32_t kp = base + tl_kpos(a, g, 0);
+    const int t0 = __shfl_sync(0xFFFFFFFFu, x.t[0], 0), t1 = __shfl_sync(0xFFFFFFFFu, x.t[1], 0);
+    if (t0 == 0) continue;
+    const int groups = t1 > 0 ? 2 : 1;
+    if (!tl_wait_warp(&sm.abort, &sm.qfull, items & 1)) return false;
+    // the first scores; dual: K0, K1, V0, V1 in the ring, else K, V
+    for (int g = 0; g < groups; ++g) {
+      const TlPos kp = a.dual ? at.ahead(g) : at;
       if (!loaded(kp)) return false;
       tl_fence_after();
-      tl_qk(tmem + 128 * g, q_at + (a.dual ? 0 : g * kTlTile), stage(kp));
-      tl_commit(&sm.sfull[g]);
-      --left;
-      if (a.dual || g == x.nq - 1) tl_commit(&sm.empty[kp % kTlStages]);
+      if (leader) {
+        tl_qk(tmem + 128 * g, q_at + (a.dual ? 0 : g * kTlTile), ring + kp.stage * kTlTile);
+        tl_commit(&sm.sfull[g]);
+        if (a.dual || g == groups - 1) tl_commit(&sm.empty[kp.stage]);
+        if (g == groups - 1 && t0 == 1) tl_commit(&sm.qempty);
+      }
+      __syncwarp();
     }
-    if (left == 0) tl_commit(&sm.qempty);
-    for (int j = 0; j < x.t[0]; ++j) {
-      for (int g = 0; g < 2; ++g) {
-        if (j >= x.t[g]) continue;
-        const bool last = a.dual || g == x.nq - 1;  // the stage's last reader
-        const uint32_t vp = base + tl_vpos(a, x, g, j);
+    for (int j = 0; j < t0; ++j) {
+      const int now = a.dual && j < t1 ? 2 : 1;  // K (and V) loads of this step
+      for (int g = 0; g < groups; ++g) {
+        if (g == 1 && j >= t1) break;
+        const bool last = a.dual || g == groups - 1;  // the stage's last reader
+        const TlPos vp = at.ahead(now + (a.dual ? g : 0));
         if (!loaded(vp)) return false;
-        if (!tl_wait(&sm.abort, &sm.pfull[g], tiles[g] & 1)) return false;
-        ++tiles[g];
+        if (!tl_wait_warp(&sm.abort, &sm.pfull[g], par_p[g])) return false;
+        par_p[g] ^= 1;
         if (j == 0) {  // O of the item before is read
-          if (outs[g] && !tl_wait(&sm.abort, &sm.oempty[g], (outs[g] - 1) & 1)) return false;
+          if (outs[g] && !tl_wait_warp(&sm.abort, &sm.oempty[g], (outs[g] - 1) & 1)) return false;
           ++outs[g];
         }
         tl_fence_after();
-        tl_pv(tmem + 256 + 128 * g, tmem + 128 * g, stage(vp), j > 0);
-        tl_commit(&sm.pvdone[g]);
-        if (last) tl_commit(&sm.empty[vp % kTlStages]);
-        if (j + 1 < x.t[g]) {
-          const uint32_t kp = base + tl_kpos(a, g, j + 1);
+        if (leader) {
+          tl_pv(tmem + 256 + 128 * g, tmem + 128 * g, ring + vp.stage * kTlTile, j > 0);
+          tl_commit(&sm.pvdone[g]);
+          if (last) tl_commit(&sm.empty[vp.stage]);
+        }
+        __syncwarp();
+        if (j + 1 < (g ? t1 : t0)) {
+          const TlPos kp = at.ahead(2 * now + (a.dual ? g : 0));
           if (!loaded(kp)) return false;
           tl_fence_after();
-          tl_qk(tmem + 128 * g, q_at + (a.dual ? 0 : g * kTlTile), stage(kp));
-          tl_commit(&sm.sfull[g]);
-          if (last) tl_commit(&sm.empty[kp % kTlStages]);
-          if (--left == 0) tl_commit(&sm.qempty);
+          if (leader) {
+            tl_qk(tmem + 128 * g, q_at + (a.dual ? 0 : g * kTlTile), ring + kp.stage * kTlTile);
+            tl_commit(&sm.sfull[g]);
+            if (last) tl_commit(&sm.empty[kp.stage]);
+            // the item's last scores: Q may go
+            const bool done = g == 1 ? j + 2 == t1 && t1 == t0 : j + 2 == t0 && t1 < t0;
+            if (done) tl_commit(&sm.qempty);
+          }
+          __syncwarp();
         }
       }
+      for (int i = 0; i < 2 * now; ++i) at.next();
     }
-    base += tl_loads(a, x);
     ++items;
   }
   // arrivals of the last commits are in before the CTA ends
-  return !items || tl_wait(&sm.abort, &sm.qempty, (items - 1) & 1);
+  return !items || tl_wait_warp(&sm.abort, &sm.qempty, (items - 1) & 1);
 }
 
 // One thread issues every K and V load of the CTA.
@@ -763,12 +825,12 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     tl_init(&sm.qempty, 1);
     for (int g = 0; g < 2; ++g) {
       tl_init(&sm.sfull[g], 1);
-      tl_init(&sm.pfull[g], 128);
+      tl_init(&sm.pfull[g], 4);
       tl_init(&sm.pvdone[g], 1);
-      tl_init(&sm.oempty[g], 128);
+      tl_init(&sm.oempty[g], 4);
       sm.bad[g][0] = sm.bad[g][1] = 0;
     }
-    tl_init(&sm.mlfull, 128);
+    tl_init(&sm.mlfull, 4);
     tl_init(&sm.drain, 1);
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -790,8 +852,9 @@ __global__ void __launch_bounds__(kTlThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
     if (warp == 8) {
-      if ((threadIdx.x & 31) == 0 && !tl_products(sm, a, tmem)) {
-        tl_commit(&sm.drain);  // gave up: the products in flight end before tensor memory goes
+      if (!tl_products(sm, a, tmem)) {
+        // gave up: the products in flight end before tensor memory goes
+        if (tl_elect()) tl_commit(&sm.drain);
         tl_drain(&sm.drain, 0);
       }
     } else if (warp == 9) {
