@@ -14,8 +14,9 @@
 // Per token tile and row tile: S = Q K^T (128 x 128 x 128, both operands from shared memory,
 // fp32 in tensor memory), p = 2^(s - m) by the softmax group whose thread owns the row, p
 // rounded to bf16 into the columns that S held, O += P V (P from tensor memory, V as it
-// lies).  The reference m is raised only when a tile's maximum exceeds it by more than 2^8,
-// and only then O is rescaled (weights are at most 2^8, and exact in their scale).
+// lies).  The reference m is a maximum of the row's earlier tiles, and stands as long as the
+// tile's weights sum up to 2^14 at most; only then the tile's maximum is sought, m raised
+// and O rescaled (a weight's rounding is relative to itself, whatever m).
 //
 // Roles (384 threads, one CTA per SM, persistent over items): warps 0-3 and 4-7 softmax and
 // output of the two row tiles, warp 8 issues the products, warp 9 the TMA loads, warps 10
@@ -51,7 +52,7 @@ constexpr int kTlStages = 5;
 constexpr uint32_t kTlTile = kDtKeys * kD * 2;  // bytes of a K, V or Q tile: 32 KB
 constexpr uint32_t kTlHalf = kTlTile / 2;       // 64 channels of it
 constexpr uint32_t kTlSpin = 1u << 22;          // try_wait rounds before a wait gives up
-constexpr float kTlSlack = 8.0f;                // log2 headroom before m is raised
+constexpr float kTlMost = 16384.0f;             // largest sum of a tile's weights against an old m
 
 struct TlSmem {
   uint8_t q[2][kTlTile];
@@ -373,6 +374,61 @@ __device__ __noinline__ void tl_row_again(const TlArgs& a, const TlItem& x, int6
   }
 }
 
+// Scores [32 c, 32 c + 32) of the thread's row as loaded, -inf where it does not see them.
+__device__ __forceinline__ void tl_mask(uint32_t* s, int c, int hi, int lo, int sk) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int k = 32 * c + i;
+    if (k >= hi || (k <= lo && k >= sk)) s[i] = 0xFF800000u;
+  }
+}
+// The row's weights 2^(s sl2 - m) as packed bf16, and their sum.
+__device__ __forceinline__ float tl_weights(uint32_t* pk, uint32_t s_at, float sl2, float m,
+                                            bool cut, int hi, int lo, int sk) {
+  const uint64_t sl = tl_two(sl2, sl2), mm = tl_two(-m, -m);
+  uint64_t sum[2] = {0, 0};  // pairs of +0
+  uint32_t s[2][32];
+  tl_ld32(s[0], s_at);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t* x = s[c & 1];
+    tl_wait_ld();
+    tl_use32(x);
+    if (c < 3) tl_ld32(s[(c + 1) & 1], s_at + 32 * (c + 1));  // while these are worked on
+    if (cut) tl_mask(x, c, hi, lo, sk);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float u, v;
+      tl_of(tl_fma2(tl_two(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sl, mm), u, v);
+      u = tl_exp2(u);
+      v = tl_exp2(v);
+      sum[i & 1] = tl_add2(sum[i & 1], tl_two(u, v));
+      pk[16 * c + i] = dn_pack(u, v);
+    }
+  }
+  float u, v;
+  tl_of(tl_add2(sum[0], sum[1]), u, v);
+  return u + v;
+}
+// The row's largest score.
+__device__ __noinline__ float tl_top(uint32_t s_at, bool cut, int hi, int lo, int sk) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t s[32];
+    tl_ld32(s, s_at + 32 * c);
+    tl_wait_ld();
+    tl_use32(s);
+    if (cut) tl_mask(s, c, hi, lo, sk);
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mx[k] = tl_max3(mx[k], __uint_as_float(s[i + 2 * k]), __uint_as_float(s[i + 2 * k + 1]));
+  }
+  return fmaxf(tl_max3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
 // Softmax of the item's row tile `g` (dual: of every second token tile), and its result.
 __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, uint32_t tmem) {
   const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
@@ -414,34 +470,26 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
       if (!tl_wait_warp(&sm.abort, &sm.sfull[g], done & 1)) return;
       tl_fence_after();
       if (warp_on) {
-        uint32_t sr[kDtKeys];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tl_ld32(sr + 32 * c, s_at + 32 * c);
-        tl_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tl_use32(sr + 32 * c);
-        float s[kDtKeys];
-#pragma unroll
-        for (int i = 0; i < kDtKeys; ++i) s[i] = __uint_as_float(sr[i]);
-        if (!same || have < kDtKeys) {
-          int hi = have, lo = -1, sk = kDtKeys;
-          if (a.causal) {
-            hi = (int)imax64(0, imin64(hi, p + 1 - c0));
-            sk = (int)imax64(0, imin64(kDtKeys, a.w.sink - c0));
-            lo = (int)imax64(-1, imin64(kDtKeys, p - a.w.window - c0));
-          }
-#pragma unroll
-          for (int i = 0; i < kDtKeys; ++i)
-            if (i >= hi || (i <= lo && i >= sk)) s[i] = -INFINITY;
+        const bool cut = !same || have < kDtKeys;
+        int hi = have, lo = -1, sk = kDtKeys;  // seen: below hi, and above lo or below sk
+        if (cut && a.causal) {
+          hi = (int)imax64(0, imin64(hi, p + 1 - c0));
+          sk = (int)imax64(0, imin64(kDtKeys, a.w.sink - c0));
+          lo = (int)imax64(-1, imin64(kDtKeys, p - a.w.window - c0));
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < kDtKeys; i += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = tl_max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
-        const float top = fmaxf(tl_max3(mx[0], mx[1], mx[2]), mx[3]) * a.sl2;
-        const bool need = top > m + kTlSlack;
-        if (__any_sync(0xFFFFFFFFu, need)) {
+        uint32_t pk[kDtKeys / 2];
+        float sum;
+        // the weights against m as it stands; a sum that says that m is too low (or that
+        // there is none yet) brings the maximum, m and O up to date, and the weights again
+        const bool first = m == -INFINITY;
+        bool low = first;
+        if (!__any_sync(0xFFFFFFFFu, first)) {
+          sum = tl_weights(pk, s_at, a.sl2, m, cut, hi, lo, sk);
+          low = !(sum <= kTlMost);
+        }
+        if (__any_sync(0xFFFFFFFFu, low)) {
+          const float top = tl_top(s_at, cut, hi, lo, sk) * a.sl2;
+          const bool need = low && top > m;
           const float f = need ? tl_exp2(m - top) : 1.0f;  // m = -inf: 0
           if (j > 0) {
             if (!tl_wait_warp(&sm.abort, &sm.pvdone[g], (done - 1) & 1)) return;
@@ -459,31 +507,11 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
           }
           l *= f;
           if (need) m = top;
+          sum = tl_weights(pk, s_at, a.sl2, m == -INFINITY ? 0.0f : m, cut, hi, lo, sk);
         }
-        const float mu = m == -INFINITY ? 0.0f : m;
-        const uint64_t sl = tl_two(a.sl2, a.sl2), mm = tl_two(-mu, -mu);
-        uint64_t sum0 = 0, sum1 = 0;  // pairs of +0
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int k = 64 * c + 2 * i;
-            float u, v;
-            tl_of(tl_fma2(tl_two(s[k], s[k + 1]), sl, mm), u, v);
-            u = tl_exp2(u);
-            v = tl_exp2(v);
-            if (i & 1)
-              sum1 = tl_add2(sum1, tl_two(u, v));
-            else
-              sum0 = tl_add2(sum0, tl_two(u, v));
-            pk[i] = dn_pack(u, v);
-          }
-          tl_st32(s_at + 32 * c, pk);
-        }
-        float u, v;
-        tl_of(tl_add2(sum0, sum1), u, v);
-        l += u + v;
+        l += sum;
+        tl_st32(s_at, pk);
+        tl_st32(s_at + 32, pk + 32);
         tl_wait_st();
       }
       if (have < kDtKeys || !same) {
@@ -508,7 +536,7 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
         }
         if ((worst & 0xFFFFu) >= 0x7F80u || (worst >> 16) >= 0x7F80u)
           *(volatile int*)&sm.bad[g][mine_n & 1] = mine_n;
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        if (have < kDtKeys) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       }
       tl_fence_before();
       __syncwarp();
@@ -702,26 +730,25 @@ __device__ __forceinline__ bool tl_products(TlSmem& sm, const TlArgs& a, uint32_
       for (int g = 0; g < groups; ++g) {
         if (g == 1 && j >= t1) break;
         const bool last = a.dual || g == groups - 1;  // the stage's last reader
-        const TlPos vp = at.ahead(now + (a.dual ? g : 0));
-        if (!loaded(vp)) return false;
-        if (!tl_wait_warp(&sm.abort, &sm.pfull[g], par_p[g])) return false;
-        par_p[g] ^= 1;
+        const bool more = j + 1 < (g ? t1 : t0);
+        const TlPos vp = at.ahead(now + (a.dual ? g : 0)), kp = at.ahead(2 * now + (a.dual ? g : 0));
+        // both tiles first, so that the scores' products follow without a gap
+        if (g == 0 || a.dual) {
+          if (!loaded(vp)) return false;
+          if (more && !loaded(kp)) return false;
+        }
         if (j == 0) {  // O of the item before is read
           if (outs[g] && !tl_wait_warp(&sm.abort, &sm.oempty[g], (outs[g] - 1) & 1)) return false;
           ++outs[g];
         }
+        if (!tl_wait_warp(&sm.abort, &sm.pfull[g], par_p[g])) return false;
+        par_p[g] ^= 1;
         tl_fence_after();
         if (leader) {
           tl_pv(tmem + 256 + 128 * g, tmem + 128 * g, ring + vp.stage * kTlTile, j > 0);
           tl_commit(&sm.pvdone[g]);
           if (last) tl_commit(&sm.empty[vp.stage]);
-        }
-        __syncwarp();
-        if (j + 1 < (g ? t1 : t0)) {
-          const TlPos kp = at.ahead(2 * now + (a.dual ? g : 0));
-          if (!loaded(kp)) return false;
-          tl_fence_after();
-          if (leader) {
+          if (more) {
             tl_qk(tmem + 128 * g, q_at + (a.dual ? 0 : g * kTlTile), ring + kp.stage * kTlTile);
             tl_commit(&sm.sfull[g]);
             if (last) tl_commit(&sm.empty[kp.stage]);
@@ -729,8 +756,8 @@ __device__ __forceinline__ bool tl_products(TlSmem& sm, const TlArgs& a, uint32_
             const bool done = g == 1 ? j + 2 == t1 && t1 == t0 : j + 2 == t0 && t1 < t0;
             if (done) tl_commit(&sm.qempty);
           }
-          __syncwarp();
         }
+        __syncwarp();
       }
       for (int i = 0; i < 2 * now; ++i) at.next();
     }
