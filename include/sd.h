@@ -554,9 +554,9 @@ int sd_qk_norm_rope(const sd_shape* shape, const sd_rope* rope, const void* q,
  *   q: bf16, strides as sd_qk_norm_rope's q; K, V: bf16 [B][hkv][n_cap][d]; out: bf16
  *   with strides of its own, rows apart; lse: fp32 [B][hq][m] or NULL.  pos, length: int32
  *   [B] (device), NULL meaning 0 and m.  Rows of tokens t >= length[b] are not written.
- *   scale >= 0.  Scores, sums and the softmax are fp32; the weights e^{z - m'} (m' at most
- *   14 log 2 below the row's largest score so far) are rounded to bf16 for the product with
- *   V, and lse comes from the sums before that.
+ *   scale >= 0.  Scores, sums and the softmax are fp32; the weights e^{z - m'} (m' from 14
+ *   log 2 below the row's largest score so far to 40 log 2 above it) are rounded to bf16 for
+ *   the product with V, and lse comes from the sums before that.
  *   A token that a query does not see reaches nothing of it, whatever its K and V hold
  *   (infinities and NaN included).
  *   Workspace: sd_window_attend_workspace_size() bytes (device, 16-byte aligned; 0 where

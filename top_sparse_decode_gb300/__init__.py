@@ -306,6 +306,19 @@ def _bf16(t, name: str, n: int) -> Optional[int]:
     return _ptr(t)
 
 
+# sd_strides records by their values: making one costs a small call a microsecond
+_strides_made: dict = {}
+
+
+def _strides(key):
+    r = _strides_made.get(key)
+    if r is None:
+        if len(_strides_made) >= 1024:
+            _strides_made.clear()
+        r = _strides_made[key] = ctypes.byref(_abi.SdStrides(*key))
+    return r
+
+
 def _rows(t, dims, m: int):
     """(pointer, strides) of a [B][hkv][>= m][128] bf16 tensor of any strides with
     consecutive channels, dims = (B, hkv, 128); a contiguous tensor of another rank that
@@ -313,6 +326,11 @@ def _rows(t, dims, m: int):
     as [B][hkv][m][128]."""
     if t is None or type(t) is int:
         return t, None
+    if t.dtype is _BFLOAT16 and t.dim() == 4:
+        b, h, n, d = t.shape
+        sb, sh, st, sd_ = t.stride()
+        if (b, h, d) == dims and n >= m and sd_ == 1:
+            return t.data_ptr(), _strides((sb, sh, st))
     if t.dtype not in _BF16:
         raise ValueError(f"libsd takes bf16 rows, got {t.dtype}")
     if t.dim() != 4:

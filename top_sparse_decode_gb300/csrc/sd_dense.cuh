@@ -9,6 +9,38 @@ namespace sd {
 constexpr float kDnLog2e = 1.4426950408889634f;
 constexpr float kDnLn2 = 0.6931471805599453f;
 
+// A kernel launched while the one before it in the stream ends waits here for it.
+__device__ __forceinline__ void dn_wait_prior() {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+// Launches a kernel that way (it makes no read-only loads), in clusters where cluster > 0.
+template <class P>
+int dn_launch_early(const char* what, void (*kern)(P), unsigned grid, int threads, size_t smem,
+                    int cluster, cudaStream_t st, const P& a, bool early = true) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (early) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return check_launch(what);
+  note_launches(1);
+  return check_launch(what);
+}
+
 // The window call's geometry: query token t of sequence b stands at first + pos[b] + t.
 struct DnWindow {
   const int32_t* pos;

@@ -83,9 +83,18 @@ __device__ __forceinline__ uint32_t sw_rank_addr(uint32_t addr, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float sw_ld_rank(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float2 sw_ld_rank2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 sw_ld_rank4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void sw_cluster_sync() {
@@ -94,12 +103,63 @@ __device__ __forceinline__ void sw_cluster_sync() {
           : "memory");
 }
 
+// A softmax's state that a warp holds for one head: lane l channels 4l .. 4l + 3.
+struct SwHead {
+  float top, sum;
+  float4 o;
+  __device__ __forceinline__ void add(float m, float l, const float4& x, float mu) {
+    const float f = exp2f(m - mu);
+    sum = fmaf(l, f, sum);
+    o.x = fmaf(x.x, f, o.x);
+    o.y = fmaf(x.y, f, o.y);
+    o.z = fmaf(x.z, f, o.z);
+    o.w = fmaf(x.w, f, o.w);
+  }
+};
+__device__ __forceinline__ SwHead sw_head(float top) {
+  return SwHead{top, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+}
+__device__ __forceinline__ float sw_ref(float top) { return top == -INFINITY ? 0.0f : top; }
+
+// Joins the prefix's parts to a head and writes out and lse.
 template <int G>
-__global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(const SwArgs a) {
+__device__ __forceinline__ void sw_finish(const SwArgs& a, SwHead x, int b, int h, int g, int lane) {
+  if (a.pre) {
+    const int64_t pr = (((int64_t)h * a.B + b) * G + g) * a.pre;
+    float top = x.top;
+    for (int s = lane; s < a.pre; s += 32) top = fmaxf(top, a.pre_ml[pr + s].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float mu = sw_ref(top);
+    SwHead y = sw_head(top);
+    y.add(x.top, x.sum, x.o, mu);
+    for (int s0 = 0; s0 < a.pre; s0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (s0 + lane < a.pre) ml = a.pre_ml[pr + s0 + lane];
+      const int n = min(32, a.pre - s0);
+#pragma unroll 8
+      for (int s = 0; s < n; ++s) {
+        const float4 v = reinterpret_cast<const float4*>(a.pre_o + (pr + s0 + s) * kD)[lane];
+        y.add(__shfl_sync(0xFFFFFFFFu, ml.x, s), __shfl_sync(0xFFFFFFFFu, ml.y, s), v, mu);
+      }
+    }
+    x = y;
+  }
+  const int head = h * G + g;
+  const float inv = x.sum == 0.0f ? 0.0f : 1.0f / x.sum;
+  *reinterpret_cast<uint2*>(a.out + b * a.oseq + head * a.ohead + 4 * lane) =
+      make_uint2(dn_pack(x.o.x * inv, x.o.y * inv), dn_pack(x.o.z * inv, x.o.w * inv));
+  if (a.lse && lane == 0)
+    a.lse[(int64_t)b * a.Hkv * G + head] =
+        x.sum == 0.0f ? -INFINITY : (x.top + log2f(x.sum)) * kDnLn2;
+}
+
+template <int G>
+__global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(SwArgs a) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float2 wml[kSwWarps][8];  // a warp's (m, l) of each head
-  __shared__ float2 cml[8];            // the CTA's
-  __shared__ float co[8][kD];          // and its O
+  __shared__ __align__(16) float2 cml[8];    // the CTA's
+  __shared__ __align__(16) float co[8][kD];  // and its O
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, tig = lane & 3;
   const bool real = gid < G;
@@ -222,6 +282,9 @@ __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(const SwArg
     }
   }
   sw_cp_wait<0>();
+  // behind a prefix's kernel every CTA waits for it, also where a later kernel joins the
+  // parts: that one waits for this kernel only
+  if (a.pre) dn_wait_prior();
 
   // the warp's (m, l, O) into its own part of the ring
   l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
@@ -240,73 +303,44 @@ __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(const SwArg
   const bool joined = a.parts > 1 && !a.cut;
   const float* all_o = reinterpret_cast<const float*>(ring);
   constexpr int kStep = kSwStages * kSwStage / sizeof(float);
-#pragma unroll 1
-  for (int g = 0; g < G; ++g) {
+  for (int g = warp; g < G; g += kSwWarps) {  // a warp per head
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kSwWarps; ++w) top = fmaxf(top, wml[w][g].x);
-    const float mu = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, acc = 0.0f;
+    SwHead x = sw_head(top);
 #pragma unroll
-    for (int w = 0; w < kSwWarps; ++w) {
-      const float f = exp2f(wml[w][g].x - mu);
-      sum = fmaf(wml[w][g].y, f, sum);
-      acc = fmaf(all_o[w * kStep + g * kD + tid], f, acc);
-    }
+    for (int w = 0; w < kSwWarps; ++w)
+      x.add(wml[w][g].x, wml[w][g].y,
+            reinterpret_cast<const float4*>(all_o + w * kStep + g * kD)[lane], sw_ref(top));
     if (a.cut) {
       const int64_t at = (row * G + g) * a.parts + part;
-      a.part_o[at * kD + tid] = acc;
-      if (tid == 0) a.part_ml[at] = make_float2(top, sum);
+      reinterpret_cast<float4*>(a.part_o + at * kD)[lane] = x.o;
+      if (lane == 0) a.part_ml[at] = make_float2(x.top, x.sum);
+    } else if (joined) {
+      reinterpret_cast<float4*>(co[g])[lane] = x.o;
+      if (lane == 0) cml[g] = make_float2(x.top, x.sum);
     } else {
-      co[g][tid] = acc;
-      if (tid == 0) cml[g] = make_float2(top, sum);
+      sw_finish<G>(a, x, b, h, g, lane);
     }
   }
-  if (a.cut) return;
-  if (joined)
-    sw_cluster_sync();
-  else
-    __syncthreads();
+  if (!joined) return;
+  sw_cluster_sync();
   // each CTA of the row finishes its share of the heads
   const uint32_t ml_at = sw_su32(cml), o_at = sw_su32(co);
-  for (int g = part; g < G; g += a.parts) {
-    const int head = h * G + g;
-    const int64_t pr = ((int64_t)h * a.B + b) * G + g;
-    float top = -INFINITY;
+  for (int g = part + a.parts * warp; g < G; g += a.parts * kSwWarps) {
+    const float2 mine2 =
+        lane < a.parts ? sw_ld_rank2(sw_rank_addr(ml_at + 8 * g, lane)) : make_float2(-INFINITY, 0.0f);
+    float top = mine2.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    SwHead x = sw_head(top);
+#pragma unroll 8
     for (int s = 0; s < a.parts; ++s)
-      top = fmaxf(top, joined ? sw_ld_rank(sw_rank_addr(ml_at + 8 * g, s)) : cml[g].x);
-    for (int s = 0; s < a.pre; ++s) top = fmaxf(top, a.pre_ml[pr * a.pre + s].x);
-    const float mu = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, acc = 0.0f;
-    for (int s = 0; s < a.parts; ++s) {
-      float mm, ll, oo;
-      if (joined) {
-        mm = sw_ld_rank(sw_rank_addr(ml_at + 8 * g, s));
-        ll = sw_ld_rank(sw_rank_addr(ml_at + 8 * g + 4, s));
-        oo = sw_ld_rank(sw_rank_addr(o_at + 4 * (g * kD + tid), s));
-      } else {
-        mm = cml[g].x, ll = cml[g].y, oo = co[g][tid];
-      }
-      const float f = exp2f(mm - mu);
-      sum = fmaf(ll, f, sum);
-      acc = fmaf(oo, f, acc);
-    }
-#pragma unroll 4
-    for (int s = 0; s < a.pre; ++s) {
-      const float2 y = a.pre_ml[pr * a.pre + s];
-      const float f = exp2f(y.x - mu);
-      sum = fmaf(y.y, f, sum);
-      acc = fmaf(a.pre_o[(pr * a.pre + s) * kD + tid], f, acc);
-    }
-    const float res = sum == 0.0f ? 0.0f : acc / sum;
-    const float next = __shfl_down_sync(0xFFFFFFFFu, res, 1);
-    if (!(tid & 1))
-      *reinterpret_cast<uint32_t*>(a.out + b * a.oseq + head * a.ohead + tid) = dn_pack(res, next);
-    if (a.lse && tid == 0)
-      a.lse[(int64_t)b * a.Hkv * G + head] =
-          sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kDnLn2;
+      x.add(__shfl_sync(0xFFFFFFFFu, mine2.x, s), __shfl_sync(0xFFFFFFFFu, mine2.y, s),
+            sw_ld_rank4(sw_rank_addr(o_at + 4 * (g * kD + 4 * lane), s)), sw_ref(top));
+    sw_finish<G>(a, x, b, h, g, lane);
   }
-  if (joined) sw_cluster_sync();  // the others' shared memory is read
+  sw_cluster_sync();  // the others' shared memory is read
 }
 
 // The largest cluster that this device runs of the kernel (cached per device).
@@ -354,27 +388,14 @@ int sw_launch(SwArgs& a, int64_t tokens, float* cut_o, float2* cut_ml, int* cut,
   *cut = p.cut ? p.parts : 0;
   if (int rc = set_smem_limit((const void*)dense_stream_kernel<G>, kSwSmem, "stream attention"))
     return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * p.parts), 1, 1);
-  cfg.blockDim = dim3(kSwThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSwSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.parts;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.parts > 1 && !p.cut ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, dense_stream_kernel<G>, (const SwArgs)a) != cudaSuccess)
-    return check_launch("stream attention");
-  note_launches(1);
-  return check_launch("stream attention");
+  // behind a prefix's kernel: started while it ends
+  return dn_launch_early("stream attention", dense_stream_kernel<G>, (unsigned)(rows * p.parts),
+                         kSwThreads, kSwSmem, p.parts > 1 && !p.cut ? p.parts : 0, st, a,
+                         a.pre > 0);
 }
 
 int sw_dispatch(SwArgs& a, int G, int64_t tokens, float* cut_o, float2* cut_ml, int* cut,
                 cudaStream_t st) {
-  // (scale 0 as in the tile kernel: unseen tokens' -inf must stay)
   switch (G) {
     case 1: return sw_launch<1>(a, tokens, cut_o, cut_ml, cut, st);
     case 2: return sw_launch<2>(a, tokens, cut_o, cut_ml, cut, st);

@@ -14,9 +14,11 @@
 // Per token tile and row tile: S = Q K^T (128 x 128 x 128, both operands from shared memory,
 // fp32 in tensor memory), p = 2^(s - m) by the softmax group whose thread owns the row, p
 // rounded to bf16 into the columns that S held, O += P V (P from tensor memory, V as it
-// lies).  The reference m is a maximum of the row's earlier tiles, and stands as long as the
-// tile's weights sum up to 2^14 at most; only then the tile's maximum is sought, m raised
-// and O rescaled (a weight's rounding is relative to itself, whatever m).
+// lies).  The reference m begins at 0 and stands as long as a tile's weights sum up to 2^14 at
+// most and a row's so far to 2^-40 at least: a weight's rounding is relative to itself, so any
+// m in that range is as good as the maximum, which is then not sought (it took 400 of a
+// tile's 2,800 cycles).  Where it does not stand, the tile's maximum is sought, m set to the
+// whole number above it, and O and l moved by a power of two, exactly.
 //
 // Roles (384 threads, one CTA per SM, persistent over items): warps 0-3 and 4-7 softmax and
 // output of the two row tiles, warp 8 issues the products, warp 9 the TMA loads, warps 10
@@ -52,7 +54,8 @@ constexpr int kTlStages = 5;
 constexpr uint32_t kTlTile = kDtKeys * kD * 2;  // bytes of a K, V or Q tile: 32 KB
 constexpr uint32_t kTlHalf = kTlTile / 2;       // 64 channels of it
 constexpr uint32_t kTlSpin = 1u << 22;          // try_wait rounds before a wait gives up
-constexpr float kTlMost = 16384.0f;             // largest sum of a tile's weights against an old m
+constexpr float kTlMost = 16384.0f;             // a tile's weights sum up to this at most,
+constexpr float kTlLeast = 0x1p-40f;            // and a row's so far to this at least, or m moves
 
 struct TlSmem {
   uint8_t q[2][kTlTile];
@@ -84,7 +87,8 @@ struct TlArgs {
   float sl2;          // scale * log2(e), above 0
   int dual, splits, wide;  // wide: rows of out on 32 bytes
   int parts_only;          // splits == 1 leaves a partial result, too
-  int64_t per, items, bh;
+  int64_t per;
+  uint32_t items, bh;
 };
 
 // ---- PTX ---------------------------------------------------------------------------------
@@ -177,6 +181,15 @@ __device__ __forceinline__ void tl_ld32(uint32_t* r, uint32_t addr) {
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
+}
+__device__ __forceinline__ void tl_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};\n" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ void tl_st32(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -285,15 +298,16 @@ struct TlItem {
   int nq;            // row tiles (dual: 2 groups of one)
 };
 
-__device__ __forceinline__ TlItem tl_item(const TlArgs& a, int64_t id) {
-  TlItem x;
-  x.split = (int)(id % a.splits);
-  const int64_t rest = id / a.splits;
-  x.bh = rest % a.bh;
+__device__ __forceinline__ TlItem tl_item(const TlArgs& a, uint32_t id) {
+  TlItem x;  // (32-bit divisions: 64-bit ones took 3,000 cycles of an item)
+  const uint32_t rest = a.splits == 1 ? id : id / (uint32_t)a.splits;
+  x.split = (int)(id - rest * (uint32_t)a.splits);
+  const uint32_t tile_up = rest / (uint32_t)a.bh, bh = rest - tile_up * (uint32_t)a.bh;
+  x.bh = bh;
   // the last rows first: under a causal mask they see most
-  const int64_t tile = a.per - 1 - rest / a.bh;
-  x.b = (int)(x.bh / a.Hkv);
-  x.h = (int)(x.bh - (int64_t)x.b * a.Hkv);
+  const int64_t tile = a.per - 1 - (int64_t)tile_up;
+  x.b = (int)(bh / (uint32_t)a.Hkv);
+  x.h = (int)(bh - (uint32_t)x.b * (uint32_t)a.Hkv);
   const int64_t len = a.causal ? a.w.len(x.b) : a.w.m;
   x.r0 = tile * (a.dual ? kDtRows : kDtPair);
   x.rows = (int)imax64(0, imin64(a.dual ? kDtRows : kDtPair, len * a.G - x.r0));
@@ -313,10 +327,14 @@ __device__ __forceinline__ TlItem tl_item(const TlArgs& a, int64_t id) {
   } else {
     x.r = DnRanges{0, 0, a.w.n};
   }
-  x.na = (int)((x.r.s1 + kDtKeys - 1) / kDtKeys);
-  const int all = x.na + (int)((x.r.w1 - x.r.w0 + kDtKeys - 1) / kDtKeys);
-  x.ta = (int)((int64_t)all * x.split / a.splits);
-  x.tb = (int)((int64_t)all * (x.split + 1) / a.splits);
+  x.na = (int)((uint32_t)(x.r.s1 + kDtKeys - 1) / kDtKeys);
+  const uint32_t all = x.na + (uint32_t)(x.r.w1 - x.r.w0 + kDtKeys - 1) / kDtKeys;
+  x.ta = 0;
+  x.tb = (int)all;
+  if (a.splits > 1) {  // all * splits < 2^32: 2^24 tiles at most, and a part for an SM
+    x.ta = (int)(all * (uint32_t)x.split / (uint32_t)a.splits);
+    x.tb = (int)(all * (uint32_t)(x.split + 1) / (uint32_t)a.splits);
+  }
   const int t = x.tb - x.ta;
   if (a.dual) {
     x.t[0] = (t + 1) / 2;
@@ -352,8 +370,8 @@ __device__ __forceinline__ uint32_t tl_loads(const TlArgs& a, const TlItem& x) {
 
 // A row's own (m, l, O) from the cache, its warp together: the tokens of the part's tiles
 // that it sees.  For items whose V holds values that are not finite.
-__device__ __noinline__ void tl_row_again(const TlArgs& a, const TlItem& x, int64_t row, DnRow& r,
-                                          int lane) {
+__device__ __noinline__ DnRow tl_row_again(const TlArgs& a, TlItem x, int64_t row, int lane) {
+  DnRow r;
   const int64_t t = row >> a.lg;
   const int g = (int)(row & (a.G - 1));
   dn_row_begin(r, a.q + x.b * a.qs.seq + (int64_t)(x.h * a.G + g) * a.qs.head + t * a.qs.token,
@@ -372,61 +390,117 @@ __device__ __noinline__ void tl_row_again(const TlArgs& a, const TlItem& x, int6
     }
     dn_row_over(r, a.K + base, a.V + base, c0, end, lane);
   }
+  return r;
 }
 
+// Bits [0, n) of a word.
+__device__ __forceinline__ uint32_t tl_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
 // Scores [32 c, 32 c + 32) of the thread's row as loaded, -inf where it does not see them.
 __device__ __forceinline__ void tl_mask(uint32_t* s, int c, int hi, int lo, int sk) {
+  const uint32_t see = tl_below(hi - 32 * c) &
+                       (~tl_below(lo + 1 - 32 * c) | tl_below(sk - 32 * c));
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const int k = 32 * c + i;
-    if (k >= hi || (k <= lo && k >= sk)) s[i] = 0xFF800000u;
-  }
+  for (int i = 0; i < 32; ++i) s[i] = see & (1u << i) ? s[i] : 0xFF800000u;
 }
-// The row's weights 2^(s sl2 - m) as packed bf16, and their sum.
-__device__ __forceinline__ float tl_weights(uint32_t* pk, uint32_t s_at, float sl2, float m,
-                                            bool cut, int hi, int lo, int sk) {
+// The weights 2^(s sl2 - m) of 2 N scores as packed bf16, and their sum.
+template <int N>
+__device__ __forceinline__ float tl_weights(uint32_t* pk, const uint32_t* s, float sl2, float m) {
   const uint64_t sl = tl_two(sl2, sl2), mm = tl_two(-m, -m);
   uint64_t sum[2] = {0, 0};  // pairs of +0
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float u, v;
+    tl_of(tl_fma2(tl_two(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sl, mm), u, v);
+    u = tl_exp2(u);
+    v = tl_exp2(v);
+    sum[i & 1] = tl_add2(sum[i & 1], tl_two(u, v));
+    pk[i] = dn_pack(u, v);
+  }
+  float u, v;
+  tl_of(tl_add2(sum[0], sum[1]), u, v);
+  return u + v;
+}
+struct TlSeen {  // of a tile's tokens the row sees those below hi, and above lo or below sk
+  int hi, lo, sk;
+  bool cut;      // not all of them
+};
+// The weights of a tile's 128 scores, the next scores on their way while some are worked on.
+template <bool CUT>
+__device__ __forceinline__ float tl_tile_weights(uint32_t* pk, uint32_t s_at, float sl2, float m,
+                                                 const TlSeen& see) {
   uint32_t s[2][32];
+  float sum = 0.0f;
   tl_ld32(s[0], s_at);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t* x = s[c & 1];
     tl_wait_ld();
     tl_use32(x);
-    if (c < 3) tl_ld32(s[(c + 1) & 1], s_at + 32 * (c + 1));  // while these are worked on
-    if (cut) tl_mask(x, c, hi, lo, sk);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float u, v;
-      tl_of(tl_fma2(tl_two(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sl, mm), u, v);
-      u = tl_exp2(u);
-      v = tl_exp2(v);
-      sum[i & 1] = tl_add2(sum[i & 1], tl_two(u, v));
-      pk[16 * c + i] = dn_pack(u, v);
-    }
+    if (c < 3) tl_ld32(s[1 - (c & 1)], s_at + 32 * (c + 1));
+    if (CUT) tl_mask(x, c, see.hi, see.lo, see.sk);
+    sum += tl_weights<16>(pk + 16 * c, x, sl2, m);
   }
-  float u, v;
-  tl_of(tl_add2(sum[0], sum[1]), u, v);
-  return u + v;
+  return sum;
 }
-// The row's largest score.
-__device__ __noinline__ float tl_top(uint32_t s_at, bool cut, int hi, int lo, int sk) {
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
+
+// The tile again, for a warp with a row whose m does not fit its scores: m becomes the whole
+// number above the tile's largest score where that is higher, or where the row has no weight
+// yet; O (unless it is the item's first tile) and l move to it by a power of two, exactly;
+// the weights are stored.  Returns their sum.
+struct TlFit {
+  float m, l, sum;
+};
+__device__ __noinline__ TlFit tl_fit(float m, float l, uint32_t s_at, uint32_t o_at, bool with_o,
+                                     TlSeen see, float sl2) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
     uint32_t s[32];
-    tl_ld32(s, s_at + 32 * c);
+    tl_ld32(s, s_at + 32 * k);
     tl_wait_ld();
     tl_use32(s);
-    if (cut) tl_mask(s, c, hi, lo, sk);
+    if (see.cut) tl_mask(s, k, see.hi, see.lo, see.sk);
+    float y[2] = {mx, mx};
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
+    for (int i = 0; i < 32; i += 4)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mx[k] = tl_max3(mx[k], __uint_as_float(s[i + 2 * k]), __uint_as_float(s[i + 2 * k + 1]));
+      for (int h = 0; h < 2; ++h)
+        y[h] = tl_max3(y[h], __uint_as_float(s[i + 2 * h]), __uint_as_float(s[i + 2 * h + 1]));
+    mx = fmaxf(y[0], y[1]);
   }
-  return fmaxf(tl_max3(mx[0], mx[1], mx[2]), mx[3]);
+  const float top = ceilf(mx * sl2);
+  float f = 1.0f;
+  if (top > m || (l == 0.0f && top != -INFINITY)) {
+    f = l == 0.0f || m - top < -126.0f ? 0.0f : exp2f(m - top);
+    m = top;
+    l *= f;
+  }
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    uint32_t s[32], pk[16];
+    tl_ld32(s, s_at + 32 * k);
+    tl_wait_ld();
+    tl_use32(s);
+    if (see.cut) tl_mask(s, k, see.hi, see.lo, see.sk);
+    sum += tl_weights<16>(pk, s, sl2, m);
+    tl_st16(s_at + 16 * k, pk);
+  }
+  if (with_o) {
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      uint32_t o[32];
+      tl_ld32(o, o_at + 32 * k);
+      tl_wait_ld();
+      tl_use32(o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+      tl_st32(o_at + 32 * k, o);
+    }
+  }
+  return TlFit{m, l, sum};
 }
 
 // Softmax of the item's row tile `g` (dual: of every second token tile), and its result.
@@ -439,7 +513,7 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
   uint32_t done1 = 0;  // dual: tiles of the second group up to this item's end
   int mine_n = 0;      // items in which this group had tiles
   int other_n = 0;     // dual: items in which the second group had
-  for (int64_t id = blockIdx.x; id < a.items; id += gridDim.x) {
+  for (uint32_t id = blockIdx.x; id < a.items; id += gridDim.x) {
     const TlItem x = tl_item(a, id);
     if (!x.rows) continue;
     const int T = x.t[g];
@@ -452,7 +526,7 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
     const int64_t pa = x.p0 + ((x.r0 + (a.dual ? 0 : kDtRows * g)) >> a.lg);
     const int64_t pb =
         x.p0 + ((x.r0 + min((a.dual ? 0 : kDtRows * g) + kDtRows, x.rows) - 1) >> a.lg);
-    float m = -INFINITY, l = 0.0f;
+    float m = 0.0f, l = 0.0f;
     if (g == 1 && (x.nq == 1 || (a.dual && T == 0))) {  // nothing of the item is this group's
       base += tl_loads(a, x);
       continue;
@@ -470,48 +544,30 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
       if (!tl_wait_warp(&sm.abort, &sm.sfull[g], done & 1)) return;
       tl_fence_after();
       if (warp_on) {
-        const bool cut = !same || have < kDtKeys;
-        int hi = have, lo = -1, sk = kDtKeys;  // seen: below hi, and above lo or below sk
-        if (cut && a.causal) {
-          hi = (int)imax64(0, imin64(hi, p + 1 - c0));
-          sk = (int)imax64(0, imin64(kDtKeys, a.w.sink - c0));
-          lo = (int)imax64(-1, imin64(kDtKeys, p - a.w.window - c0));
+        TlSeen see = {have, -1, kDtKeys, !same || have < kDtKeys};
+        if (see.cut && a.causal) {
+          see.hi = (int)imax64(0, imin64(have, p + 1 - c0));
+          see.sk = (int)imax64(0, imin64(kDtKeys, a.w.sink - c0));
+          see.lo = (int)imax64(-1, imin64(kDtKeys, p - a.w.window - c0));
         }
+        const bool some = see.hi > 0 && (see.lo + 1 < see.hi || see.sk > 0);
         uint32_t pk[kDtKeys / 2];
-        float sum;
-        // the weights against m as it stands; a sum that says that m is too low (or that
-        // there is none yet) brings the maximum, m and O up to date, and the weights again
-        const bool first = m == -INFINITY;
-        bool low = first;
-        if (!__any_sync(0xFFFFFFFFu, first)) {
-          sum = tl_weights(pk, s_at, a.sl2, m, cut, hi, lo, sk);
-          low = !(sum <= kTlMost);
-        }
-        if (__any_sync(0xFFFFFFFFu, low)) {
-          const float top = tl_top(s_at, cut, hi, lo, sk) * a.sl2;
-          const bool need = low && top > m;
-          const float f = need ? tl_exp2(m - top) : 1.0f;  // m = -inf: 0
+        float sum = see.cut ? tl_tile_weights<true>(pk, s_at, a.sl2, m, see)
+                            : tl_tile_weights<false>(pk, s_at, a.sl2, m, see);
+        // m is far below a score, or far above all scores so far
+        const bool off = !(sum <= kTlMost) || (some && l + sum < kTlLeast);
+        if (!__any_sync(0xFFFFFFFFu, off)) {
+          tl_st32(s_at, pk);
+          tl_st32(s_at + 32, pk + 32);
+        } else {
           if (j > 0) {
             if (!tl_wait_warp(&sm.abort, &sm.pvdone[g], (done - 1) & 1)) return;
             tl_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tl_ld32(o, o_at + 32 * c);
-              tl_wait_ld();
-              tl_use32(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tl_st32(o_at + 32 * c, o);
-            }
           }
-          l *= f;
-          if (need) m = top;
-          sum = tl_weights(pk, s_at, a.sl2, m == -INFINITY ? 0.0f : m, cut, hi, lo, sk);
+          const TlFit y = tl_fit(m, l, s_at, o_at, j > 0, see, a.sl2);
+          m = y.m, l = y.l, sum = y.sum;
         }
         l += sum;
-        tl_st32(s_at, pk);
-        tl_st32(s_at + 32, pk + 32);
         tl_wait_st();
       }
       if (have < kDtKeys || !same) {
@@ -521,21 +577,22 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
         const uint32_t st = pos % kTlStages;
         if (!tl_wait_warp(&sm.abort, &sm.full[st], (pos / kTlStages) & 1)) return;
         uint4* v = reinterpret_cast<uint4*>(sm.ring[st]) + tid;
-        uint32_t worst = 0;  // largest magnitude bits of a half (exponent all ones: not finite)
-#pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
-          if ((((tid >> 3) + 16 * k) & 127) >= have) {
-            v[128 * k] = make_uint4(0u, 0u, 0u, 0u);
-          } else if (!same) {
-            const uint4 y = v[128 * k];
-            worst = __vmaxu2(worst, y.x & 0x7FFF7FFFu);
-            worst = __vmaxu2(worst, y.y & 0x7FFF7FFFu);
-            worst = __vmaxu2(worst, y.z & 0x7FFF7FFFu);
-            worst = __vmaxu2(worst, y.w & 0x7FFF7FFFu);
-          }
+        if (have < kDtKeys) {
+#pragma unroll 1
+          for (int k = 0; k < 16; ++k)
+            if ((((tid >> 3) + 16 * k) & 127) >= have) v[128 * k] = make_uint4(0u, 0u, 0u, 0u);
         }
-        if ((worst & 0xFFFFu) >= 0x7F80u || (worst >> 16) >= 0x7F80u)
-          *(volatile int*)&sm.bad[g][mine_n & 1] = mine_n;
+        if (!same) {
+          // an exponent of all ones and 1 more reach the half's top bit
+          uint32_t odd = 0;
+#pragma unroll 8
+          for (int k = 0; k < 16; ++k) {
+            const uint4 y = v[128 * k];
+            odd |= ((y.x & 0x7F807F80u) + 0x00800080u) | ((y.y & 0x7F807F80u) + 0x00800080u);
+            odd |= ((y.z & 0x7F807F80u) + 0x00800080u) | ((y.w & 0x7F807F80u) + 0x00800080u);
+          }
+          if (odd & 0x80008000u) *(volatile int*)&sm.bad[g][mine_n & 1] = mine_n;
+        }
         if (have < kDtKeys) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       }
       tl_fence_before();
@@ -544,6 +601,7 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
       ++done;
     }
     base += tl_loads(a, x);
+    if (l == 0.0f) m = -INFINITY;  // no weight
     if (T > 0) {
       if (!tl_wait_warp(&sm.abort, &sm.pvdone[g], (done - 1) & 1)) return;
       tl_fence_after();
@@ -652,8 +710,7 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
         const int li = (a.dual ? 0 : kDtRows * g) + 32 * warp + i;
         if (li >= x.rows) break;
         const int64_t rw = x.r0 + li;
-        DnRow r;
-        tl_row_again(a, x, rw, r, lane);
+        const DnRow r = tl_row_again(a, x, rw, lane);
         const int hd = x.h * a.G + (int)(rw & (a.G - 1));
         const int64_t tt = rw >> a.lg;
         if (a.splits == 1 && !a.parts_only) {
@@ -706,7 +763,7 @@ __device__ __forceinline__ bool tl_products(TlSmem& sm, const TlArgs& a, uint32_
   auto loaded = [&](const TlPos& p) {
     return tl_wait_warp(&sm.abort, &sm.full[p.stage], p.par);
   };
-  for (int64_t id = blockIdx.x; id < a.items; id += gridDim.x) {
+  for (uint32_t id = blockIdx.x; id < a.items; id += gridDim.x) {
     const TlItem x = tl_item(a, id);
     const int t0 = __shfl_sync(0xFFFFFFFFu, x.t[0], 0), t1 = __shfl_sync(0xFFFFFFFFu, x.t[1], 0);
     if (t0 == 0) continue;
@@ -768,70 +825,87 @@ __device__ __forceinline__ bool tl_products(TlSmem& sm, const TlArgs& a, uint32_
 }
 
 // One thread issues every K and V load of the CTA.
-__device__ __forceinline__ void tl_loader(TlSmem& sm, const TlArgs& a, const CUtensorMap* mk,
-                                          const CUtensorMap* mv) {
-  uint32_t n = 0;
-  bool ok = true;
-  auto load = [&](const CUtensorMap* map, const TlItem& x, int tile) {
-    const uint32_t st = n % kTlStages, round = n / kTlStages;
-    if (round && !tl_wait(&sm.abort, &sm.empty[st], (round - 1) & 1)) return false;
-    int64_t c0, end;
-    tl_tile(x, tile, c0, end);
-    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n" ::"r"(
-                     tl_su32(&sm.full[st])),
-                 "r"(kTlTile)
-                 : "memory");
-    tl_tma(sm.ring[st], map, 0, (int)c0, (int)x.bh, &sm.full[st]);
-    tl_tma(sm.ring[st] + kTlHalf, map, 64, (int)c0, (int)x.bh, &sm.full[st]);
-    ++n;
-    return true;
-  };
-  for (int64_t id = blockIdx.x; ok && id < a.items; id += gridDim.x) {
+struct TlLoader {
+  uint32_t n;
+  bool ok;
+};
+__device__ __forceinline__ void tl_load(TlSmem& sm, TlLoader& ld, const CUtensorMap* map,
+                                        const TlItem& x, int tile) {
+  if (!ld.ok) return;
+  const uint32_t st = ld.n % kTlStages, round = ld.n / kTlStages;
+  if (round && !tl_wait(&sm.abort, &sm.empty[st], (round - 1) & 1)) {
+    ld.ok = false;
+    return;
+  }
+  int64_t c0, end;
+  tl_tile(x, tile, c0, end);
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n" ::"r"(
+                   tl_su32(&sm.full[st])),
+               "r"(kTlTile)
+               : "memory");
+  tl_tma(sm.ring[st], map, 0, (int)c0, (int)x.bh, &sm.full[st]);
+  tl_tma(sm.ring[st] + kTlHalf, map, 64, (int)c0, (int)x.bh, &sm.full[st]);
+  ++ld.n;
+}
+// Steps [j0, j1) of an item's loads.
+__device__ __forceinline__ void tl_load_steps(TlSmem& sm, TlLoader& ld, const TlArgs& a,
+                                              const CUtensorMap* mk, const CUtensorMap* mv,
+                                              const TlItem& x, int j0, int j1) {
+  for (int j = j0; ld.ok && j < j1; ++j) {
+    const int i = tl_index(a, x, 0, j);
+    const bool two = a.dual && j < x.t[1];
+    tl_load(sm, ld, mk, x, i);
+    if (two) tl_load(sm, ld, mk, x, i + 1);
+    tl_load(sm, ld, mv, x, i);
+    if (two) tl_load(sm, ld, mv, x, i + 1);
+  }
+}
+// Steps that fill no more than the ring: loaded before the CTA's warps meet.
+__device__ __forceinline__ int tl_early(const TlArgs& a, const TlItem& x) {
+  return min(x.t[0], a.dual ? 1 : 2);
+}
+__device__ __forceinline__ void tl_loader(TlSmem& sm, TlLoader ld, const TlArgs& a,
+                                          const CUtensorMap* mk, const CUtensorMap* mv) {
+  for (uint32_t id = blockIdx.x; ld.ok && id < a.items; id += gridDim.x) {
     const TlItem x = tl_item(a, id);
-    if (x.tb == x.ta) continue;
-    for (int j = 0; ok && j < x.t[0]; ++j) {
-      if (!a.dual) {
-        ok = load(mk, x, x.ta + j) && load(mv, x, x.ta + j);
-      } else {
-        const int i = x.ta + 2 * j;
-        const bool two = j < x.t[1];
-        ok = load(mk, x, i) && (!two || load(mk, x, i + 1)) && load(mv, x, i) &&
-             (!two || load(mv, x, i + 1));
-      }
-    }
+    tl_load_steps(sm, ld, a, mk, mv, x, id == blockIdx.x ? tl_early(a, x) : 0, x.t[0]);
   }
   // every load has landed and every stage is released before the CTA ends
-  const uint32_t first = n > kTlStages ? n - kTlStages : 0;
-  for (uint32_t i = first; i < n; ++i) {
+  const uint32_t first = ld.n > kTlStages ? ld.n - kTlStages : 0;
+  for (uint32_t i = first; i < ld.n; ++i) {
     const uint32_t st = i % kTlStages, par = (i / kTlStages) & 1;
-    if (ok) ok = tl_wait(&sm.abort, &sm.empty[st], par);
-    if (!ok) tl_drain(&sm.full[st], par);
+    if (ld.ok) ld.ok = tl_wait(&sm.abort, &sm.empty[st], par);
+    if (!ld.ok) tl_drain(&sm.full[st], par);
   }
 }
 
-// Two warps load each item's query rows, in the swizzle of the products.
+// An item's query rows into shared memory, in the swizzle of the products.
+__device__ __forceinline__ void tl_load_q(TlSmem& sm, const TlArgs& a, const TlItem& x, int tid,
+                                          int threads) {
+  const int rows = a.dual ? kDtRows : x.nq * kDtRows;
+  const int c = tid & 15;
+  const uint16_t* base = a.q + x.b * a.qs.seq + (int64_t)x.h * a.G * a.qs.head + 8 * c;
+#pragma unroll 4
+  for (int r = tid >> 4; r < rows; r += threads >> 4) {
+    const int64_t row = x.r0 + min(r, x.rows - 1);
+    const uint16_t* src = base + (row & (a.G - 1)) * a.qs.head + (row >> a.lg) * a.qs.token;
+    const uint32_t dst = tl_su32(sm.q[r >> 7]) + (c >> 3) * kTlHalf + (r & 127) * 128 +
+                         (((c & 7) ^ (r & 7)) << 4);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+                 "r"(r < x.rows ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;\n" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+}
+// Two warps load the rows of each item with tiles but the CTA's first item.
 __device__ __forceinline__ void tl_queries(TlSmem& sm, const TlArgs& a) {
-  const int tid = threadIdx.x - 320;
   uint32_t items = 0;
-  for (int64_t id = blockIdx.x; id < a.items; id += gridDim.x) {
+  for (uint32_t id = blockIdx.x; id < a.items; id += gridDim.x) {
     const TlItem x = tl_item(a, id);
     if (x.tb == x.ta) continue;
     if (items && !tl_wait_warp(&sm.abort, &sm.qempty, (items - 1) & 1)) return;
-    const int rows = a.dual ? kDtRows : x.nq * kDtRows;
-    const int c = tid & 15;
-    for (int r = tid >> 4; r < rows; r += 4) {
-      const int64_t row = x.r0 + min(r, x.rows - 1);
-      const int64_t t = row >> a.lg;
-      const int head = x.h * a.G + (int)(row & (a.G - 1));
-      const uint16_t* src = a.q + x.b * a.qs.seq + head * a.qs.head + t * a.qs.token + 8 * c;
-      const uint32_t dst = tl_su32(sm.q[r >> 7]) + (c >> 3) * kTlHalf + (r & 127) * 128 +
-                           (((c & 7) ^ (r & 7)) << 4);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
-                   "r"(r < x.rows ? 16 : 0)
-                   : "memory");
-    }
-    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;\n" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    if (id != blockIdx.x) tl_load_q(sm, a, x, threadIdx.x - 320, 64);
     tl_arrive(&sm.qfull);
     ++items;
   }
@@ -843,7 +917,11 @@ __global__ void __launch_bounds__(kTlThreads, 1)
   extern __shared__ uint8_t raw[];
   TlSmem& sm = *reinterpret_cast<TlSmem*>(raw + ((1024u - (tl_su32(raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
+  // the kernel behind may start where there is room; it waits before it reads the parts
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  TlLoader ld = {0, true};
+  if (threadIdx.x == 288) {  // the loader's thread: the first loads are under way early
+    asm volatile("prefetch.tensormap [%0];\n\tprefetch.tensormap [%1];\n" ::"l"(&mk), "l"(&mv));
     for (int i = 0; i < kTlStages; ++i) {
       tl_init(&sm.full[i], 1);
       tl_init(&sm.empty[i], 1);
@@ -861,12 +939,16 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     tl_init(&sm.drain, 1);
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-  }
-  if (warp == 8) {
+    const TlItem x = tl_item(a, blockIdx.x);
+    tl_load_steps(sm, ld, a, &mk, &mv, x, 0, tl_early(a, x));
+  } else if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
                      tl_su32(&sm.tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  } else if (warp < 8) {
+    const TlItem x = tl_item(a, blockIdx.x);
+    if (x.tb > x.ta) tl_load_q(sm, a, x, threadIdx.x, 256);
   }
   tl_fence_before();
   __syncthreads();
@@ -885,7 +967,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         tl_drain(&sm.drain, 0);
       }
     } else if (warp == 9) {
-      if ((threadIdx.x & 31) == 0) tl_loader(sm, a, &mk, &mv);
+      if ((threadIdx.x & 31) == 0) tl_loader(sm, ld, a, &mk, &mv);
     } else {
       tl_queries(sm, a);
     }
@@ -918,6 +1000,7 @@ struct TlJoin {
 __global__ void __launch_bounds__(128) dense_join_kernel(TlJoin a) {
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  dn_wait_prior();
   if (i >= a.rows) return;
   const int64_t m = a.w.m, bhq = i / m, t = i - bhq * m;
   const int64_t b = bhq / a.Hq;
@@ -1010,8 +1093,8 @@ int tl_launch(TlArgs& a, int64_t rows_bh, const DtPlan& p, cudaStream_t st) {
   a.dual = p.dual;
   a.splits = p.splits;
   a.per = p.per;
-  a.items = p.items;
-  a.bh = rows_bh;
+  a.items = (uint32_t)p.items;
+  a.bh = (uint32_t)rows_bh;
   a.wide = ((uintptr_t)a.out & 31) == 0 && a.os.seq % 16 == 0 && a.os.head % 16 == 0 &&
            a.os.token % 16 == 0;
   if (int rc = set_smem_limit((const void*)dense_tile_kernel, kTlSmemBytes, "tile attention"))
@@ -1023,9 +1106,8 @@ int tl_launch(TlArgs& a, int64_t rows_bh, const DtPlan& p, cudaStream_t st) {
 }
 
 int tl_join(const TlJoin& j, cudaStream_t st) {
-  dense_join_kernel<<<(unsigned)((j.rows + 3) / 4), 128, 0, st>>>(j);
-  note_launches(1);
-  return check_launch("attention join");
+  return dn_launch_early("attention join", dense_join_kernel, (unsigned)((j.rows + 3) / 4), 128, 0,
+                         0, st, j);
 }
 
 // Partial results in a workspace: O first, then (m, l).
