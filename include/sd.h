@@ -500,8 +500,8 @@ int sd_kv4_gather_attend(const sd_shape* shape, const void* q, const sd_kv4* cac
  *   q_weight, k_weight: fp32 [d] (device) or NULL; with a weight, a head's row x becomes
  *     x / sqrt(mean(x^2) + eps) * weight, without one it is not normed.
  *   inv_freq: double [rot / 2] (device), radians per position; channel pair j is turned
- *     by the angle a = position * inv_freq[j] (a formed and reduced in 64 bits, so far
- *     positions keep their phase): (x, y) -> (x cos a - y sin a, y cos a + x sin a).
+ *     by the angle a = position * inv_freq[j] (formed and reduced in 64 bits, so far
+ *     positions keep their phase; finite values): (x, y) -> (x cos a - y sin a, y cos a + x sin a).
  *   rot: rotated channels, the first of the head; a multiple of 16 in [0, d] (0: no
  *     rotation, inv_freq not read).
  *   pairs: 0: pair j is channels j and j + rot / 2; 1: channels 2j and 2j + 1.

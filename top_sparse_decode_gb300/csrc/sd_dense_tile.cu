@@ -638,7 +638,9 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
     if (!again) {
       const bool final = a.splits == 1 && !a.parts_only;
       if (final) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        float inv;  // (to 2^-23; what it multiplies is rounded to bf16)
+        asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(l));
+        inv = l == 0.0f ? 0.0f : inv;
         f0 *= inv;
         f1 *= inv;
       }

@@ -6,22 +6,24 @@
 //   y_b cos t + y_a sin t),  t = position * inv_freq[j], pair j = (j, j + rot / 2) or
 //   (2j, 2j + 1).
 //
-// Bound by HBM: every row is read and written once (512 bytes), with some 15 instructions
-// per 16 bytes.  A CTA takes kRpTok tokens of a sequence (one, and a share of its heads,
-// where there are few): its threads form the tokens' angles first, one each, while the first
-// rows' loads are in flight -- in 64 bits up to the fraction of a turn, since position *
-// inv_freq reaches 10^6 radians -- and then 16 lanes take a row, 16 bytes a lane, kRpRows
-// rows of a lane in flight.  A pair's other channel is in the lane rot / 16 away (or in the
-// same lane, `pairs`), the row's sum of squares in a 16-lane shuffle tree.
+// Bound by HBM: every row is read and written once (512 bytes).  Sixteen lanes take a token
+// and walk heads, 16 bytes of a row a lane, kRpRows rows in flight.  What depends on the
+// token alone is formed once: its angles, since position * inv_freq reaches 10^6 radians as
+// the fraction of a turn, a whole number of 2^-64 per position times the position in 64-bit
+// integers, which drop the whole turns by themselves (64-bit floats run at 2 a cycle and SM
+// here); a thread forms a few of the CTA's, through shared memory; and per channel the factors A = w cos t and B = -+ w' sin t, w' the pair's other
+// weight, so that a row's channel is r (x A + x' B) with r the row's norm: the other channel
+// x' comes as it was loaded, from the lane rot / 16 away or (`pairs`) from the same word.
+// (With the angles read again and applied after the norm for every row the arithmetic was
+// the bound: 4 x 32,768 tokens of 48 heads took 1,064 us.)
 #include "sd_internal.cuh"
 
 namespace sd {
 namespace {
 
 constexpr int kRpThreads = 256;
-constexpr int kRpHalves = kRpThreads / 16;  // rows a CTA holds at a time
-constexpr int kRpRows = 3;                  // rows of a lane in flight
-constexpr int kRpTok = 4;                   // tokens per CTA where there are many
+constexpr int kRpTok = kRpThreads / 16;  // tokens per CTA
+constexpr int kRpRows = 4;               // rows of a lane in flight
 
 struct RpArgs {
   const uint16_t* q;
@@ -38,13 +40,13 @@ struct RpArgs {
   int rot;
   int Hq, Hkv;       // heads present (0: that side is absent)
   int Hv, Hcache;    // value heads present; KV heads of the cache
-  int64_t n, ncap, m, first;
+  int64_t n, ncap, first;
+  uint32_t m;
+  int64_t tokens;    // B * m
   const int32_t* pos;
   const int32_t* length;
   const int32_t* rotary;
-  int toks;          // tokens per CTA
-  int heads_per;     // heads per CTA
-  int64_t tiles;     // token tiles per sequence
+  int heads_per;     // heads per CTA (of queries, then keys, then values)
 };
 
 __device__ __forceinline__ uint32_t rp_pack(float lo, float hi) {
@@ -52,150 +54,152 @@ __device__ __forceinline__ uint32_t rp_pack(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+__device__ __forceinline__ uint32_t rp_word(const uint4& x, int i) {
+  return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+}
 
-// What a lane does with one row: where it comes from and goes to.
-struct RpRow {
-  const uint16_t* src;
-  uint16_t* dst;
-  const float* w;
-  int tok;    // token of the CTA's tile; -1: no row
-  int plain;  // a value row: copied
-};
-
-__device__ __forceinline__ RpRow rp_row(const RpArgs& a, int b, int64_t t0, int ntok, int h0,
-                                        int nh, int i, int64_t cache0) {
-  RpRow r;
-  r.tok = -1;
-  r.plain = 0;
-  r.w = nullptr;
-  r.src = nullptr;
-  r.dst = nullptr;
-  const int tok = i / nh, h = h0 + (i - tok * nh);
-  if (tok >= ntok) return r;
-  const int64_t t = t0 + tok;
-  if (h < a.Hq) {
-    r.src = a.q + b * a.qs.seq + h * a.qs.head + t * a.qs.token;
-    r.dst = a.qo + b * a.qos.seq + h * a.qos.head + t * a.qos.token;
-    r.w = a.qw;
-    r.tok = tok;
-    return r;
+// Heads [h, end) of a token: rows at src + h * sstep to dst + h * dstep.
+template <bool PAIRS, bool PLAIN>
+__device__ __forceinline__ void rp_heads(const uint16_t* src, int64_t sstep, uint16_t* dst,
+                                         int64_t dstep, int h, int end, bool on,
+                                         const float (&A)[8], const float (&B)[8], bool norm,
+                                         bool turned, int other, float eps) {
+  uint4 x[kRpRows];
+#pragma unroll
+  for (int u = 0; u < kRpRows; ++u) {
+    x[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (on && h + u < end) x[u] = *reinterpret_cast<const uint4*>(src + (h + u) * sstep);
   }
-  const int64_t at = cache0 + tok;
-  if (at < 0 || at >= a.n) return r;
-  const bool val = h >= a.Hq + a.Hkv;
-  const int hk = h - a.Hq - (val ? a.Hkv : 0);
-  const int64_t to = (((int64_t)b * a.Hcache + hk) * a.ncap + at) * kD;
-  if (val) {
-    r.src = a.v + b * a.vs.seq + hk * a.vs.head + t * a.vs.token;
-    r.dst = a.V + to;
-    r.plain = 1;
-  } else {
-    r.src = a.k + b * a.ks.seq + hk * a.ks.head + t * a.ks.token;
-    r.dst = a.K + to;
-    r.w = a.kw;
+  for (; h < end; h += kRpRows) {
+    uint4 next[kRpRows];
+#pragma unroll
+    for (int u = 0; u < kRpRows; ++u) {
+      next[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (on && h + kRpRows + u < end)
+        next[u] = *reinterpret_cast<const uint4*>(src + (h + kRpRows + u) * sstep);
+    }
+#pragma unroll
+    for (int u = 0; u < kRpRows; ++u) {
+      uint4 y = x[u];
+      if (!PLAIN) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = bf16_lo(rp_word(x[u], i));
+          f[2 * i + 1] = bf16_hi(rp_word(x[u], i));
+        }
+        float r = 1.0f;
+        if (norm) {
+          float ss = 0.0f, st = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            ss = fmaf(f[i], f[i], ss);
+            st = fmaf(f[i + 1], f[i + 1], st);
+          }
+          ss += st;
+#pragma unroll
+          for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+          r = rsqrtf(ss * (1.0f / kD) + eps);
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t own = rp_word(x[u], i);
+          const uint32_t o = PAIRS ? __byte_perm(own, own, 0x1032)
+                                   : __shfl_sync(0xFFFFFFFFu, own, other, 16);
+          float lo = f[2 * i] * A[2 * i], hi = f[2 * i + 1] * A[2 * i + 1];
+          if (turned) {
+            lo = fmaf(bf16_lo(o), B[2 * i], lo);
+            hi = fmaf(bf16_hi(o), B[2 * i + 1], hi);
+          }
+          w[i] = rp_pack(lo * r, hi * r);
+        }
+        y = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (on && h + u < end) *reinterpret_cast<uint4*>(dst + (h + u) * dstep) = y;
+      x[u] = next[u];
+    }
   }
-  r.tok = tok;
-  return r;
 }
 
 template <bool PAIRS>
 __global__ void __launch_bounds__(kRpThreads) norm_rope_kernel(RpArgs a) {
   __shared__ float2 cs[kRpTok][kD / 2];  // cos, sin
-  const int tid = threadIdx.x, lane16 = tid & 15, half = tid >> 4;
-  const int b = (int)(blockIdx.x / a.tiles);
-  const int64_t t0 = (blockIdx.x - b * a.tiles) * a.toks;
-  const int64_t len = a.length ? imin64(a.m, a.length[b]) : a.m;
-  const int ntok = (int)imin64(a.toks, len - t0);
-  if (ntok <= 0) return;
-  const int heads = a.Hq + a.Hkv + a.Hv;
-  const int h0 = blockIdx.y * a.heads_per, nh = min(a.heads_per, heads - h0);
-  const int64_t cache0 = a.first + (a.pos ? a.pos[b] : 0) + t0;
-  const int rows = ntok * nh;
-
-  RpRow r[kRpRows];
-  uint4 x[kRpRows];
-  auto load = [&](int base) {
-#pragma unroll
-    for (int u = 0; u < kRpRows; ++u) {
-      const int i = base + u * kRpHalves + half;
-      r[u] = rp_row(a, b, t0, i < rows ? ntok : 0, h0, nh, i, cache0);
-      x[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (r[u].tok >= 0) x[u] = *reinterpret_cast<const uint4*>(r[u].src + 8 * lane16);
-    }
-  };
-  load(0);
+  __shared__ uint64_t turn[kD / 2];      // turns per position, their fraction in 2^-64
+  const int tid = threadIdx.x, lane16 = tid & 15, slot = tid >> 4;
+  const int64_t t_cta = (int64_t)blockIdx.x * kRpTok;
   const int pairs = a.rot >> 1;
-  for (int i = tid; i < ntok * pairs; i += kRpThreads) {
-    const int tok = i / pairs, j = i - tok * pairs;
-    const int64_t p = a.rotary ? (int64_t)a.rotary[b] + t0 + tok : cache0 + tok;
-    // the angle in turns (1 / 2 pi), its whole turns dropped, all in 64 bits
-    const double turns = (double)p * a.freq[j] * 0.15915494309189533577;
-    const float half_turns = (float)(2.0 * (turns - rint(turns)));
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    cs[tok][j] = make_float2(c, s);
+  // the sequence and token of a place among the CTA's
+  auto where = [&](int i, int& b, uint32_t& t) {
+    const int64_t at = t_cta + i;
+    if (at >= a.tokens) return false;
+    b = a.tokens < ((int64_t)1 << 32) ? (int)((uint32_t)at / a.m) : (int)(at / a.m);
+    t = (uint32_t)(at - (int64_t)b * a.m);
+    return !a.length || (int64_t)t < a.length[b];
+  };
+  if (tid < pairs) {
+    const double x = a.freq[tid] * 0.15915494309189533577;  // 1 / 2 pi
+    turn[tid] = (uint64_t)__double2ll_rn((x - rint(x)) * 18446744073709551616.0);
+  }
+  __syncthreads();
+  for (int i = tid; i < kRpTok * pairs; i += kRpThreads) {
+    const int s = i / pairs, j = i - s * pairs;
+    int b;
+    uint32_t t;
+    if (!where(s, b, t)) continue;
+    const int64_t p = (a.rotary ? (int64_t)a.rotary[b] : a.first + (a.pos ? a.pos[b] : 0)) + t;
+    // whole turns drop out of the product's upper half
+    const float half_turns = (float)(int64_t)((uint64_t)p * turn[j]) * 0x1p-63f;
+    float s0, c0;
+    sincospif(half_turns, &s0, &c0);
+    cs[s][j] = make_float2(c0, s0);
   }
   __syncthreads();
 
-  const int c0 = 8 * lane16, hw = pairs >> 3;  // lanes to a pair's other channel
-  const bool turned = c0 < a.rot;
-  for (int base = 0;; ) {
+  int b = 0;
+  uint32_t t = 0;
+  const bool on = where(slot, b, t);
+  const int c0 = 8 * lane16;
+  const bool turned = c0 < a.rot, low = c0 < pairs;
+  const int other = !turned ? lane16 : low ? lane16 + (pairs >> 3) : lane16 - (pairs >> 3);
+  const int h0 = blockIdx.y * a.heads_per;
+  const int h1 = min(h0 + a.heads_per, a.Hq + a.Hkv + a.Hv);
+  const int64_t at = a.first + (a.pos ? a.pos[b] : 0) + t;
+  const bool in = on && at >= 0 && at < a.n;
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {  // queries, keys
+    const int s0 = side ? a.Hq : 0, s1 = side ? a.Hq + a.Hkv : a.Hq;
+    const int lo = max(h0, s0) - s0, hi = min(h1, s1) - s0;
+    if (lo >= hi) continue;
+    const float* w = side ? a.kw : a.qw;
+    float A[8], B[8];
 #pragma unroll
-    for (int u = 0; u < kRpRows; ++u) {
-      float f[8];
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
-      }
-      if (__any_sync(0xFFFFFFFFu, r[u].w != nullptr)) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-#pragma unroll
-        for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if (r[u].w) {
-          const float inv = rsqrtf(ss * (1.0f / kD) + a.eps);
-          const float4 w0 = *reinterpret_cast<const float4*>(r[u].w + c0);
-          const float4 w1 = *reinterpret_cast<const float4*>(r[u].w + c0 + 4);
-          f[0] *= inv * w0.x, f[1] *= inv * w0.y, f[2] *= inv * w0.z, f[3] *= inv * w0.w;
-          f[4] *= inv * w1.x, f[5] *= inv * w1.y, f[6] *= inv * w1.z, f[7] *= inv * w1.w;
-        }
-      }
-      const int tok = max(r[u].tok, 0);
-      if constexpr (PAIRS) {
-        if (turned) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 e = cs[tok][(c0 >> 1) + i];
-            const float p = f[2 * i], q = f[2 * i + 1];
-            f[2 * i] = p * e.x - q * e.y;
-            f[2 * i + 1] = q * e.x + p * e.y;
-          }
-        }
-      } else if (a.rot) {
-        const bool low = c0 < pairs;
-        const int other = turned ? (low ? lane16 + hw : lane16 - hw) : lane16;
-        const int j0 = low ? c0 : c0 - pairs;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_sync(0xFFFFFFFFu, f[i], other, 16);
-          if (turned) {
-            const float2 e = cs[tok][j0 + i];
-            f[i] = f[i] * e.x + (low ? -o : o) * e.y;
-          }
-        }
-      }
-      if (r[u].tok >= 0) {
-        const uint4 y = make_uint4(rp_pack(f[0], f[1]), rp_pack(f[2], f[3]),
-                                   rp_pack(f[4], f[5]), rp_pack(f[6], f[7]));
-        *reinterpret_cast<uint4*>(r[u].dst + c0) = r[u].plain ? x[u] : y;
+    for (int i = 0; i < 8; ++i) {
+      A[i] = w ? w[c0 + i] : 1.0f;
+      B[i] = 0.0f;
+      if (turned) {
+        const float2 e = cs[slot][PAIRS ? (c0 + i) >> 1 : (low ? c0 : c0 - pairs) + i];
+        const float wo = w ? w[PAIRS ? c0 + (i ^ 1) : 8 * other + i] : 1.0f;
+        const bool first = PAIRS ? !(i & 1) : low;
+        B[i] = (first ? -wo : wo) * e.y;
+        A[i] *= e.x;
       }
     }
-    base += kRpRows * kRpHalves;
-    if (base >= rows) break;
-    load(base);
+    const uint16_t* src = side ? a.k + b * a.ks.seq + t * a.ks.token
+                               : a.q + b * a.qs.seq + t * a.qs.token;
+    uint16_t* dst = side ? a.K + ((int64_t)b * a.Hcache * a.ncap + at) * kD
+                         : a.qo + b * a.qos.seq + t * a.qos.token;
+    rp_heads<PAIRS, false>(src + c0, side ? a.ks.head : a.qs.head, dst + c0,
+                           side ? a.ncap * kD : a.qos.head, lo, hi, side ? in : on, A, B,
+                           w != nullptr, turned, other, a.eps);
+  }
+  const int s0 = a.Hq + a.Hkv;
+  const int lo = max(h0, s0) - s0, hi = min(h1, s0 + a.Hv) - s0;
+  if (lo < hi) {
+    const float none[8] = {};
+    rp_heads<PAIRS, true>(a.v + b * a.vs.seq + t * a.vs.token + c0, a.vs.head,
+                          a.V + ((int64_t)b * a.Hcache * a.ncap + at) * kD + c0, a.ncap * kD, lo,
+                          hi, in, none, none, false, false, lane16, a.eps);
   }
 }
 
@@ -212,18 +216,18 @@ int launch_norm_rope(const Dims& s, const sd_rope& rope, const uint16_t* q, cons
   a.qw = rope.q_weight, a.kw = rope.k_weight, a.freq = rope.inv_freq;
   a.eps = rope.eps, a.rot = rope.rot;
   a.Hq = q ? s.Hq : 0, a.Hkv = k ? s.Hkv : 0, a.Hv = v ? s.Hkv : 0, a.Hcache = s.Hkv;
-  a.n = s.n, a.ncap = s.ncap, a.m = m, a.first = first;
+  a.n = s.n, a.ncap = s.ncap, a.m = (uint32_t)m, a.first = first;
   a.pos = pos, a.length = length, a.rotary = rotary;
+  a.tokens = (int64_t)s.B * m;
   const int heads = a.Hq + a.Hkv + a.Hv;
-  const int64_t sms = device_sm_count();
-  // few tokens: one per CTA, its heads over several CTAs
-  a.toks = (int64_t)s.B * m >= 4 * sms * kRpTok ? kRpTok : 1;
-  a.tiles = (m + a.toks - 1) / a.toks;
-  const int64_t ctas = a.tiles * s.B;
+  const int64_t ctas = (a.tokens + kRpTok - 1) / kRpTok;
   if (ctas >= (int64_t)1 << 31)
     return fail(SD_ERR_UNSUPPORTED, "sd_qk_norm_rope: batch * m too large");
-  a.heads_per = heads;
-  if (a.toks == 1 && ctas < 2 * sms) a.heads_per = min(heads, kRpHalves);
+  // few tokens: their heads over several CTAs, down to one round of rows, as long as each of
+  // the GPU's SMs has room for them (four CTAs)
+  const int64_t want = imax64(1, 4 * (int64_t)device_sm_count() / ctas);
+  const int64_t rounds = (heads + kRpRows - 1) / kRpRows;
+  a.heads_per = (int)((rounds + imin64(rounds, want) - 1) / imin64(rounds, want)) * kRpRows;
   const dim3 grid((unsigned)ctas, (unsigned)((heads + a.heads_per - 1) / a.heads_per));
   if (rope.pairs)
     norm_rope_kernel<true><<<grid, kRpThreads, 0, st>>>(a);
