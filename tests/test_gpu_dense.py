@@ -340,6 +340,53 @@ def test_window_repeats_and_graph(sd):
             assert torch.equal(out, a[3]) and torch.equal(lse, a[4])
 
 
+@pytest.mark.parametrize("off", [0, 16])
+def test_bases_on_16_bytes(sd, off):
+    """Inputs, outputs and workspaces that start on 16 bytes and no more."""
+    def at16(shape, dtype, fill=None):
+        n = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
+        raw = torch.zeros(n + 512, dtype=torch.uint8, device="cuda")
+        skip = off - raw.data_ptr() % 256 + 256
+        x = raw[skip:skip + n].view(dtype).view(shape)
+        assert x.data_ptr() % 256 == off
+        if fill is not None:
+            x.copy_(fill)
+        return x
+    B, hkv, G, n, window = 1, 2, 4, 3000, 2900
+    hq = hkv * G
+    K, V = (at16((B, hkv, n, D), torch.bfloat16, normal((B, hkv, n, D), s)) for s in (1, 2))
+    shape = sd.make_shape(B, hq, hkv, n)
+    for m in (1, 20, 300):
+        q = at16((B, hq, m, D), torch.bfloat16, normal((B, hq, m, D), 3))
+        out, lse = at16((B, hq, m, D), torch.bfloat16), at16((B, hq, m), torch.float32)
+        ws = at16((max(16, sd.sd_window_attend_workspace_size(shape, m, window)),), torch.uint8)
+        sd.sd_window_attend(shape, q, K, V, m, window, 0, SCALE, out, lse, ws, first=n - m)
+        check_window((B, hkv, G, n, n, m, n - m, None, None, window, 0), (q, K, V, out, lse))
+    p, own = 1500, 40
+    q = at16((B, hq, D), torch.bfloat16, normal((B, hq, D), 4))
+    out, lse = at16((B, hq, D), torch.bfloat16), at16((B, hq), torch.float32)
+    Kp, Vp = (at16((hkv, p, D), torch.bfloat16, normal((hkv, p, D), s)) for s in (5, 6))
+    Ko, Vo = (at16((B, hkv, own, D), torch.bfloat16, normal((B, hkv, own, D), s)) for s in (7, 8))
+    shape = sd.make_shape(B, hq, hkv, own)
+    ws = at16((max(16, sd.sd_prefix_attend_workspace_size(shape, p)),), torch.uint8)
+    sd.sd_prefix_attend(shape, q, Kp, Vp, p, Ko, Vo, SCALE, out, lse, ws)
+    check_prefix((B, hkv, G, p, p, own, own, None), (q, Kp, Vp, Ko, Vo, out, lse))
+
+
+@pytest.mark.parametrize("fallback", [False, True])
+def test_without_clusters(sd, fallback):
+    """Single tokens and own tokens joined in clusters, and by a kernel of their own."""
+    prev = sd.sd_set_fallback_paths(fallback)
+    try:
+        for case in ((1, 2, 4, 5000, 5000, 1, 4999, None, None, 4000, 100),
+                     (3, 1, 8, 700, 700, 1, 0, [699, 3, 350], None, 700, 0)):
+            check_window(case, run_window(sd, *case))
+        for case in ((2, 2, 4, 700, 700, 900, 900, [900, 17]), (1, 1, 1, 0, 0, 4000, 4000, None)):
+            check_prefix(case, run_prefix(sd, *case))
+    finally:
+        sd.sd_set_fallback_paths(prev)
+
+
 # ---- shared prefix -------------------------------------------------------------------------
 PREFIX = [
     # B, hkv, G, p, p_cap, n, n_cap, end

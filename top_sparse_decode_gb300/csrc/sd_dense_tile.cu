@@ -30,9 +30,9 @@
 // swizzle that the TMA writes.  Tensor memory: S 2 x 128 and O 2 x 128 columns, all 512.
 //
 // What a row does not see reaches nothing of it: scores by selection; V rows behind a
-// range's end are set to zero in shared memory; and where a tile's rows differ in what they
-// see, V is searched for values that are not finite (0 x inf is not 0), and an item that
-// holds one is computed again row by row.
+// range's end are set to zero in shared memory; and a row whose O comes out not finite, as
+// from a weight of 0 times an infinity that the row does not see (0 x inf is not 0), is
+// computed again by itself, token by token.
 //
 // Every wait is bounded: one that runs out sets the library's error word (sd_device_status)
 // and ends the CTA's work.
@@ -64,8 +64,6 @@ struct TlSmem {
   unsigned long long qfull, qempty;
   unsigned long long sfull[2], pfull[2], pvdone[2], oempty[2], mlfull, drain;
   float2 ml[kDtRows];   // dual: the second group's (m, l)
-  int bad[2][2];        // [group][item of the group & 1]: the last such item (counted from 1)
-                        // whose V held a value that is not finite
   uint32_t tmem;
   int abort;
 };
@@ -85,7 +83,7 @@ struct TlArgs {
   int Hkv, G, lg;     // lg: log2 G
   int64_t ncap;
   float sl2;          // scale * log2(e), above 0
-  int dual, splits, wide;  // wide: rows of out on 32 bytes
+  int dual, splits, wide;  // wide: rows of the result on 32 bytes
   int parts_only;          // splits == 1 leaves a partial result, too
   int64_t per;
   uint32_t items, bh;
@@ -274,6 +272,17 @@ __device__ __forceinline__ uint64_t tl_fma2(uint64_t a, uint64_t b, uint64_t c) 
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t tl_mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 32 bytes, on 32 bytes.
+__device__ __forceinline__ void tl_st256(void* dst, const uint32_t* y) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(y[0]),
+               "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+               : "memory");
+}
 __device__ __forceinline__ uint64_t tl_add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
@@ -369,7 +378,7 @@ __device__ __forceinline__ uint32_t tl_loads(const TlArgs& a, const TlItem& x) {
 }
 
 // A row's own (m, l, O) from the cache, its warp together: the tokens of the part's tiles
-// that it sees.  For items whose V holds values that are not finite.
+// that it sees.  For rows whose O is not finite.
 __device__ __noinline__ DnRow tl_row_again(const TlArgs& a, TlItem x, int64_t row, int lane) {
   DnRow r;
   const int64_t t = row >> a.lg;
@@ -511,8 +520,7 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
   uint32_t base = 0;   // ring position of the item's first load
   uint32_t done = 0;   // tiles of this group so far
   uint32_t done1 = 0;  // dual: tiles of the second group up to this item's end
-  int mine_n = 0;      // items in which this group had tiles
-  int other_n = 0;     // dual: items in which the second group had
+  uint32_t other_n = 0;  // dual: items in which the second group had tiles
   for (uint32_t id = blockIdx.x; id < a.items; id += gridDim.x) {
     const TlItem x = tl_item(a, id);
     if (!x.rows) continue;
@@ -531,7 +539,6 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
       base += tl_loads(a, x);
       continue;
     }
-    if (T > 0) ++mine_n;
     if (a.dual && x.t[1] > 0) ++other_n;
     if (a.dual) done1 += x.t[1];
     for (int j = 0; j < T; ++j) {
@@ -570,30 +577,15 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
         l += sum;
         tl_wait_st();
       }
-      if (have < kDtKeys || !same) {
-        // V rows behind the range's end become zero; rows that some do not see are searched
-        // for values that are not finite
+      if (have < kDtKeys) {  // V rows behind the range's end become zero
         const uint32_t pos = base + tl_vpos(a, x, g, j);
         const uint32_t st = pos % kTlStages;
         if (!tl_wait_warp(&sm.abort, &sm.full[st], (pos / kTlStages) & 1)) return;
         uint4* v = reinterpret_cast<uint4*>(sm.ring[st]) + tid;
-        if (have < kDtKeys) {
 #pragma unroll 1
-          for (int k = 0; k < 16; ++k)
-            if ((((tid >> 3) + 16 * k) & 127) >= have) v[128 * k] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (!same) {
-          // an exponent of all ones and 1 more reach the half's top bit
-          uint32_t odd = 0;
-#pragma unroll 8
-          for (int k = 0; k < 16; ++k) {
-            const uint4 y = v[128 * k];
-            odd |= ((y.x & 0x7F807F80u) + 0x00800080u) | ((y.y & 0x7F807F80u) + 0x00800080u);
-            odd |= ((y.z & 0x7F807F80u) + 0x00800080u) | ((y.w & 0x7F807F80u) + 0x00800080u);
-          }
-          if (odd & 0x80008000u) *(volatile int*)&sm.bad[g][mine_n & 1] = mine_n;
-        }
-        if (have < kDtKeys) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        for (int k = 0; k < 16; ++k)
+          if ((((tid >> 3) + 16 * k) & 127) >= have) v[128 * k] = make_uint4(0u, 0u, 0u, 0u);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       }
       tl_fence_before();
       __syncwarp();
@@ -618,10 +610,6 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
       if (!tl_wait_warp(&sm.abort, &sm.pvdone[1], (done1 - 1) & 1)) return;
       tl_fence_after();
     }
-    // all threads of a group have searched their parts of V before its last product
-    bool again = T > 0 && *(volatile int*)&sm.bad[g][mine_n & 1] == mine_n;
-    if (a.dual && x.t[1] > 0)
-      again = again || *(volatile int*)&sm.bad[1][other_n & 1] == other_n;
     float f0 = 1.0f, f1 = 0.0f;
     if (a.dual && x.t[1] > 0) {
       const float2 y = sm.ml[tid];
@@ -635,95 +623,104 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
     const int head = x.h * a.G + (int)(row & (a.G - 1));
     const int64_t prow = (x.bh * a.w.m * a.G + row) * a.splits + x.split;
     const int64_t orow = x.b * a.os.seq + head * a.os.head + t * a.os.token;
-    if (!again) {
-      const bool final = a.splits == 1 && !a.parts_only;
-      if (final) {
-        float inv;  // (to 2^-23; what it multiplies is rounded to bf16)
-        asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(l));
-        inv = l == 0.0f ? 0.0f : inv;
-        f0 *= inv;
-        f1 *= inv;
-      }
-      if (warp_on) {
+    const bool final = a.splits == 1 && !a.parts_only;
+    if (final) {
+      float inv;  // (to 2^-23; what it multiplies is rounded to bf16)
+      asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(l));
+      inv = l == 0.0f ? 0.0f : inv;
+      f0 *= inv;
+      f1 *= inv;
+    }
+    uint64_t odd = 0;  // 0 times every value of O: NaN if one is not finite
+    if (warp_on) {
+      const uint64_t f00 = tl_two(f0, f0), f11 = tl_two(f1, f1);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          if (x.t[0] > 0) {
-            tl_ld32(o, o_at + 32 * c);
-            tl_wait_ld();
-            tl_use32(o);
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0u;
+        if (x.t[0] > 0) {
+          tl_ld32(o, o_at + 32 * c);
+          tl_wait_ld();
+          tl_use32(o);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float u, v;
+            tl_of(tl_mul2(tl_two(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f00), u, v);
+            o[i] = __float_as_uint(u);
+            o[i + 1] = __float_as_uint(v);
           }
+        }
+        if (a.dual && x.t[1] > 0) {
+          uint32_t o1[32];
+          tl_ld32(o1, o_at + 128 + 32 * c);
+          tl_wait_ld();
+          tl_use32(o1);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            o[i] = x.t[0] > 0 ? __float_as_uint(__uint_as_float(o[i]) * f0) : 0u;
-          if (a.dual && x.t[1] > 0) {
-            uint32_t o1[32];
-            tl_ld32(o1, o_at + 128 + 32 * c);
-            tl_wait_ld();
-            tl_use32(o1);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o[i])));
+          for (int i = 0; i < 32; i += 2) {
+            float u, v;
+            tl_of(tl_fma2(tl_two(__uint_as_float(o1[i]), __uint_as_float(o1[i + 1])), f11,
+                          tl_two(__uint_as_float(o[i]), __uint_as_float(o[i + 1]))),
+                  u, v);
+            o[i] = __float_as_uint(u);
+            o[i + 1] = __float_as_uint(v);
           }
-          if (mine && final) {
-            uint32_t y[16];
+        }
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              y[i] = l == 0.0f ? 0u
-                               : dn_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-            uint16_t* dst = a.out + orow + 32 * c;
-            if (a.wide) {  // whole 32-byte sectors
+        for (int i = 0; i < 32; i += 2)
+          odd = tl_fma2(tl_two(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), 0ull, odd);
+        if (mine && final) {
+          uint32_t y[16];
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(
-                                 dst + 16 * i),
-                             "r"(y[8 * i]), "r"(y[8 * i + 1]), "r"(y[8 * i + 2]), "r"(y[8 * i + 3]),
-                             "r"(y[8 * i + 4]), "r"(y[8 * i + 5]), "r"(y[8 * i + 6]),
-                             "r"(y[8 * i + 7])
-                             : "memory");
-            } else {
+          for (int i = 0; i < 16; ++i)
+            y[i] = dn_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+          uint16_t* dst = a.out + orow + 32 * c;
+          if (a.wide) {  // whole 32-byte sectors
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(dst + 8 * i) =
-                    make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-            }
-          } else if (mine) {
-            float* dst = a.part_o + prow * kD + 32 * c;
+            for (int i = 0; i < 2; ++i) tl_st256(dst + 16 * i, y + 8 * i);
+          } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(
-                               dst + 8 * i),
-                           "r"(o[8 * i]), "r"(o[8 * i + 1]), "r"(o[8 * i + 2]), "r"(o[8 * i + 3]),
-                           "r"(o[8 * i + 4]), "r"(o[8 * i + 5]), "r"(o[8 * i + 6]),
-                           "r"(o[8 * i + 7])
-                           : "memory");
+              *reinterpret_cast<uint4*>(dst + 8 * i) =
+                  make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
+        } else if (mine) {
+          float* dst = a.part_o + prow * kD + 32 * c;
+          if (a.wide) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tl_st256(dst + 8 * i, o + 8 * i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(dst + 4 * i) =
+                  make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
       }
-      if (mine) {
-        if (!final)
-          a.part_ml[prow] = make_float2(m, l);
-        else if (a.lse)
-          a.lse[((int64_t)x.b * a.Hkv * a.G + head) * a.w.m + t] =
-              l == 0.0f ? -INFINITY : (m + log2f(l)) * kDnLn2;
-      }
-    } else {
-      for (int i = 0; i < 32; ++i) {
-        const int li = (a.dual ? 0 : kDtRows * g) + 32 * warp + i;
-        if (li >= x.rows) break;
-        const int64_t rw = x.r0 + li;
-        const DnRow r = tl_row_again(a, x, rw, lane);
-        const int hd = x.h * a.G + (int)(rw & (a.G - 1));
-        const int64_t tt = rw >> a.lg;
-        if (a.splits == 1 && !a.parts_only) {
-          dn_row_end(r, a.out + x.b * a.os.seq + hd * a.os.head + tt * a.os.token,
-                     a.lse ? a.lse + ((int64_t)x.b * a.Hkv * a.G + hd) * a.w.m + tt : nullptr,
-                     lane);
-        } else {
-          const int64_t pr = (x.bh * a.w.m * a.G + rw) * a.splits + x.split;
-          reinterpret_cast<float4*>(a.part_o + pr * kD)[lane] = r.o;
-          if (lane == 0) a.part_ml[pr] = make_float2(r.m, r.l);
-        }
+    }
+    if (mine) {
+      if (!final)
+        a.part_ml[prow] = make_float2(m, l);
+      else if (a.lse)
+        a.lse[((int64_t)x.b * a.Hkv * a.G + head) * a.w.m + t] =
+            l == 0.0f ? -INFINITY : (m + log2f(l)) * kDnLn2;
+    }
+    // a row whose O is not finite may owe that to tokens that it does not see: again by itself
+    float odd0, odd1;
+    tl_of(odd, odd0, odd1);
+    for (uint32_t rows = __ballot_sync(0xFFFFFFFFu, mine && !(odd0 == 0.0f && odd1 == 0.0f)); rows;
+         rows &= rows - 1) {
+      const int64_t rw = x.r0 + (local - lane) + __ffs((int)rows) - 1;
+      const DnRow r = tl_row_again(a, x, rw, lane);
+      const int hd = x.h * a.G + (int)(rw & (a.G - 1));
+      const int64_t tt = rw >> a.lg;
+      if (final) {
+        dn_row_end(r, a.out + x.b * a.os.seq + hd * a.os.head + tt * a.os.token,
+                   a.lse ? a.lse + ((int64_t)x.b * a.Hkv * a.G + hd) * a.w.m + tt : nullptr, lane);
+      } else {
+        const int64_t pr = (x.bh * a.w.m * a.G + rw) * a.splits + x.split;
+        reinterpret_cast<float4*>(a.part_o + pr * kD)[lane] = r.o;
+        if (lane == 0) a.part_ml[pr] = make_float2(r.m, r.l);
       }
     }
     tl_fence_before();
@@ -935,7 +932,6 @@ __global__ void __launch_bounds__(kTlThreads, 1)
       tl_init(&sm.pfull[g], 4);
       tl_init(&sm.pvdone[g], 1);
       tl_init(&sm.oempty[g], 4);
-      sm.bad[g][0] = sm.bad[g][1] = 0;
     }
     tl_init(&sm.mlfull, 4);
     tl_init(&sm.drain, 1);
@@ -1097,8 +1093,10 @@ int tl_launch(TlArgs& a, int64_t rows_bh, const DtPlan& p, cudaStream_t st) {
   a.per = p.per;
   a.items = (uint32_t)p.items;
   a.bh = (uint32_t)rows_bh;
-  a.wide = ((uintptr_t)a.out & 31) == 0 && a.os.seq % 16 == 0 && a.os.head % 16 == 0 &&
-           a.os.token % 16 == 0;
+  a.wide = a.splits > 1 || a.parts_only
+               ? ((uintptr_t)a.part_o & 31) == 0
+               : ((uintptr_t)a.out & 31) == 0 && a.os.seq % 16 == 0 && a.os.head % 16 == 0 &&
+                     a.os.token % 16 == 0;
   if (int rc = set_smem_limit((const void*)dense_tile_kernel, kTlSmemBytes, "tile attention"))
     return rc;
   const unsigned grid = (unsigned)imin64(p.items, device_sm_count());
