@@ -62,7 +62,8 @@ struct TlSmem {
   uint8_t ring[kTlStages][kTlTile];
   unsigned long long full[kTlStages], empty[kTlStages];
   unsigned long long qfull, qempty;
-  unsigned long long sfull[2], pfull[2], pvdone[2], oempty[2], mlfull, drain;
+  // (a barrier for each half of a tile's weights and products: a group may be a half ahead)
+  unsigned long long sfull[2], pfull[2][2], pvhalf[2], pvdone[2], oempty[2], mlfull, drain;
   float2 ml[kDtRows];   // dual: the second group's (m, l)
   uint32_t tmem;
   int abort;
@@ -240,12 +241,12 @@ __device__ __forceinline__ void tl_qk(uint32_t s, uint32_t q, uint32_t k) {
     tl_mma_qk<true>(s, dq + off, dk + off);
   }
 }
-// O += P V: 16 tokens a product, two 8-row groups; 8 columns of P.
+// O += P V over 64 tokens: 16 a product, two 8-row groups; 8 columns of P.
 __device__ __forceinline__ void tl_pv(uint32_t o, uint32_t p, uint32_t v, bool add) {
   const uint32_t dv = tl_desc(v, kTlHalf);
   tl_mma_pv(o, p, dv, add);
 #pragma unroll
-  for (int kk = 1; kk < 8; ++kk) tl_mma_pv(o, p + 8 * kk, dv + ((2048 * kk) >> 4), 1u);
+  for (int kk = 1; kk < 4; ++kk) tl_mma_pv(o, p + 8 * kk, dv + ((2048 * kk) >> 4), 1u);
 }
 __device__ __forceinline__ bool tl_elect() {
   uint32_t p;
@@ -305,6 +306,7 @@ struct TlItem {
   int na, ta, tb;    // tiles of [0, s1); this part's tiles
   int t[2];          // token tiles of each softmax group
   int nq;            // row tiles (dual: 2 groups of one)
+  bool tail;         // holds its sequence's last row
 };
 
 __device__ __forceinline__ TlItem tl_item(const TlArgs& a, uint32_t id) {
@@ -321,6 +323,7 @@ __device__ __forceinline__ TlItem tl_item(const TlArgs& a, uint32_t id) {
   x.r0 = tile * (a.dual ? kDtRows : kDtPair);
   x.rows = (int)imax64(0, imin64(a.dual ? kDtRows : kDtPair, len * a.G - x.r0));
   x.p0 = a.causal ? a.w.at(x.b) : 0;
+  x.tail = a.causal && x.r0 + x.rows == len * a.G;
   x.ta = x.tb = x.na = 0;
   x.t[0] = x.t[1] = 0;
   x.nq = a.dual || x.rows > kDtRows ? 2 : 1;
@@ -406,12 +409,14 @@ __device__ __noinline__ DnRow tl_row_again(const TlArgs& a, TlItem x, int64_t ro
 __device__ __forceinline__ uint32_t tl_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
 }
-// Scores [32 c, 32 c + 32) of the thread's row as loaded, -inf where it does not see them.
-__device__ __forceinline__ void tl_mask(uint32_t* s, int c, int hi, int lo, int sk) {
+// Scores [32 c, 32 c + 32) of the thread's row as loaded, -inf where it does not see them;
+// returns a bit for each that it sees.
+__device__ __forceinline__ uint32_t tl_mask(uint32_t* s, int c, int hi, int lo, int sk) {
   const uint32_t see = tl_below(hi - 32 * c) &
                        (~tl_below(lo + 1 - 32 * c) | tl_below(sk - 32 * c));
 #pragma unroll
   for (int i = 0; i < 32; ++i) s[i] = see & (1u << i) ? s[i] : 0xFF800000u;
+  return see;
 }
 // The weights 2^(s sl2 - m) of 2 N scores as packed bf16, and their sum.
 template <int N>
@@ -435,37 +440,18 @@ struct TlSeen {  // of a tile's tokens the row sees those below hi, and above lo
   int hi, lo, sk;
   bool cut;      // not all of them
 };
-// The weights of a tile's 128 scores, the next scores on their way while some are worked on.
-template <bool CUT>
-__device__ __forceinline__ float tl_tile_weights(uint32_t* pk, uint32_t s_at, float sl2, float m,
-                                                 const TlSeen& see) {
-  uint32_t s[2][32];
-  float sum = 0.0f;
-  tl_ld32(s[0], s_at);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t* x = s[c & 1];
-    tl_wait_ld();
-    tl_use32(x);
-    if (c < 3) tl_ld32(s[1 - (c & 1)], s_at + 32 * (c + 1));
-    if (CUT) tl_mask(x, c, see.hi, see.lo, see.sk);
-    sum += tl_weights<16>(pk + 16 * c, x, sl2, m);
-  }
-  return sum;
-}
-
-// The tile again, for a warp with a row whose m does not fit its scores: m becomes the whole
-// number above the tile's largest score where that is higher, or where the row has no weight
-// yet; O (unless it is the item's first tile) and l move to it by a power of two, exactly;
-// the weights are stored.  Returns their sum.
+// Half a tile again, for a warp with a row whose m does not fit its scores: m becomes the
+// whole number above the half's largest score where that is higher, or where the row has no
+// weight yet; O (unless the item has none) and l move to it by a power of two, exactly; the
+// weights are stored.  Returns m, l and their sum.
 struct TlFit {
   float m, l, sum;
 };
-__device__ __noinline__ TlFit tl_fit(float m, float l, uint32_t s_at, uint32_t o_at, bool with_o,
-                                     TlSeen see, float sl2) {
+__device__ __noinline__ TlFit tl_fit(float m, float l, uint32_t s_at, uint32_t o_at, int half,
+                                     bool with_o, TlSeen see, float sl2) {
   float mx = -INFINITY;
 #pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 2 * half; k < 2 * half + 2; ++k) {
     uint32_t s[32];
     tl_ld32(s, s_at + 32 * k);
     tl_wait_ld();
@@ -488,7 +474,7 @@ __device__ __noinline__ TlFit tl_fit(float m, float l, uint32_t s_at, uint32_t o
   }
   float sum = 0.0f;
 #pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 2 * half; k < 2 * half + 2; ++k) {
     uint32_t s[32], pk[16];
     tl_ld32(s, s_at + 32 * k);
     tl_wait_ld();
@@ -550,46 +536,65 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
                                       (c0 + have <= a.w.sink || c0 > pb - a.w.window));
       if (!tl_wait_warp(&sm.abort, &sm.sfull[g], done & 1)) return;
       tl_fence_after();
-      if (warp_on) {
-        TlSeen see = {have, -1, kDtKeys, !same || have < kDtKeys};
-        if (see.cut && a.causal) {
-          see.hi = (int)imax64(0, imin64(have, p + 1 - c0));
-          see.sk = (int)imax64(0, imin64(kDtKeys, a.w.sink - c0));
-          see.lo = (int)imax64(-1, imin64(kDtKeys, p - a.w.window - c0));
-        }
-        const bool some = see.hi > 0 && (see.lo + 1 < see.hi || see.sk > 0);
-        uint32_t pk[kDtKeys / 2];
-        float sum = see.cut ? tl_tile_weights<true>(pk, s_at, a.sl2, m, see)
-                            : tl_tile_weights<false>(pk, s_at, a.sl2, m, see);
-        // m is far below a score, or far above all scores so far
-        const bool off = !(sum <= kTlMost) || (some && l + sum < kTlLeast);
-        if (!__any_sync(0xFFFFFFFFu, off)) {
-          tl_st32(s_at, pk);
-          tl_st32(s_at + 32, pk + 32);
-        } else {
-          if (j > 0) {
-            if (!tl_wait_warp(&sm.abort, &sm.pvdone[g], (done - 1) & 1)) return;
-            tl_fence_after();
-          }
-          const TlFit y = tl_fit(m, l, s_at, o_at, j > 0, see, a.sl2);
-          m = y.m, l = y.l, sum = y.sum;
-        }
-        l += sum;
-        tl_wait_st();
-      }
-      if (have < kDtKeys) {  // V rows behind the range's end become zero
+      if (x.tail && have < kDtKeys) {
+        // behind the sequence's last token the cache may hold anything: V rows become zero
         const uint32_t pos = base + tl_vpos(a, x, g, j);
         const uint32_t st = pos % kTlStages;
         if (!tl_wait_warp(&sm.abort, &sm.full[st], (pos / kTlStages) & 1)) return;
-        uint4* v = reinterpret_cast<uint4*>(sm.ring[st]) + tid;
+        uint8_t* v = sm.ring[st] + (tid >> 3 & 1) * kTlHalf + (tid & 7) * 16;
 #pragma unroll 1
-        for (int k = 0; k < 16; ++k)
-          if ((((tid >> 3) + 16 * k) & 127) >= have) v[128 * k] = make_uint4(0u, 0u, 0u, 0u);
+        for (int r = have + (tid >> 4); r < kDtKeys; r += 8)
+          *reinterpret_cast<uint4*>(v + r * 128) = make_uint4(0u, 0u, 0u, 0u);
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       }
-      tl_fence_before();
-      __syncwarp();
-      if (lane == 0) tl_arrive(&sm.pfull[g]);
+      TlSeen see = {have, -1, kDtKeys, !same || have < kDtKeys};
+      if (see.cut && a.causal) {
+        see.hi = (int)imax64(0, imin64(have, p + 1 - c0));
+        see.sk = (int)imax64(0, imin64(kDtKeys, a.w.sink - c0));
+        see.lo = (int)imax64(-1, imin64(kDtKeys, p - a.w.window - c0));
+      }
+      // by halves of 64 tokens, so that the first half's product with V runs beside the second
+      // half's weights
+      uint32_t s[2][32];
+      if (warp_on) tl_ld32(s[0], s_at);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (warp_on) {
+          uint32_t pk[32], seen = 1;
+          tl_wait_ld();
+          tl_use32(s[0]);
+          tl_ld32(s[1], s_at + 64 * half + 32);
+          if (see.cut) seen = tl_mask(s[0], 2 * half, see.hi, see.lo, see.sk);
+          float sum = tl_weights<16>(pk, s[0], a.sl2, m);
+          tl_wait_ld();
+          tl_use32(s[1]);
+          if (half == 0) tl_ld32(s[0], s_at + 64);
+          if (see.cut) seen |= tl_mask(s[1], 2 * half + 1, see.hi, see.lo, see.sk);
+          sum += tl_weights<16>(pk + 16, s[1], a.sl2, m);
+          // m is far below a score, or far above all scores so far
+          const bool off = !(sum <= kTlMost) || (seen && l + sum < kTlLeast);
+          if (!__any_sync(0xFFFFFFFFu, off)) {
+            tl_st32(s_at + 32 * half, pk);
+          } else {
+            tl_wait_ld();
+            tl_use32(s[0]);
+            const bool with_o = j > 0 || half > 0;
+            if (with_o) {  // the products so far are done
+              if (!tl_wait_warp(&sm.abort, half ? &sm.pvhalf[g] : &sm.pvdone[g],
+                                (done + half - 1) & 1))
+                return;
+              tl_fence_after();
+            }
+            const TlFit y = tl_fit(m, l, s_at, o_at, half, with_o, see, a.sl2);
+            m = y.m, l = y.l, sum = y.sum;
+          }
+          l += sum;
+          tl_wait_st();
+        }
+        tl_fence_before();
+        __syncwarp();
+        if (lane == 0) tl_arrive(&sm.pfull[g][half]);
+      }
       ++done;
     }
     base += tl_loads(a, x);
@@ -797,11 +802,19 @@ __device__ __forceinline__ bool tl_products(TlSmem& sm, const TlArgs& a, uint32_
           if (outs[g] && !tl_wait_warp(&sm.abort, &sm.oempty[g], (outs[g] - 1) & 1)) return false;
           ++outs[g];
         }
-        if (!tl_wait_warp(&sm.abort, &sm.pfull[g], par_p[g])) return false;
+        const uint32_t o = tmem + 256 + 128 * g, pp = tmem + 128 * g, v = ring + vp.stage * kTlTile;
+        if (!tl_wait_warp(&sm.abort, &sm.pfull[g][0], par_p[g])) return false;
+        tl_fence_after();
+        if (leader) {
+          tl_pv(o, pp, v, j > 0);
+          tl_commit(&sm.pvhalf[g]);
+        }
+        __syncwarp();
+        if (!tl_wait_warp(&sm.abort, &sm.pfull[g][1], par_p[g])) return false;
         par_p[g] ^= 1;
         tl_fence_after();
         if (leader) {
-          tl_pv(tmem + 256 + 128 * g, tmem + 128 * g, ring + vp.stage * kTlTile, j > 0);
+          tl_pv(o, pp + 32, v + kTlHalf / 2, true);
           tl_commit(&sm.pvdone[g]);
           if (last) tl_commit(&sm.empty[vp.stage]);
           if (more) {
@@ -929,7 +942,9 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     tl_init(&sm.qempty, 1);
     for (int g = 0; g < 2; ++g) {
       tl_init(&sm.sfull[g], 1);
-      tl_init(&sm.pfull[g], 4);
+      tl_init(&sm.pfull[g][0], 4);
+      tl_init(&sm.pfull[g][1], 4);
+      tl_init(&sm.pvhalf[g], 1);
       tl_init(&sm.pvdone[g], 1);
       tl_init(&sm.oempty[g], 4);
     }
