@@ -115,6 +115,7 @@ __device__ __forceinline__ bool tl_try(unsigned long long* b, uint32_t parity) {
 // Waits for the phase of the given parity to complete; false once the rounds ran out or
 // another thread of the CTA gave up.
 __device__ __forceinline__ bool tl_wait(int* abort, unsigned long long* b, uint32_t parity) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kTlSpin; ++i) {
     if (tl_try(b, parity)) return true;
     if (*(volatile int*)abort) return false;
@@ -214,13 +215,12 @@ constexpr uint32_t kTlInstr = (1u << 4) | (1u << 7) | (1u << 10) | ((128u / 8) <
                               ((128u / 16) << 24);
 constexpr uint32_t kTlInstrV = kTlInstr | (1u << 16);
 
-template <bool ADD>
-__device__ __forceinline__ void tl_mma_qk(uint32_t s, uint32_t q, uint32_t k) {
+__device__ __forceinline__ void tl_mma_qk(uint32_t s, uint32_t q, uint32_t k, uint32_t add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %3};\n\t"
       "mov.b64 db, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(s),
-      "r"(q), "r"(k), "r"(kTlDescHi), "r"(kTlInstr), "n"(ADD ? 1 : 0)
+      "r"(q), "r"(k), "r"(kTlDescHi), "r"(kTlInstr), "r"(add)
       : "memory");
 }
 __device__ __forceinline__ void tl_mma_pv(uint32_t o, uint32_t p, uint32_t v, uint32_t add) {
@@ -234,19 +234,19 @@ __device__ __forceinline__ void tl_mma_pv(uint32_t o, uint32_t p, uint32_t v, ui
 // S = Q K^T by one thread: 16 channels a product, 32 bytes of a 64-channel half.
 __device__ __forceinline__ void tl_qk(uint32_t s, uint32_t q, uint32_t k) {
   const uint32_t dq = tl_desc(q, 16), dk = tl_desc(k, 16);
-  tl_mma_qk<false>(s, dq, dk);
-#pragma unroll
-  for (int kk = 1; kk < 8; ++kk) {
-    const uint32_t off = ((kk >> 2) * kTlHalf + (kk & 3) * 32) >> 4;
-    tl_mma_qk<true>(s, dq + off, dk + off);
+  tl_mma_qk(s, dq, dk, 0u);
+#pragma unroll 1
+  for (uint32_t kk = 1; kk < 8; ++kk) {
+    const uint32_t off = (kk >> 2) * (kTlHalf >> 4) + (kk & 3) * 2;
+    tl_mma_qk(s, dq + off, dk + off, 1u);
   }
 }
 // O += P V over 64 tokens: 16 a product, two 8-row groups; 8 columns of P.
 __device__ __forceinline__ void tl_pv(uint32_t o, uint32_t p, uint32_t v, bool add) {
   const uint32_t dv = tl_desc(v, kTlHalf);
   tl_mma_pv(o, p, dv, add);
-#pragma unroll
-  for (int kk = 1; kk < 4; ++kk) tl_mma_pv(o, p + 8 * kk, dv + ((2048 * kk) >> 4), 1u);
+#pragma unroll 1
+  for (uint32_t kk = 1; kk < 4; ++kk) tl_mma_pv(o, p + 8 * kk, dv + 128 * kk, 1u);
 }
 __device__ __forceinline__ bool tl_elect() {
   uint32_t p;
@@ -409,14 +409,12 @@ __device__ __noinline__ DnRow tl_row_again(const TlArgs& a, TlItem x, int64_t ro
 __device__ __forceinline__ uint32_t tl_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
 }
-// Scores [32 c, 32 c + 32) of the thread's row as loaded, -inf where it does not see them;
-// returns a bit for each that it sees.
-__device__ __forceinline__ uint32_t tl_mask(uint32_t* s, int c, int hi, int lo, int sk) {
+// Scores [32 c, 32 c + 32) of the thread's row as loaded, -inf where it does not see them.
+__device__ __forceinline__ void tl_mask(uint32_t* s, int c, int hi, int lo, int sk) {
   const uint32_t see = tl_below(hi - 32 * c) &
                        (~tl_below(lo + 1 - 32 * c) | tl_below(sk - 32 * c));
 #pragma unroll
   for (int i = 0; i < 32; ++i) s[i] = see & (1u << i) ? s[i] : 0xFF800000u;
-  return see;
 }
 // The weights 2^(s sl2 - m) of 2 N scores as packed bf16, and their sum.
 template <int N>
@@ -440,15 +438,22 @@ struct TlSeen {  // of a tile's tokens the row sees those below hi, and above lo
   int hi, lo, sk;
   bool cut;      // not all of them
 };
-// Half a tile again, for a warp with a row whose m does not fit its scores: m becomes the
-// whole number above the half's largest score where that is higher, or where the row has no
-// weight yet; O (unless the item has none) and l move to it by a power of two, exactly; the
-// weights are stored.  Returns m, l and their sum.
+// Whether m is far below a score, or far above all scores of the row so far (kTlMost,
+// kTlLeast), for any row of the warp.
+__device__ __forceinline__ bool tl_off(float sum, float l) {
+  return __any_sync(0xFFFFFFFFu, !(sum <= kTlMost) || l + sum < kTlLeast);
+}
+// The weights of half a tile for a warp whose rows see a part of it, or with a row whose m
+// does not fit: where the half's largest score is over 8 above m, or 30 below while the row
+// has no weight yet, m becomes the whole number above it, and l and O move by a power of two,
+// exactly.  with_o: O holds products, done when `b` completes its phase.
 struct TlFit {
-  float m, l, sum;
+  float m, l;
+  bool ok;
 };
-__device__ __noinline__ TlFit tl_fit(float m, float l, uint32_t s_at, uint32_t o_at, int half,
-                                     bool with_o, TlSeen see, float sl2) {
+__device__ __noinline__ TlFit tl_fit(int* abort, unsigned long long* b, uint32_t parity, float m,
+                                     float l, uint32_t s_at, uint32_t o_at, int half, bool with_o,
+                                     TlSeen see, float sl2) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int k = 2 * half; k < 2 * half + 2; ++k) {
@@ -467,23 +472,14 @@ __device__ __noinline__ TlFit tl_fit(float m, float l, uint32_t s_at, uint32_t o
   }
   const float top = ceilf(mx * sl2);
   float f = 1.0f;
-  if (top > m || (l == 0.0f && top != -INFINITY)) {
+  if (top > m + 8.0f || (l == 0.0f && top < m - 30.0f && top != -INFINITY)) {
     f = l == 0.0f || m - top < -126.0f ? 0.0f : exp2f(m - top);
     m = top;
     l *= f;
   }
-  float sum = 0.0f;
-#pragma unroll 1
-  for (int k = 2 * half; k < 2 * half + 2; ++k) {
-    uint32_t s[32], pk[16];
-    tl_ld32(s, s_at + 32 * k);
-    tl_wait_ld();
-    tl_use32(s);
-    if (see.cut) tl_mask(s, k, see.hi, see.lo, see.sk);
-    sum += tl_weights<16>(pk, s, sl2, m);
-    tl_st16(s_at + 16 * k, pk);
-  }
-  if (with_o) {
+  if (with_o && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
+    if (!tl_wait_warp(abort, b, parity)) return TlFit{m, l, false};
+    tl_fence_after();
 #pragma unroll 1
     for (int k = 0; k < 4; ++k) {
       uint32_t o[32];
@@ -495,7 +491,17 @@ __device__ __noinline__ TlFit tl_fit(float m, float l, uint32_t s_at, uint32_t o
       tl_st32(o_at + 32 * k, o);
     }
   }
-  return TlFit{m, l, sum};
+#pragma unroll 1
+  for (int k = 2 * half; k < 2 * half + 2; ++k) {
+    uint32_t s[32], pk[16];
+    tl_ld32(s, s_at + 32 * k);
+    tl_wait_ld();
+    tl_use32(s);
+    if (see.cut) tl_mask(s, k, see.hi, see.lo, see.sk);
+    l += tl_weights<16>(pk, s, sl2, m);
+    tl_st16(s_at + 16 * k, pk);
+  }
+  return TlFit{m, l, true};
 }
 
 // Softmax of the item's row tile `g` (dual: of every second token tile), and its result.
@@ -555,40 +561,33 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
       }
       // by halves of 64 tokens, so that the first half's product with V runs beside the second
       // half's weights
-      uint32_t s[2][32];
-      if (warp_on) tl_ld32(s[0], s_at);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         if (warp_on) {
-          uint32_t pk[32], seen = 1;
-          tl_wait_ld();
-          tl_use32(s[0]);
-          tl_ld32(s[1], s_at + 64 * half + 32);
-          if (see.cut) seen = tl_mask(s[0], 2 * half, see.hi, see.lo, see.sk);
-          float sum = tl_weights<16>(pk, s[0], a.sl2, m);
-          tl_wait_ld();
-          tl_use32(s[1]);
-          if (half == 0) tl_ld32(s[0], s_at + 64);
-          if (see.cut) seen |= tl_mask(s[1], 2 * half + 1, see.hi, see.lo, see.sk);
-          sum += tl_weights<16>(pk + 16, s[1], a.sl2, m);
-          // m is far below a score, or far above all scores so far
-          const bool off = !(sum <= kTlMost) || (seen && l + sum < kTlLeast);
-          if (!__any_sync(0xFFFFFFFFu, off)) {
-            tl_st32(s_at + 32 * half, pk);
-          } else {
+          bool fit = see.cut;
+          if (!fit) {
+            uint32_t s[2][32], pk[32];
+            tl_ld32(s[0], s_at + 64 * half);
             tl_wait_ld();
             tl_use32(s[0]);
-            const bool with_o = j > 0 || half > 0;
-            if (with_o) {  // the products so far are done
-              if (!tl_wait_warp(&sm.abort, half ? &sm.pvhalf[g] : &sm.pvdone[g],
-                                (done + half - 1) & 1))
-                return;
-              tl_fence_after();
+            tl_ld32(s[1], s_at + 64 * half + 32);  // while these are worked on
+            float sum = tl_weights<16>(pk, s[0], a.sl2, m);
+            tl_wait_ld();
+            tl_use32(s[1]);
+            sum += tl_weights<16>(pk + 16, s[1], a.sl2, m);
+            fit = tl_off(sum, l);
+            if (!fit) {
+              l += sum;
+              tl_st32(s_at + 32 * half, pk);
             }
-            const TlFit y = tl_fit(m, l, s_at, o_at, half, with_o, see, a.sl2);
-            m = y.m, l = y.l, sum = y.sum;
           }
-          l += sum;
+          if (fit) {
+            const TlFit y = tl_fit(&sm.abort, half ? &sm.pvhalf[g] : &sm.pvdone[g],
+                                   (done + half - 1) & 1, m, l, s_at, o_at, half,
+                                   j > 0 || half > 0, see, a.sl2);
+            if (!y.ok) return;
+            m = y.m, l = y.l;
+          }
           tl_wait_st();
         }
         tl_fence_before();
