@@ -454,6 +454,25 @@ struct TlFit {
 __device__ __noinline__ TlFit tl_fit(int* abort, unsigned long long* b, uint32_t parity, float m,
                                      float l, uint32_t s_at, uint32_t o_at, int half, bool with_o,
                                      TlSeen see, float sl2) {
+  if (see.cut) {  // as the whole halves: against m as it stands
+    uint32_t pk[32];
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t s[32];
+      tl_ld32(s, s_at + 64 * half + 32 * c);
+      tl_wait_ld();
+      tl_use32(s);
+      tl_mask(s, 2 * half + c, see.hi, see.lo, see.sk);
+      sum += tl_weights<16>(pk + 16 * c, s, sl2, m);
+    }
+    const int at = 64 * half;
+    const bool sees = see.hi > at && (see.lo + 1 < see.hi || see.sk > at);
+    if (!tl_off(sum, sees ? l : 1.0f)) {
+      tl_st32(s_at + 32 * half, pk);
+      return TlFit{m, l + sum, true};
+    }
+  }
   float mx = -INFINITY;
 #pragma unroll 1
   for (int k = 2 * half; k < 2 * half + 2; ++k) {
