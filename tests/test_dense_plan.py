@@ -20,8 +20,8 @@ def plan(tmp_path_factory):
     d = tmp_path_factory.mktemp("plan")
     src, lib = d / "plan.cc", d / "plan.so"
     src.write_text('#include "sd_dense_plan.cuh"\n'
-                   'extern "C" void tile(long long h, long long r, long long k, int sms, '
-                   'long long* o) {\n  auto p = sd::dt_plan(h, r, k, sms);\n'
+                   'extern "C" void tile(long long h, long long r, long long k, int sms, int min, '
+                   'long long* o) {\n  auto p = sd::dt_plan(h, r, k, sms, min);\n'
                    '  o[0] = p.dual, o[1] = p.per, o[2] = p.splits, o[3] = p.items;\n}\n'
                    'extern "C" void stream(long long r, long long t, int sms, int most, '
                    'long long* o) {\n  auto p = sd::sw_plan(r, t, sms, most);\n'
@@ -30,7 +30,7 @@ def plan(tmp_path_factory):
                     f"-I{CSRC}", str(src), "-o", str(lib)], check=True)
     dll = ctypes.CDLL(str(lib))
     ll = ctypes.c_longlong
-    dll.tile.argtypes = [ll, ll, ll, ctypes.c_int, ctypes.POINTER(ll)]
+    dll.tile.argtypes = [ll, ll, ll, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ll)]
     dll.stream.argtypes = [ll, ll, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ll)]
 
     def call(fn, n, *args):
@@ -41,19 +41,20 @@ def plan(tmp_path_factory):
 
 
 @pytest.mark.parametrize("sms", [1, 20, 152])
-def test_tile_cut(plan, sms):
+@pytest.mark.parametrize("least", [1, 4])
+def test_tile_cut(plan, sms, least):
     tile, _ = plan
     for heads in (1, 2, 8, 512, 65535):
         for rows in (1, 4, 128, 129, 256, 257, 5000, 131072 * 8):
             for keys in (1, 128, 129, 4300, 131072, (1 << 31) - 1):
-                dual, per, splits, items = tile(heads, rows, keys, sms)
+                dual, per, splits, items = tile(heads, rows, keys, sms, least)
                 assert dual == (rows <= 128)
                 size = 128 if dual else 256
                 assert (per - 1) * size < rows <= per * size
                 assert items == heads * per * splits and 1 <= splits <= max(1, sms)
                 assert splits == 1 or items <= sms
                 # a split has token tiles for both softmax groups
-                assert splits == 1 or splits * 2 * (2 if dual else 1) <= -(-keys // 128) + 1
+                assert splits == 1 or splits * least * (2 if dual else 1) <= -(-keys // 128) + 1
                 # tiles times splits stay in 32 bits
                 assert (-(-keys // 128) + 2) * (splits + 1) < 1 << 32
 

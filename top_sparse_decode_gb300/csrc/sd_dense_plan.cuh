@@ -26,15 +26,17 @@ struct DtPlan {
 };
 
 // Splits where the items are fewer than the SMs: as many as give each SM one, with at least
-// kDtMinTiles tiles for each softmax group of a part.
-constexpr int kDtMinTiles = 2;
-inline DtPlan dt_plan(int64_t heads, int64_t rows, int64_t keys, int sms) {
+// min_tiles tiles for each softmax group of a part: kDtOwnJoin where a kernel of its own
+// joins the parts (a window: it takes as long as three tiles or so), kDtFreeJoin where what
+// follows does (a prefix).
+constexpr int kDtOwnJoin = 4, kDtFreeJoin = 1;
+inline DtPlan dt_plan(int64_t heads, int64_t rows, int64_t keys, int sms, int min_tiles) {
   DtPlan p;
   p.dual = rows <= kDtRows;
   p.per = dt_ceil(rows, p.dual ? kDtRows : kDtPair);
   const int64_t base = heads * p.per;
   const int64_t tiles = dt_ceil(keys, kDtKeys) + 1;  // two ranges may end in a cut tile each
-  const int64_t most = dt_max(1, tiles / (kDtMinTiles * (p.dual ? 2 : 1)));
+  const int64_t most = dt_max(1, tiles / (min_tiles * (p.dual ? 2 : 1)));
   p.splits = (int)dt_max(1, dt_min(sms / base, most));
   p.items = base * p.splits;
   return p;

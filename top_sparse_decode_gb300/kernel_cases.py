@@ -34,6 +34,14 @@ the cases fix those.  Cases:
   kv4_attend    decode attention over a 4-bit cache, 8 KV heads x 256K tokens (302 MB)
   kv4_gather    ... over 129 blocks of 16 tokens per KV head, 64 x 8 heads x 16,384 tokens
                 (152 MB gathered)
+  norm_rope     queries and keys normed and rotated into the cache, 1 x 32,768 tokens of
+                32 + 8 + 8 heads (805 MB moved)
+  window        a prompt of 8,192 tokens under a 4,096-token window and 128 first tokens,
+                32 query and 8 KV heads (sd_window_attend)
+  window_decode one token of 64 sequences under a 1,024-token window, 8 KV heads
+                (sd_window_attend, 268 MB)
+  prefix        decode of 64 sequences over a shared prefix of 32,768 tokens and 64 tokens
+                of their own, 32 query and 8 KV heads (sd_prefix_attend)
   topk_quest    top-128 of 1,024 block scores (16-token blocks, last block forced) in
                 each of 64 x 8 rows (sd_topk), the Quest step's selection
 """
@@ -273,6 +281,35 @@ def make_case(name: str):
         cnt = torch.full((B * Hkv,), c, dtype=torch.int32, device=DEV)
         return lambda: sd.sd_kv4_gather_attend(shp, q, cache, idx, c, cnt, c, 1 / math.sqrt(128),
                                                out, lse, ws)
+    if name == "norm_rope":
+        Hq, Hkv, m = 32, 8, 32768
+        x = _bf16((1, m, Hq + 2 * Hkv, 128), gen).transpose(1, 2)
+        q, k, v = x.split([Hq, Hkv, Hkv], dim=1)
+        out = torch.empty((1, m, Hq, 128), dtype=torch.int16, device=DEV).transpose(1, 2)
+        K, V = (torch.empty((1, Hkv, m, 128), dtype=torch.int16, device=DEV) for _ in range(2))
+        w = torch.ones(128, device=DEV)
+        freq = 1e4 ** (-torch.arange(64, dtype=torch.float64, device=DEV) / 64)
+        rope, shp = sd.make_rope(freq, w, w), sd.make_shape(1, Hq, Hkv, m)
+        return lambda: sd.sd_qk_norm_rope(shp, rope, q, out, k, v, K, V, m)
+    if name in ("window", "window_decode"):
+        Hq, Hkv = 32, 8
+        B, n, m, window = (1, 8192, 8192, 4096) if name == "window" else (64, 2048, 1, 1024)
+        q, K, V = (_bf16((B, h, t, 128), gen) for h, t in ((Hq, m), (Hkv, n), (Hkv, n)))
+        out, shp = torch.empty_like(q), sd.make_shape(B, Hq, Hkv, n)
+        lse = torch.empty((B, Hq, m), dtype=torch.float32, device=DEV)
+        ws = torch.empty(max(sd.sd_window_attend_workspace_size(shp, m, window, 128), 256),
+                         dtype=torch.uint8, device=DEV)
+        return lambda: sd.sd_window_attend(shp, q, K, V, m, window, 128, 1 / math.sqrt(128), out,
+                                           lse, ws, first=n - m)
+    if name == "prefix":
+        B, Hq, Hkv, p, n = 64, 32, 8, 32768, 64
+        q, out = _bf16((B, Hq, 128), gen), torch.empty((B, Hq, 128), dtype=torch.int16, device=DEV)
+        Kp, Vp = _bf16((Hkv, p, 128), gen), _bf16((Hkv, p, 128), gen)
+        K, V = _bf16((B, Hkv, n, 128), gen), _bf16((B, Hkv, n, 128), gen)
+        shp = sd.make_shape(B, Hq, Hkv, n)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=DEV)
+        ws = torch.empty(sd.sd_prefix_attend_workspace_size(shp, p), dtype=torch.uint8, device=DEV)
+        return lambda: sd.sd_prefix_attend(shp, q, Kp, Vp, p, K, V, 1 / math.sqrt(128), out, lse, ws)
     if name == "merge":
         S, rows, k = 16, 64, 512
         cs = torch.randn((S, rows, k), device=DEV, generator=gen)
