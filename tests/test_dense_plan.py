@@ -20,8 +20,8 @@ def plan(tmp_path_factory):
     d = tmp_path_factory.mktemp("plan")
     src, lib = d / "plan.cc", d / "plan.so"
     src.write_text('#include "sd_dense_plan.cuh"\n'
-                   'extern "C" void tile(long long h, long long r, long long k, int sms, int min, '
-                   'long long* o) {\n  auto p = sd::dt_plan(h, r, k, sms, min);\n'
+                   'extern "C" void tile(long long h, long long r, long long k, int sms, int own, '
+                   'long long* o) {\n  auto p = sd::dt_plan(h, r, k, sms, own != 0);\n'
                    '  o[0] = p.dual, o[1] = p.per, o[2] = p.splits, o[3] = p.items;\n}\n'
                    'extern "C" void stream(long long r, long long t, int sms, int most, '
                    'long long* o) {\n  auto p = sd::sw_plan(r, t, sms, most);\n'
@@ -41,20 +41,21 @@ def plan(tmp_path_factory):
 
 
 @pytest.mark.parametrize("sms", [1, 20, 152])
-@pytest.mark.parametrize("least", [1, 4])
-def test_tile_cut(plan, sms, least):
+@pytest.mark.parametrize("own", [0, 1])
+def test_tile_cut(plan, sms, own):
     tile, _ = plan
     for heads in (1, 2, 8, 512, 65535):
         for rows in (1, 4, 128, 129, 256, 257, 5000, 131072 * 8):
             for keys in (1, 128, 129, 4300, 131072, (1 << 31) - 1):
-                dual, per, splits, items = tile(heads, rows, keys, sms, least)
+                dual, per, splits, items = tile(heads, rows, keys, sms, own)
                 assert dual == (rows <= 128)
                 size = 128 if dual else 256
                 assert (per - 1) * size < rows <= per * size
                 assert items == heads * per * splits and 1 <= splits <= max(1, sms)
                 assert splits == 1 or items <= sms
                 # a split has token tiles for both softmax groups
-                assert splits == 1 or splits * least * (2 if dual else 1) <= -(-keys // 128) + 1
+                least = 2 if not own else 8 if dual else 4
+                assert splits == 1 or splits * least <= -(-keys // 128) + 1
                 # tiles times splits stay in 32 bits
                 assert (-(-keys // 128) + 2) * (splits + 1) < 1 << 32
 

@@ -483,6 +483,85 @@ def test_prefix_equals_window_on_the_same_tokens(sd):
     assert (l.squeeze(2) - lse).abs().max() <= 1e-4
 
 
+def test_prefix_graph_and_no_lse(sd):
+    """A captured call follows new values in its inputs; without lse out is the same."""
+    case = (6, 2, 4, 2500, 2500, 300, 300, [300, 0, 17, 299, 150, 1])
+    B, hkv, G, p, pcap, n, cap, end = case
+    q, Kp, Vp, K, V, out, lse = run_prefix(sd, *case)
+    shape, ends = sd.make_shape(B, hkv * G, hkv, n), i32(end)
+    ws = torch.empty(sd.sd_prefix_attend_workspace_size(shape, p), dtype=torch.uint8,
+                     device="cuda")
+    o1, o2, l2 = torch.zeros_like(out), torch.zeros_like(out), torch.zeros_like(lse)
+    sd.sd_prefix_attend(shape, q, Kp, Vp, p, K, V, SCALE, o1, None, ws, end=ends)
+    assert torch.equal(o1, out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            sd.sd_prefix_attend(shape, q, Kp, Vp, p, K, V, SCALE, o2, l2, ws, end=ends)
+            sd.sd_prefix_attend(shape, q, Kp, Vp, p, K, V, SCALE, o2, l2, ws, end=ends)
+    for seed in (1, 2):
+        q.copy_(normal((B, hkv * G, D), 90 + seed))
+        ends.copy_(i32([(seed * 71 + 50 * b) % 301 for b in range(B)]))
+        K.copy_(normal(K.shape, 95 + seed))
+        V.copy_(normal(V.shape, 97 + seed))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        check_prefix((B, hkv, G, p, pcap, n, cap, ends.tolist()), (q, Kp, Vp, K, V, o2, l2))
+
+
+def test_two_streams(sd):
+    """Calls that run beside each other, each with its own workspace."""
+    case = (2, 2, 4, 2500, 2500, 200, 2300, None, None, 2400, 0)
+    want = run_window(sd, *case)
+    B, hkv, G, n, cap, m, first = case[:7]
+    shape = sd.make_shape(B, hkv * G, hkv, n)
+    outs, streams = [], [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for st in streams * 4:
+        with torch.cuda.stream(st):
+            out, lse = torch.zeros_like(want[3]), torch.zeros_like(want[4])
+            ws = torch.empty(max(16, sd.sd_window_attend_workspace_size(shape, m, 2400)),
+                             dtype=torch.uint8, device="cuda")
+            sd.sd_window_attend(shape, *want[:3], m, 2400, 0, SCALE, out, lse, ws, first=first)
+            outs.append((out, lse, ws))
+    torch.cuda.synchronize()
+    for out, lse, _ in outs:
+        assert torch.equal(out, want[3]) and torch.equal(lse, want[4])
+
+
+def test_caches_past_32_bits(sd):
+    """The last sequence of caches of more than 2^31 values: written, attended by many tokens
+    and by one, and as a prefix's own tokens."""
+    B, hkv, G, n, m = 17, 8, 1, 131072, 40
+    shape = sd.make_shape(B, hkv, hkv, n)
+    K, V = (torch.zeros((B, hkv, n, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert K.numel() > 1 << 31
+    K[-1, -1], V[-1, -1] = normal((n, D), 1), normal((n, D), 2)
+    q, k, v = (normal((B, hkv, m, D), s) for s in (3, 4, 5))
+    w, freq = torch.ones(D, device="cuda"), torch.rand(64, device="cuda", dtype=torch.float64)
+    qo, first = torch.zeros_like(q), n - m
+    sd.sd_qk_norm_rope(shape, sd.make_rope(freq, w, w), q, qo, k, v, K, V, m, first=first)
+    r = torch.arange(first, n, device="cuda")
+    ref = norm_rope(k[-1, -1], w, 1e-6, r, freq, 128, False)
+    check(K[-1, -1, first:], ref, norm_rope_tol(ref, k[-1, -1], w, 1e-6, r, freq, 128, False), "K")
+    assert torch.equal(V[-1, -1, first:], v[-1, -1])
+    for t, window in ((m, 600), (m, n), (1, n)):
+        out, lse = torch.zeros_like(q[:, :, :t]), torch.zeros((B, hkv, t), device="cuda")
+        ws = torch.empty(max(16, sd.sd_window_attend_workspace_size(shape, t, window, 4)),
+                         dtype=torch.uint8, device="cuda")
+        x = qo[:, :, m - t:].contiguous()
+        sd.sd_window_attend(shape, x, K, V, t, window, 4, SCALE, out, lse, ws, first=n - t)
+        p = torch.arange(n - t, n, device="cuda")
+        o, e, tol, ltol = attention(x[-1, -1], K[-1, -1], V[-1, -1],
+                                    visible(p, n, window, 4, "cuda"), SCALE)
+        check(out[-1, -1], o, tol, "out")
+        check(lse[-1, -1], e, ltol, "lse")
+    sd.sd_device_status()
+
+
 # ---- together ------------------------------------------------------------------------------
 def test_prompt_then_decode(sd):
     """A prompt goes through norm, rotation and window attention in chunks, then tokens one at

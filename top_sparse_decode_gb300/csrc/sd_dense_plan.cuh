@@ -25,19 +25,19 @@ struct DtPlan {
   int64_t items; // heads * per * splits
 };
 
-// Splits where the items are fewer than the SMs: as many as give each SM one, with at least
-// min_tiles tiles for each softmax group of a part: kDtOwnJoin where a kernel of its own
-// joins the parts (a window: it takes as long as three tiles or so), kDtFreeJoin where what
-// follows does (a prefix).
-constexpr int kDtOwnJoin = 4, kDtFreeJoin = 1;
-inline DtPlan dt_plan(int64_t heads, int64_t rows, int64_t keys, int sms, int min_tiles) {
+// Splits where the items are fewer than the SMs: as many as give each SM one, with some token
+// tiles for a part.  Where a kernel of its own joins the parts (a window) that takes as long
+// as three tiles or so: four for each softmax group (3 x 2 heads x 257 tokens of G = 8 under
+// a window of 501: 19.1 us, 21.4 with two).  Where what follows joins them (a prefix), two:
+// 17 x 4 heads of G = 8 over 5,003 tokens 19.0 us, 21.0 with one.
+inline DtPlan dt_plan(int64_t heads, int64_t rows, int64_t keys, int sms, bool own_join) {
   DtPlan p;
   p.dual = rows <= kDtRows;
   p.per = dt_ceil(rows, p.dual ? kDtRows : kDtPair);
   const int64_t base = heads * p.per;
   const int64_t tiles = dt_ceil(keys, kDtKeys) + 1;  // two ranges may end in a cut tile each
-  const int64_t most = dt_max(1, tiles / (min_tiles * (p.dual ? 2 : 1)));
-  p.splits = (int)dt_max(1, dt_min(sms / base, most));
+  const int64_t least = !own_join ? 2 : p.dual ? 8 : 4;
+  p.splits = (int)dt_max(1, dt_min(sms / base, tiles / least));
   p.items = base * p.splits;
   return p;
 }

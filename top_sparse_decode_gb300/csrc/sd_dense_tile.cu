@@ -1168,7 +1168,7 @@ static DtPlan window_plan(const Dims& s, int64_t m, int64_t window, int64_t sink
   const int64_t rows = m * s.G;
   const int64_t span = imin64(m, (rows <= kDtRows ? kDtRows : kDtPair) / s.G);
   const int64_t keys = imin64(s.n, imin64(sink, s.n) + imin64(window, s.n) + span - 1);
-  return dt_plan((int64_t)s.B * s.Hkv, rows, keys, device_sm_count(), kDtOwnJoin);
+  return dt_plan((int64_t)s.B * s.Hkv, rows, keys, device_sm_count(), true);
 }
 // Tokens that a single query token may see.
 static int64_t window_tokens(const Dims& s, int64_t window, int64_t sink) {
@@ -1217,7 +1217,7 @@ int launch_window_attend(const Dims& s, const uint16_t* q, const sd_strides& qs,
 }
 
 static DtPlan prefix_plan(const Dims& s, int64_t p) {
-  return dt_plan(s.Hkv, (int64_t)s.B * s.G, p, device_sm_count(), kDtFreeJoin);
+  return dt_plan(s.Hkv, (int64_t)s.B * s.G, p, device_sm_count(), false);
 }
 
 size_t prefix_attend_workspace_bytes(const Dims& s, int64_t p) {
