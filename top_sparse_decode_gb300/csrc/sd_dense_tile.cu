@@ -14,11 +14,15 @@
 // Per token tile and row tile: S = Q K^T (128 x 128 x 128, both operands from shared memory,
 // fp32 in tensor memory), p = 2^(s - m) by the softmax group whose thread owns the row, p
 // rounded to bf16 into the columns that S held, O += P V (P from tensor memory, V as it
-// lies).  The reference m begins at 0 and stands as long as a tile's weights sum up to 2^14 at
+// lies), by halves of 64 tokens: the first half's product runs beside the second half's
+// weights.  The rounding of p costs as much as that of the bf16 result (out is 1.4 times as
+// far from 64 bits); l and lse are of the sums before it.
+//
+// The reference m begins at 0 and stands as long as half a tile's weights sum up to 2^14 at
 // most and a row's so far to 2^-40 at least: a weight's rounding is relative to itself, so any
 // m in that range is as good as the maximum, which is then not sought (it took 400 of a
-// tile's 2,800 cycles).  Where it does not stand, the tile's maximum is sought, m set to the
-// whole number above it, and O and l moved by a power of two, exactly.
+// tile's 2,800 cycles).  Where it does not stand, the half's maximum is sought, m set to the
+// whole number above it, and O and l moved by a power of two, exactly (tl_fit).
 //
 // Roles (384 threads, one CTA per SM, persistent over items): warps 0-3 and 4-7 softmax and
 // output of the two row tiles, warp 8 issues the products, warp 9 the TMA loads, warps 10
@@ -30,9 +34,21 @@
 // swizzle that the TMA writes.  Tensor memory: S 2 x 128 and O 2 x 128 columns, all 512.
 //
 // What a row does not see reaches nothing of it: scores by selection; V rows behind a
-// range's end are set to zero in shared memory; and a row whose O comes out not finite, as
+// sequence's last token are set to zero in shared memory; and a row whose O comes out not finite, as
 // from a weight of 0 times an infinity that the row does not see (0 x inf is not 0), is
 // computed again by itself, token by token.
+//
+// What bounds it: the chain of a row tile, whose scores' product, two halves of softmax and
+// product with V follow each other; two row tiles in flight keep the tensor pipe busy for 56
+// to 60 % of the cycles.  32,768 tokens of 32 heads, window 4,096: 1,603 us, 1.32 PFLOP/s, 69
+// % of the measured bf16 rate; 4 x 4,096 tokens causal: 463 us, 62 %.  What its steps
+// measured on the first of these: products issued by one diverged thread 2,479 us, by a warp
+// 1,934; no maximum before the weights, products back to back 1,857; rows that are not finite
+// found in O, not by a search of V, 1,777; halves 1,757; the masked softmax out of line,
+// products and chunks in loops 1,638 (before that the code did not fit the instruction cache:
+// its misses ran at 67 % of what the cache behind it gives, now 14 %).  Slower: the maximum
+// and the weights by 32 columns with a vote each (2,125), the weights again by a loop around
+// the same code (2,179).
 //
 // Every wait is bounded: one that runs out sets the library's error word (sd_device_status)
 // and ends the CTA's work.
@@ -54,7 +70,7 @@ constexpr int kTlStages = 5;
 constexpr uint32_t kTlTile = kDtKeys * kD * 2;  // bytes of a K, V or Q tile: 32 KB
 constexpr uint32_t kTlHalf = kTlTile / 2;       // 64 channels of it
 constexpr uint32_t kTlSpin = 1u << 22;          // try_wait rounds before a wait gives up
-constexpr float kTlMost = 16384.0f;             // a tile's weights sum up to this at most,
+constexpr float kTlMost = 16384.0f;             // half a tile's weights sum up to this at most,
 constexpr float kTlLeast = 0x1p-40f;            // and a row's so far to this at least, or m moves
 
 struct TlSmem {

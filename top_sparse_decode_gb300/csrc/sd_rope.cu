@@ -14,8 +14,9 @@
 // here); a thread forms a few of the CTA's, through shared memory; and per channel the factors A = w cos t and B = -+ w' sin t, w' the pair's other
 // weight, so that a row's channel is r (x A + x' B) with r the row's norm: the other channel
 // x' comes as it was loaded, from the lane rot / 16 away or (`pairs`) from the same word.
-// (With the angles read again and applied after the norm for every row the arithmetic was
-// the bound: 4 x 32,768 tokens of 48 heads took 1,064 us.)
+// 4 x 32,768 tokens of 48 heads: 536 us, 6.0 TB/s, 89 % of the measured copy rate.  (With the
+// angles read again and applied after the norm for every row the arithmetic was the bound:
+// 1,064 us.  With angles in 64-bit floats 545, and 64 tokens 7.0 us, 5.8 now.)
 #include "sd_internal.cuh"
 
 namespace sd {
