@@ -554,9 +554,10 @@ int sd_qk_norm_rope(const sd_shape* shape, const sd_rope* rope, const void* q,
  *   q: bf16, strides as sd_qk_norm_rope's q; K, V: bf16 [B][hkv][n_cap][d]; out: bf16
  *   with strides of its own, rows apart; lse: fp32 [B][hq][m] or NULL.  pos, length: int32
  *   [B] (device), NULL meaning 0 and m.  Rows of tokens t >= length[b] are not written.
- *   scale >= 0.  Scores, sums and the softmax are fp32; the weights e^{z - m'} (m' from 14
- *   log 2 below the row's largest score so far to 40 log 2 above it) are rounded to bf16 for
- *   the product with V, and lse comes from the sums before that.
+ *   scale >= 0.  Scores, sums and the softmax are fp32.  For the product with V the weights
+ *   e^{z - m'} (m' from 14 log 2 below the row's largest score so far to 40 log 2 above it)
+ *   are rounded to bf16, with m = 1 to two bf16 parts (16 bits); lse comes from the sums
+ *   before that.
  *   A token that a query does not see reaches nothing of it, whatever its K and V hold
  *   (infinities and NaN included).
  *   Workspace: sd_window_attend_workspace_size() bytes (device, 16-byte aligned; 0 where
@@ -583,8 +584,9 @@ int sd_window_attend(const sd_shape* shape, const void* q, const sd_strides* q_s
  *   bf16 [B][hkv][n_cap][d], or both NULL (no own tokens; the shape's n is then not used);
  *   end: int32 [B] (device), NULL meaning n; out: bf16 [B][hq][d]; lse: fp32 [B][hq] or
  *   NULL.  p may be 0 (K_prefix, V_prefix not read).  A sequence with no token at all
- *   gives out = 0, lse = -inf.  scale, arithmetic and roundings as sd_window_attend; cache
- *   contents outside the ranges reach no output.
+ *   gives out = 0, lse = -inf.  scale and arithmetic as sd_window_attend (weights of the
+ *   prefix rounded to bf16, own tokens' to two parts); cache contents outside the ranges
+ *   reach no output.
  *   Workspace: sd_prefix_attend_workspace_size() bytes, as sd_window_attend's.
  *   Errors: SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED (p or n >= 2^31, B * hq >= 2^24),
  *   SD_ERR_WORKSPACE, SD_ERR_CUDA.

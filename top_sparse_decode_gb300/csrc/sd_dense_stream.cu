@@ -10,7 +10,8 @@
 // matrix loads meet no bank twice), 16 KB of a warp in flight, which 8 warps of an SM make
 // 128 KB.  S = Q K^T as m16n8k16 bf16 products (M: the group's heads), p = 2^(s - m) in fp32
 // with the reference m raised only when a group's maximum exceeds it by more than 2^8, O^T +=
-// V^T P^T with p rounded to bf16 and V^T read by transposing matrix loads.
+// V^T P^T with p as two bf16 parts (16 bits of it: the products have time to spare) and V^T
+// read by transposing matrix loads.
 //
 // Measured: 64 x 8 rows of up to 4,224 tokens 140 us (7.0 TB/s; a part stays in L2 between
 // passes), 64 x 8 of 1,152 after an L2 flush 48 us (6.4 TB/s, 94 % of the copy rate); 8 rows of
@@ -270,12 +271,13 @@ __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(SwArgs a) {
       if (need) m = top;
     }
     const float mu = m == -INFINITY ? 0.0f : m;
-    uint32_t p[2];
+    uint32_t p[2], rest[2];  // a weight as two bf16: 16 bits of it
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const float u = exp2f(x[n][0] - mu), v = exp2f(x[n][1] - mu);
       l += u + v;
       p[n] = dn_pack(u, v);
+      rest[n] = dn_pack(u - bf16_lo(p[n]), v - bf16_hi(p[n]));
     }
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
@@ -283,6 +285,7 @@ __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(SwArgs a) {
       uint32_t v[4];
       sw_ldmt(v, at + kSwHalf + t * kSwRow + (((2 * mt + ((lane >> 3) & 1)) ^ (t & 7)) << 4));
       mma_bf16(o[mt], v[0], v[1], v[2], v[3], p[0], p[1]);
+      mma_bf16(o[mt], v[0], v[1], v[2], v[3], rest[0], rest[1]);
     }
   }
   sw_cp_wait<0>();
