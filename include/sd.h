@@ -766,8 +766,9 @@ int sd_device_status(void* stream);
  * split-n gather-attend with workspace partials, the sampled-threshold
  * sample/filter/finish top-k, the one-CTA word-maxima top-k, sd_select_attend
  * as its two calls, and the cp.async bit-plane scan; sd_kv4_attend and
- * sd_kv4_gather_attend take their streaming kernel at every size.  Results are the
- * same.
+ * sd_kv4_gather_attend take their streaming kernel at every size; sd_window_attend of
+ * single tokens and sd_prefix_attend's own tokens join a row's parts by a kernel of its
+ * own.  Results are the same.
  * Returns the previous setting.
  */
 int sd_set_fallback_paths(int on);

@@ -1,6 +1,9 @@
 """sd_qk_norm_rope, sd_window_attend and sd_prefix_attend against their 64-bit forms
 (_dense.py), at the sizes, masks and layouts where they can go wrong."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -401,6 +404,7 @@ PREFIX = [
     (4, 8, 4, 20000, 20000, 700, 700, [700, 1, 0, 699]),
     (2, 1, 1, 129, 129, 5000, 5000, [5000, 4999]),
     (9, 2, 8, 500, 500, 0, 0, None),
+    (3, 1, 1, 40000, 40000, 3, 3, [3, 0, 1]),
 ]
 
 
@@ -510,6 +514,52 @@ def test_prefix_graph_and_no_lse(sd):
         g.replay()
         torch.cuda.synchronize()
         check_prefix((B, hkv, G, p, pcap, n, cap, ends.tolist()), (q, Kp, Vp, K, V, o2, l2))
+
+
+FIRST = """
+import torch, top_sparse_decode_gb300 as sd
+bf = dict(dtype=torch.bfloat16, device="cuda")
+B, hkv, G, n, m = 2, 2, 4, 3000, {m}
+hq, shape = hkv * G, sd.make_shape(2, 8, 2, 3000)
+x = torch.randn((B, hq + 2 * hkv, m, 128), device="cuda").bfloat16()
+q, k, v = x.split([hq, hkv, hkv], dim=1)
+K, V = torch.zeros((B, hkv, n, 128), **bf), torch.zeros((B, hkv, n, 128), **bf)
+w, f = torch.ones(128, device="cuda"), torch.rand(64, device="cuda", dtype=torch.float64)
+rope = sd.make_rope(f, w, w)
+ws = torch.zeros(max(16, sd.sd_window_attend_workspace_size(shape, m, n),
+                     sd.sd_prefix_attend_workspace_size(shape, n)), dtype=torch.uint8,
+                 device="cuda")
+qo, out = torch.zeros((B, hq, m, 128), **bf), torch.zeros((B, hq, m, 128), **bf)
+q1, o1 = torch.randn((B, hq, 128), device="cuda").bfloat16(), torch.zeros((B, hq, 128), **bf)
+l1 = torch.zeros((B, hq), device="cuda")
+def calls():
+    sd.sd_qk_norm_rope(shape, rope, q, qo, k, v, K, V, m, first=n - m)
+    sd.sd_window_attend(shape, qo, K, V, m, n, 0, 0.09, out, None, ws, first=n - m)
+    sd.sd_prefix_attend(shape, q1, K[0], V[0], n, K, V, 0.09, o1, l1, ws)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    calls()
+g.replay()
+torch.cuda.synchronize()
+a = out.clone(), o1.clone(), l1.clone(), K.clone()
+for y in (out, o1, l1):
+    y.zero_()
+calls()
+torch.cuda.synchronize()
+assert all(torch.equal(s, t) for s, t in zip(a, (out, o1, l1, K))) and out.abs().max() > 0
+sd.sd_device_status()
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("m", [1, 150])
+def test_first_calls_captured(sd, m):
+    """The very first calls of a process are made inside a capture."""
+    r = subprocess.run([sys.executable, "-c", FIRST.format(m=m)], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
 
 
 def test_two_streams(sd):

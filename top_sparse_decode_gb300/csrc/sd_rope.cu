@@ -229,6 +229,7 @@ int launch_norm_rope(const Dims& s, const sd_rope& rope, const uint16_t* q, cons
   const int64_t want = imax64(1, 4 * (int64_t)device_sm_count() / ctas);
   const int64_t rounds = (heads + kRpRows - 1) / kRpRows;
   a.heads_per = (int)((rounds + imin64(rounds, want) - 1) / imin64(rounds, want)) * kRpRows;
+  a.heads_per = max(a.heads_per, (heads + 65534) / 65535);  // a grid's second extent
   const dim3 grid((unsigned)ctas, (unsigned)((heads + a.heads_per - 1) / a.heads_per));
   if (rope.pairs)
     norm_rope_kernel<true><<<grid, kRpThreads, 0, st>>>(a);
