@@ -14,7 +14,7 @@
 // read by transposing matrix loads.
 //
 // Measured: 64 x 8 rows of up to 4,224 tokens 140 us (7.0 TB/s; a part stays in L2 between
-// passes), 64 x 8 of 1,152 after an L2 flush 48 us (6.4 TB/s, 94 % of the copy rate); 8 rows of
+// passes), 64 x 8 of 1,152 with cold caches 49 us (6.2 TB/s, 92 % of the copy rate); 8 rows of
 // 1,152 5.7 us, 8 of 32,768 31.6 us (4.2 TB/s: 38 CTAs a row and a kernel that joins them).
 //
 // Warps of a CTA join through shared memory, CTAs of a row through the cluster's (up to

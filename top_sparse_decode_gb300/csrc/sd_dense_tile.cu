@@ -46,7 +46,7 @@
 // maximum before the weights, products back to back 1,857; rows that are not finite found in
 // O, not by a search of V, 1,777; halves 1,757; the masked softmax out of line 1,603 (before
 // that the code did not fit the instruction cache: its misses ran at 67 % of what the cache
-// behind it gives, now 14 %); the products unrolled again 1,549.  Slower: the maximum and the
+// behind it gives, now 18 %); the products unrolled again 1,549.  Slower: the maximum and the
 // weights by 32 columns with a vote each (2,125), the weights again by a loop around the same
 // code (2,179), the softmax groups looking for landed tiles in the issuing warp's place
 // (1,637), a barrier for PV at an item's end only and stages released behind QK (1,602).
