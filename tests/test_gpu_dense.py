@@ -247,6 +247,43 @@ def test_window_unseen_tokens_reach_nothing(sd, m):
     check_window(case, got)
 
 
+def median_us(call, reps=21):
+    """Median time of a call, from events around each."""
+    for _ in range(3):
+        call()
+    marks = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
+             for _ in range(reps)]
+    for a, b in marks:
+        a.record()
+        call()
+        b.record()
+    torch.cuda.synchronize()
+    return sorted(a.elapsed_time(b) for a, b in marks)[reps // 2] * 1e3
+
+
+@pytest.mark.parametrize("G", [1, 4, 8])
+def test_window_unseen_tokens_cost_nothing(sd, G):
+    """Between the first tokens and the window, and behind the sequence, the cache holds NaN,
+    as one that was never written there may: the tiles that reach into these cells take no
+    longer for it.  (Rows computed again by themselves take more than ten times as long.)"""
+    first, window, sink, n, m = 1000, 256, 4, 4096, 2048
+    case = (1, 4, G, n, n, m, first, None, [m - 5], window, sink)
+
+    def spoil(q, K, V):
+        for x in (K, V):
+            x[:, :, sink:first - window + 1] = math.nan
+            x[:, :, first + m - 5:] = math.nan
+    clean, got = run_window(sd, *case), run_window(sd, *case, prep=spoil)
+    check_window(case, got, some=200)
+    shape, times, length = sd.make_shape(1, 4 * G, 4, n), [], i32([m - 5])
+    ws = torch.empty(max(16, sd.sd_window_attend_workspace_size(shape, m, window, sink)),
+                     dtype=torch.uint8, device="cuda")
+    for q, K, V, out, lse in (clean, got):
+        times.append(median_us(lambda: sd.sd_window_attend(
+            shape, q, K, V, m, window, sink, SCALE, out, lse, ws, length=length, first=first)))
+    assert times[1] <= 2 * times[0], times
+
+
 @pytest.mark.parametrize("where", [0, 127, 128, 200, 255, 399])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_window_bad_value_reaches_who_sees_it(sd, where, bad):

@@ -33,10 +33,11 @@
 // Shared memory: Q 64 KB, a ring of five 32 KB stages for K and V tiles, all in the 128-byte
 // swizzle that the TMA writes.  Tensor memory: S 2 x 128 and O 2 x 128 columns, all 512.
 //
-// What a row does not see reaches nothing of it: scores by selection; V rows behind a
-// sequence's last token are set to zero in shared memory; and a row whose O comes out not finite, as
-// from a weight of 0 times an infinity that the row does not see (0 x inf is not 0), is
-// computed again by itself, token by token.
+// What a row does not see reaches nothing of it: scores by selection; V rows of a tile that no
+// row sees, behind the first tokens or a sequence's last row, come as zeros or are set to zero
+// in shared memory; and a row whose O comes out not finite, as from a weight of 0 times an
+// infinity that the row does not see and others of its tile do (0 x inf is not 0), is computed
+// again by itself, token by token.
 //
 // What bounds it: the chain of a row tile, whose scores' product, two halves of softmax and
 // product with V follow each other; two row tiles in flight keep the tensor pipe busy for some
@@ -323,7 +324,7 @@ struct TlItem {
   int na, ta, tb;    // tiles of [0, s1); this part's tiles
   int t[2];          // token tiles of each softmax group
   int nq;            // row tiles (dual: 2 groups of one)
-  bool tail;         // holds its sequence's last row
+  int64_t behind;    // position behind the sequence's last row
 };
 
 __device__ __forceinline__ TlItem tl_item(const TlArgs& a, uint32_t id) {
@@ -340,7 +341,7 @@ __device__ __forceinline__ TlItem tl_item(const TlArgs& a, uint32_t id) {
   x.r0 = tile * (a.dual ? kDtRows : kDtPair);
   x.rows = (int)imax64(0, imin64(a.dual ? kDtRows : kDtPair, len * a.G - x.r0));
   x.p0 = a.causal ? a.w.at(x.b) : 0;
-  x.tail = a.causal && x.r0 + x.rows == len * a.G;
+  x.behind = x.p0 + len;
   x.ta = x.tb = x.na = 0;
   x.t[0] = x.t[1] = 0;
   x.nq = a.dual || x.rows > kDtRows ? 2 : 1;
@@ -578,8 +579,9 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
                                       (c0 + have <= a.w.sink || c0 > pb - a.w.window));
       if (!tl_wait_warp(&sm.abort, &sm.sfull[g], done & 1)) return;
       tl_fence_after();
-      if (x.tail && have < kDtKeys) {
-        // behind the sequence's last token the cache may hold anything: V rows become zero
+      if (a.causal && have < kDtKeys && c0 + kDtKeys > x.behind) {
+        // behind the sequence's last row the cache may hold anything: V rows become zero
+        // (the TMA gives zeros behind the first tokens, by a map that ends there)
         const uint32_t pos = base + tl_vpos(a, x, g, j);
         const uint32_t st = pos % kTlStages;
         if (!tl_wait_warp(&sm.abort, &sm.full[st], (pos / kTlStages) & 1)) return;
@@ -871,6 +873,10 @@ __device__ __forceinline__ bool tl_products(TlSmem& sm, const TlArgs& a, uint32_
   return !items || tl_wait_warp(&sm.abort, &sm.qempty, (items - 1) & 1);
 }
 
+struct TlMaps {
+  CUtensorMap k, v, vs;  // vs: V's first tokens, zeros behind them
+};
+
 // One thread issues every K and V load of the CTA.
 struct TlLoader {
   uint32_t n;
@@ -896,15 +902,14 @@ __device__ __forceinline__ void tl_load(TlSmem& sm, TlLoader& ld, const CUtensor
 }
 // Steps [j0, j1) of an item's loads.
 __device__ __forceinline__ void tl_load_steps(TlSmem& sm, TlLoader& ld, const TlArgs& a,
-                                              const CUtensorMap* mk, const CUtensorMap* mv,
-                                              const TlItem& x, int j0, int j1) {
+                                              const TlMaps& t, const TlItem& x, int j0, int j1) {
   for (int j = j0; ld.ok && j < j1; ++j) {
     const int i = tl_index(a, x, 0, j);
     const bool two = a.dual && j < x.t[1];
-    tl_load(sm, ld, mk, x, i);
-    if (two) tl_load(sm, ld, mk, x, i + 1);
-    tl_load(sm, ld, mv, x, i);
-    if (two) tl_load(sm, ld, mv, x, i + 1);
+    tl_load(sm, ld, &t.k, x, i);
+    if (two) tl_load(sm, ld, &t.k, x, i + 1);
+    tl_load(sm, ld, i < x.na ? &t.vs : &t.v, x, i);
+    if (two) tl_load(sm, ld, i + 1 < x.na ? &t.vs : &t.v, x, i + 1);
   }
 }
 // Steps that fill no more than the ring: loaded before the CTA's warps meet.
@@ -912,10 +917,10 @@ __device__ __forceinline__ int tl_early(const TlArgs& a, const TlItem& x) {
   return min(x.t[0], a.dual ? 1 : 2);
 }
 __device__ __forceinline__ void tl_loader(TlSmem& sm, TlLoader ld, const TlArgs& a,
-                                          const CUtensorMap* mk, const CUtensorMap* mv) {
+                                          const TlMaps& t) {
   for (uint32_t id = blockIdx.x; ld.ok && id < a.items; id += gridDim.x) {
     const TlItem x = tl_item(a, id);
-    tl_load_steps(sm, ld, a, mk, mv, x, id == blockIdx.x ? tl_early(a, x) : 0, x.t[0]);
+    tl_load_steps(sm, ld, a, t, x, id == blockIdx.x ? tl_early(a, x) : 0, x.t[0]);
   }
   // every load has landed and every stage is released before the CTA ends
   const uint32_t first = ld.n > kTlStages ? ld.n - kTlStages : 0;
@@ -959,8 +964,7 @@ __device__ __forceinline__ void tl_queries(TlSmem& sm, const TlArgs& a) {
 }
 
 __global__ void __launch_bounds__(kTlThreads, 1)
-    dense_tile_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                      const __grid_constant__ TlArgs a) {
+    dense_tile_kernel(const __grid_constant__ TlMaps maps, const __grid_constant__ TlArgs a) {
   extern __shared__ uint8_t raw[];
   TlSmem& sm = *reinterpret_cast<TlSmem*>(raw + ((1024u - (tl_su32(raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5;
@@ -968,7 +972,8 @@ __global__ void __launch_bounds__(kTlThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   TlLoader ld = {0, true};
   if (threadIdx.x == 288) {  // the loader's thread: the first loads are under way early
-    asm volatile("prefetch.tensormap [%0];\n\tprefetch.tensormap [%1];\n" ::"l"(&mk), "l"(&mv));
+    asm volatile("prefetch.tensormap [%0];\n\tprefetch.tensormap [%1];\n" ::"l"(&maps.k),
+                 "l"(&maps.v));
     for (int i = 0; i < kTlStages; ++i) {
       tl_init(&sm.full[i], 1);
       tl_init(&sm.empty[i], 1);
@@ -988,7 +993,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     const TlItem x = tl_item(a, blockIdx.x);
-    tl_load_steps(sm, ld, a, &mk, &mv, x, 0, tl_early(a, x));
+    tl_load_steps(sm, ld, a, maps, x, 0, tl_early(a, x));
   } else if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
                      tl_su32(&sm.tmem))
@@ -1015,7 +1020,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         tl_drain(&sm.drain, 0);
       }
     } else if (warp == 9) {
-      if ((threadIdx.x & 31) == 0) tl_loader(sm, ld, a, &mk, &mv);
+      if ((threadIdx.x & 31) == 0) tl_loader(sm, ld, a, maps);
     } else {
       tl_queries(sm, a);
     }
@@ -1131,9 +1136,13 @@ int tl_map(CUtensorMap* map, const uint16_t* base, int64_t n, int64_t ncap, int6
 }
 
 int tl_launch(TlArgs& a, int64_t rows_bh, const DtPlan& p, cudaStream_t st) {
-  CUtensorMap mk, mv;
-  if (int rc = tl_map(&mk, a.K, a.w.n, a.ncap, rows_bh)) return rc;
-  if (int rc = tl_map(&mv, a.V, a.w.n, a.ncap, rows_bh)) return rc;
+  TlMaps maps;
+  if (int rc = tl_map(&maps.k, a.K, a.w.n, a.ncap, rows_bh)) return rc;
+  if (int rc = tl_map(&maps.v, a.V, a.w.n, a.ncap, rows_bh)) return rc;
+  maps.vs = maps.v;
+  const int64_t firsts = imin64(a.w.sink, a.w.n);
+  if (firsts % kDtKeys)
+    if (int rc = tl_map(&maps.vs, a.V, firsts, a.ncap, rows_bh)) return rc;
   a.lg = a.G == 8 ? 3 : a.G == 4 ? 2 : a.G - 1;
   // scale 0: every score 0, as a product with a factor this small gives (0 would turn the
   // -inf of unseen tokens into NaN)
@@ -1150,7 +1159,7 @@ int tl_launch(TlArgs& a, int64_t rows_bh, const DtPlan& p, cudaStream_t st) {
   if (int rc = set_smem_limit((const void*)dense_tile_kernel, kTlSmemBytes, "tile attention"))
     return rc;
   const unsigned grid = (unsigned)imin64(p.items, device_sm_count());
-  dense_tile_kernel<<<grid, kTlThreads, kTlSmemBytes, st>>>(mk, mv, a);
+  dense_tile_kernel<<<grid, kTlThreads, kTlSmemBytes, st>>>(maps, a);
   note_launches(1);
   return check_launch("tile attention");
 }
