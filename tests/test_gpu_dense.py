@@ -307,6 +307,24 @@ def test_window_bad_value_reaches_who_sees_it(sd, where, bad):
         assert ((b.float() - a.float()).abs() <= 2.0 ** -5).all()
 
 
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("n", [1, 40, 600, 9000])
+def test_single_token_bad_value(sd, n, bad):
+    """Single tokens, and the own tokens behind a prefix: a value of V that is not finite comes
+    out as itself in its channel, whatever the weights of its token, and in no other."""
+    where = sorted({0, n // 3, n // 2, n - 1})
+
+    def spoil(q, K, V):
+        for j, w in enumerate(where):
+            V[0, :, w, 10 * j + 3] = bad
+    case = (2, 2, 4, n, n, 1, n - 1, None, None, n, 0)
+    got = run_window(sd, *case, prep=spoil)
+    check_window(case, got)
+    assert int((~torch.isfinite(got[3].float())).sum()) == 8 * len(where)
+    case = (2, 2, 4, 300, 300, n, n, None)
+    check_prefix(case, run_prefix(sd, *case, prep=lambda q, Kp, Vp, K, V: spoil(q, K, V)))
+
+
 def test_window_bad_key(sd):
     """A key that is not finite makes its own readers' scores NaN or infinite, and nothing
     else."""

@@ -271,13 +271,15 @@ __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(SwArgs a) {
       if (need) m = top;
     }
     const float mu = m == -INFINITY ? 0.0f : m;
-    uint32_t p[2], rest[2];  // a weight as two bf16: 16 bits of it
+    // a weight as two bf16, its upper half and what that leaves: 16 bits of it.  Neither part
+    // is negative, and the second not 0 either, so that an infinity in V stays what it is.
+    uint32_t p[2], rest[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const float u = exp2f(x[n][0] - mu), v = exp2f(x[n][1] - mu);
       l += u + v;
-      p[n] = dn_pack(u, v);
-      rest[n] = dn_pack(u - bf16_lo(p[n]), v - bf16_hi(p[n]));
+      p[n] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x7632);
+      rest[n] = dn_pack(fmaxf(u - bf16_lo(p[n]), 0x1p-126f), fmaxf(v - bf16_hi(p[n]), 0x1p-126f));
     }
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
