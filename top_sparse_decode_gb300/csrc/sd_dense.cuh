@@ -2,7 +2,9 @@
 // sd_prefix_attend): what its kernels share.
 #pragma once
 
+#include "sd_dense_plan.cuh"
 #include "sd_internal.cuh"
+#include "sd_mma.cuh"
 
 namespace sd {
 
@@ -78,9 +80,6 @@ __device__ __forceinline__ float4 dn_ld4(const uint16_t* p) {
 __device__ __forceinline__ void dn_row_begin(DnRow& r, const uint16_t* q, float sl2, int lane) {
   const float4 x = dn_ld4(q + 4 * lane);
   r.q = make_float4(x.x * sl2, x.y * sl2, x.z * sl2, x.w * sl2);
-  r.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  r.m = -INFINITY;
-  r.l = 0.0f;
 }
 __device__ __forceinline__ void dn_row_over(DnRow& r, const uint16_t* K, const uint16_t* V,
                                             int64_t i0, int64_t i1, int lane) {
@@ -109,6 +108,146 @@ __device__ __forceinline__ void dn_row_end(const DnRow& r, uint16_t* out, float*
   *reinterpret_cast<uint2*>(out + 4 * lane) =
       make_uint2(dn_pack(r.o.x * inv, r.o.y * inv), dn_pack(r.o.z * inv, r.o.w * inv));
   if (lse && lane == 0) *lse = r.l == 0.0f ? -INFINITY : (r.m + log2f(r.l)) * kDnLn2;
+}
+
+// ---- a warp's softmax of eight rows over groups of 16 tokens --------------------------------
+// S = Q K^T as m16n8k16 bf16 products (M: the rows, upper half empty), p = 2^(s - m) in fp32,
+// O^T += V^T P^T with p as two bf16 parts (16 bits of it) and V^T read by transposing matrix
+// loads.  A group's K and V lie in shared memory, chunks of 16 bytes XOR-swizzled by token, so
+// that the matrix loads meet no bank twice.
+constexpr uint32_t kDnRowBytes = kD * 2;
+constexpr uint32_t kDnHalf = kSwGroup * kDnRowBytes;  // a group's K: 4 KB; V behind it
+constexpr uint32_t kDnStage = 2 * kDnHalf;
+
+__device__ __forceinline__ uint32_t dn_su32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void dn_ldm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void dn_ldmt(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void dn_cp16(uint32_t dst, const uint16_t* src, bool v) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+               "r"(v ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void dn_cp_commit() {
+  asm volatile("cp.async.commit_group;\n" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void dn_cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+// Copies of a group whose first token is at element `at` of K and V, `have` of 16 tokens.
+__device__ __forceinline__ void dn_fetch(uint32_t stage, const uint16_t* K, const uint16_t* V,
+                                         int64_t at, int have, int lane) {
+  const int lr = lane >> 4, lc = lane & 15;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int t = 2 * k + lr;
+    const uint32_t dst = stage + t * kDnRowBytes + ((lc ^ (t & 7)) << 4);
+    const int64_t src = at + 8 * lc + (t < have ? t : 0) * kD;
+    dn_cp16(dst, K + src, t < have);
+    dn_cp16(dst + kDnHalf, V + src, t < have);
+  }
+}
+// Row gid = lane / 4 of S: m (log2 units) and this lane's share of l; columns 2 tig, 2 tig + 1
+// (tig = lane % 4) of O^T.
+struct DnEight {
+  float o[8][4];
+  float m, l;
+};
+__device__ __forceinline__ void dn_eight_begin(DnEight& x) {
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) x.o[mt][0] = x.o[mt][1] = x.o[mt][2] = x.o[mt][3] = 0.0f;
+  x.m = -INFINITY;
+  x.l = 0.0f;
+}
+// A group of `have` tokens; real: this lane's row exists.  m moves when a group's maximum is
+// more than `slack` above it.
+__device__ __forceinline__ void dn_eight_step(DnEight& x, const uint32_t (&qa)[8][2],
+                                              uint32_t at, int have, bool real, float sl2,
+                                              float slack, int lane) {
+  const int tig = lane & 3;
+  float sc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int t = 8 * n + (lane & 7);
+#pragma unroll
+    for (int kp = 0; kp < 4; ++kp) {
+      uint32_t k[4];
+      dn_ldm(k, at + t * kDnRowBytes + (((4 * kp + (lane >> 3)) ^ (t & 7)) << 4));
+      mma_bf16(sc[n], qa[2 * kp][0], 0u, qa[2 * kp][1], 0u, k[0], k[1]);
+      mma_bf16(sc[n], qa[2 * kp + 1][0], 0u, qa[2 * kp + 1][1], 0u, k[2], k[3]);
+    }
+  }
+  float z[2][2], top = -INFINITY;
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      z[n][e] = real && 8 * n + 2 * tig + e < have ? sc[n][e] * sl2 : -INFINITY;
+      top = fmaxf(top, z[n][e]);
+    }
+  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+  const bool need = top > x.m + slack;
+  if (__any_sync(0xFFFFFFFFu, need)) {
+    const float f = need ? exp2f(x.m - top) : 1.0f;  // m = -inf: 0
+    // O^T's columns 2tig, 2tig + 1 are rows whose factors the lanes of S's rows hold
+    const float fa = __shfl_sync(0xFFFFFFFFu, f, 8 * tig);
+    const float fb = __shfl_sync(0xFFFFFFFFu, f, 8 * tig + 4);
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      x.o[mt][0] *= fa;
+      x.o[mt][1] *= fb;
+      x.o[mt][2] *= fa;
+      x.o[mt][3] *= fb;
+    }
+    x.l *= f;
+    if (need) x.m = top;
+  }
+  const float mu = x.m == -INFINITY ? 0.0f : x.m;
+  // a weight as two bf16, its upper half and what that leaves: 16 bits of it.  Neither part is
+  // negative, and the second not 0 either, so that an infinity in V stays what it is.
+  uint32_t p[2], rest[2];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const float u = exp2f(z[n][0] - mu), v = exp2f(z[n][1] - mu);
+    x.l += u + v;
+    p[n] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x7632);
+    rest[n] = dn_pack(fmaxf(u - bf16_lo(p[n]), 0x1p-126f), fmaxf(v - bf16_hi(p[n]), 0x1p-126f));
+  }
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) {
+    const int t = (lane & 7) + 8 * (lane >> 4);
+    uint32_t v[4];
+    dn_ldmt(v, at + kDnHalf + t * kDnRowBytes + (((2 * mt + ((lane >> 3) & 1)) ^ (t & 7)) << 4));
+    mma_bf16(x.o[mt], v[0], v[1], v[2], v[3], p[0], p[1]);
+    mma_bf16(x.o[mt], v[0], v[1], v[2], v[3], rest[0], rest[1]);
+  }
+}
+// O to shared memory, o[row][d], of the first `rows` rows; each row's l whole in its lanes.
+__device__ __forceinline__ void dn_eight_end(DnEight& x, float* o, int rows, int lane) {
+  const int gid = lane >> 2, tig = lane & 3;
+  x.l += __shfl_xor_sync(0xFFFFFFFFu, x.l, 1);
+  x.l += __shfl_xor_sync(0xFFFFFFFFu, x.l, 2);
+  __syncwarp();  // o may lie where the last groups did
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = 2 * tig + (e & 1);
+      if (row < rows) o[row * kD + 16 * mt + 8 * (e >> 1) + gid] = x.o[mt][e];
+    }
 }
 
 // sd_dense_stream.cu: one query token per sequence.

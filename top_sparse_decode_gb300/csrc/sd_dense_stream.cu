@@ -23,20 +23,13 @@
 #include <atomic>
 
 #include "sd_dense.cuh"
-#include "sd_dense_plan.cuh"
-#include "sd_mma.cuh"
 
 namespace sd {
 namespace {
 
-constexpr int kSwGrp = 16;     // tokens per group
-constexpr int kSwWarps = 4;    // warps per CTA
-constexpr int kSwThreads = 32 * kSwWarps;
+constexpr int kSwThreads = 32 * kSwCtaWarps;
 constexpr int kSwStages = 3;
-constexpr uint32_t kSwRow = kD * 2;
-constexpr uint32_t kSwHalf = kSwGrp * kSwRow;  // a group's K: 4 KB; V behind it
-constexpr uint32_t kSwStage = 2 * kSwHalf;
-constexpr size_t kSwSmem = (size_t)kSwWarps * kSwStages * kSwStage;  // 96 KB
+constexpr size_t kSwSmem = (size_t)kSwCtaWarps * kSwStages * kDnStage;  // 96 KB
 constexpr float kSwSlack = 8.0f;
 
 struct SwArgs {
@@ -59,30 +52,6 @@ struct SwArgs {
   float sl2;
 };
 
-__device__ __forceinline__ uint32_t sw_su32(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ void sw_ldm(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void sw_ldmt(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void sw_cp16(uint32_t dst, const uint16_t* src, bool v) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
-               "r"(v ? 16 : 0)
-               : "memory");
-}
-template <int N>
-__device__ __forceinline__ void sw_cp_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint32_t sw_rank_addr(uint32_t addr, int rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
@@ -162,7 +131,7 @@ __device__ __forceinline__ void sw_finish(const SwArgs& a, SwHead x, int b, int 
 template <int G>
 __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(SwArgs a) {
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ float2 wml[kSwWarps][8];  // a warp's (m, l) of each head
+  __shared__ float2 wml[kSwCtaWarps][8];  // a warp's (m, l) of each head
   __shared__ __align__(16) float2 cml[8];    // the CTA's
   __shared__ __align__(16) float co[8][kD];  // and its O
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -180,32 +149,28 @@ __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(SwArgs a) {
     const int64_t p = a.w.at(b);
     r = dn_ranges(a.w, p, p);
   }
-  const int na = (int)((r.s1 + kSwGrp - 1) / kSwGrp);
-  const int all = na + (int)((r.w1 - r.w0 + kSwGrp - 1) / kSwGrp);
+  const int na = (int)((r.s1 + kSwGroup - 1) / kSwGroup);
+  const int all = na + (int)((r.w1 - r.w0 + kSwGroup - 1) / kSwGroup);
   const int g0 = (int)((int64_t)all * part / a.parts) + warp;
   const int g1 = (int)((int64_t)all * (part + 1) / a.parts);
 
-  const uint32_t mine = sw_su32(ring) + warp * kSwStages * kSwStage;
+  const uint32_t mine = dn_su32(ring) + warp * kSwStages * kDnStage;
   const int64_t base = row * a.ncap * kD;
-  const int lr = lane >> 4, lc = lane & 15;
+  auto group = [&](int i, int& have) {  // its first token
+    const int64_t c0 = i < na ? (int64_t)i * kSwGroup : r.w0 + (int64_t)(i - na) * kSwGroup;
+    have = (int)imin64(kSwGroup, (i < na ? r.s1 : r.w1) - c0);
+    return c0;
+  };
   auto fetch = [&](int i, int slot) {
     if (i < g1) {
-      const int64_t c0 = i < na ? (int64_t)i * kSwGrp : r.w0 + (int64_t)(i - na) * kSwGrp;
-      const int have = (int)imin64(kSwGrp, (i < na ? r.s1 : r.w1) - c0);
-      const int64_t at = base + c0 * kD + 8 * lc;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int t = 2 * k + lr;
-        const uint32_t dst = mine + slot * kSwStage + t * kSwRow + ((lc ^ (t & 7)) << 4);
-        const int64_t src = at + (t < have ? t : 0) * kD;
-        sw_cp16(dst, a.K + src, t < have);
-        sw_cp16(dst + kSwHalf, a.V + src, t < have);
-      }
+      int have;
+      const int64_t c0 = group(i, have);
+      dn_fetch(mine + slot * kDnStage, a.K, a.V, base + c0 * kD, have, lane);
     }
-    asm volatile("cp.async.commit_group;\n" ::: "memory");
+    dn_cp_commit();
   };
 #pragma unroll
-  for (int s = 0; s < kSwStages - 1; ++s) fetch(g0 + s * kSwWarps, s);
+  for (int s = 0; s < kSwStages - 1; ++s) fetch(g0 + s * kSwCtaWarps, s);
 
   uint32_t qa[8][2];
   {
@@ -217,108 +182,38 @@ __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(SwArgs a) {
       qa[kk][1] = real ? q[8 * kk + 4 + tig] : 0u;
     }
   }
-  float o[8][4];
-#pragma unroll
-  for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.0f;
-  float m = -INFINITY, l = 0.0f;
-
+  DnEight x;
+  dn_eight_begin(x);
   int slot = 0;
-  for (int i = g0; i < g1; i += kSwWarps) {
+  for (int i = g0; i < g1; i += kSwCtaWarps) {
     __syncwarp();  // the slot filled next is read by all
-    fetch(i + (kSwStages - 1) * kSwWarps, slot == 0 ? kSwStages - 1 : slot - 1);
-    sw_cp_wait<kSwStages - 1>();
+    fetch(i + (kSwStages - 1) * kSwCtaWarps, slot == 0 ? kSwStages - 1 : slot - 1);
+    dn_cp_wait<kSwStages - 1>();
     __syncwarp();
-    const uint32_t at = mine + slot * kSwStage;
+    int have;
+    group(i, have);
+    dn_eight_step(x, qa, mine + slot * kDnStage, have, real, a.sl2, kSwSlack, lane);
     slot = slot == kSwStages - 1 ? 0 : slot + 1;
-    const int64_t c0 = i < na ? (int64_t)i * kSwGrp : r.w0 + (int64_t)(i - na) * kSwGrp;
-    const int have = (int)imin64(kSwGrp, (i < na ? r.s1 : r.w1) - c0);
-    float sc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int t = 8 * n + (lane & 7);
-#pragma unroll
-      for (int kp = 0; kp < 4; ++kp) {
-        uint32_t k[4];
-        sw_ldm(k, at + t * kSwRow + (((4 * kp + (lane >> 3)) ^ (t & 7)) << 4));
-        mma_bf16(sc[n], qa[2 * kp][0], 0u, qa[2 * kp][1], 0u, k[0], k[1]);
-        mma_bf16(sc[n], qa[2 * kp + 1][0], 0u, qa[2 * kp + 1][1], 0u, k[2], k[3]);
-      }
-    }
-    float x[2][2], top = -INFINITY;
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        x[n][e] = real && 8 * n + 2 * tig + e < have ? sc[n][e] * a.sl2 : -INFINITY;
-        top = fmaxf(top, x[n][e]);
-      }
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    const bool need = top > m + kSwSlack;
-    if (__any_sync(0xFFFFFFFFu, need)) {
-      const float f = need ? exp2f(m - top) : 1.0f;  // m = -inf: 0
-      // O^T's columns 2tig, 2tig + 1 are heads whose factors the lanes of S's rows hold
-      const float fa = __shfl_sync(0xFFFFFFFFu, f, 8 * tig);
-      const float fb = __shfl_sync(0xFFFFFFFFu, f, 8 * tig + 4);
-#pragma unroll
-      for (int mt = 0; mt < 8; ++mt) {
-        o[mt][0] *= fa;
-        o[mt][1] *= fb;
-        o[mt][2] *= fa;
-        o[mt][3] *= fb;
-      }
-      l *= f;
-      if (need) m = top;
-    }
-    const float mu = m == -INFINITY ? 0.0f : m;
-    // a weight as two bf16, its upper half and what that leaves: 16 bits of it.  Neither part
-    // is negative, and the second not 0 either, so that an infinity in V stays what it is.
-    uint32_t p[2], rest[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const float u = exp2f(x[n][0] - mu), v = exp2f(x[n][1] - mu);
-      l += u + v;
-      p[n] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x7632);
-      rest[n] = dn_pack(fmaxf(u - bf16_lo(p[n]), 0x1p-126f), fmaxf(v - bf16_hi(p[n]), 0x1p-126f));
-    }
-#pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
-      const int t = (lane & 7) + 8 * (lane >> 4);
-      uint32_t v[4];
-      sw_ldmt(v, at + kSwHalf + t * kSwRow + (((2 * mt + ((lane >> 3) & 1)) ^ (t & 7)) << 4));
-      mma_bf16(o[mt], v[0], v[1], v[2], v[3], p[0], p[1]);
-      mma_bf16(o[mt], v[0], v[1], v[2], v[3], rest[0], rest[1]);
-    }
   }
-  sw_cp_wait<0>();
+  dn_cp_wait<0>();
   // behind a prefix's kernel every CTA waits for it, also where a later kernel joins the
   // parts: that one waits for this kernel only
   if (a.pre) dn_wait_prior();
 
   // the warp's (m, l, O) into its own part of the ring
-  l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-  l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-  if (tig == 0) wml[warp][gid] = make_float2(m, l);
-  __syncwarp();
-  float* wo = reinterpret_cast<float*>(ring + warp * kSwStages * kSwStage);
-#pragma unroll
-  for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int head = 2 * tig + (e & 1);
-      if (head < G) wo[head * kD + 16 * mt + 8 * (e >> 1) + gid] = o[mt][e];
-    }
+  dn_eight_end(x, reinterpret_cast<float*>(ring + warp * kSwStages * kDnStage), G, lane);
+  if (tig == 0) wml[warp][gid] = make_float2(x.m, x.l);
   __syncthreads();
   const bool joined = a.parts > 1 && !a.cut;
   const float* all_o = reinterpret_cast<const float*>(ring);
-  constexpr int kStep = kSwStages * kSwStage / sizeof(float);
-  for (int g = warp; g < G; g += kSwWarps) {  // a warp per head
+  constexpr int kStep = kSwStages * kDnStage / sizeof(float);
+  for (int g = warp; g < G; g += kSwCtaWarps) {  // a warp per head
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kSwWarps; ++w) top = fmaxf(top, wml[w][g].x);
+    for (int w = 0; w < kSwCtaWarps; ++w) top = fmaxf(top, wml[w][g].x);
     SwHead x = sw_head(top);
 #pragma unroll
-    for (int w = 0; w < kSwWarps; ++w)
+    for (int w = 0; w < kSwCtaWarps; ++w)
       x.add(wml[w][g].x, wml[w][g].y,
             reinterpret_cast<const float4*>(all_o + w * kStep + g * kD)[lane], sw_ref(top));
     if (a.cut) {
@@ -335,8 +230,8 @@ __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(SwArgs a) {
   if (!joined) return;
   sw_cluster_sync();
   // each CTA of the row finishes its share of the heads
-  const uint32_t ml_at = sw_su32(cml), o_at = sw_su32(co);
-  for (int g = part + a.parts * warp; g < G; g += a.parts * kSwWarps) {
+  const uint32_t ml_at = dn_su32(cml), o_at = dn_su32(co);
+  for (int g = part + a.parts * warp; g < G; g += a.parts * kSwCtaWarps) {
     const float2 mine2 =
         lane < a.parts ? sw_ld_rank2(sw_rank_addr(ml_at + 8 * g, lane)) : make_float2(-INFINITY, 0.0f);
     float top = mine2.x;

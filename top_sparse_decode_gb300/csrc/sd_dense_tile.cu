@@ -37,7 +37,7 @@
 // row sees, behind the first tokens or a sequence's last row, come as zeros or are set to zero
 // in shared memory; and a row whose O comes out not finite, as from a weight of 0 times an
 // infinity that the row does not see and others of its tile do (0 x inf is not 0), is computed
-// again by itself, token by token.
+// again when the CTA's items are done (tl_again).
 //
 // What bounds it: the chain of a row tile, whose scores' product, two halves of softmax and
 // product with V follow each other; two row tiles in flight keep the tensor pipe busy for some
@@ -74,6 +74,7 @@ constexpr uint32_t kTlHalf = kTlTile / 2;       // 64 channels of it
 constexpr uint32_t kTlSpin = 1u << 22;          // try_wait rounds before a wait gives up
 constexpr float kTlMost = 16384.0f;             // half a tile's weights sum up to this at most,
 constexpr float kTlLeast = 0x1p-40f;            // and a row's so far to this at least, or m moves
+constexpr uint32_t kTlAgainItems = 1024;        // items with a bit of their own in `again`
 
 struct TlSmem {
   uint8_t q[2][kTlTile];
@@ -85,6 +86,7 @@ struct TlSmem {
   float2 ml[kDtRows];   // dual: the second group's (m, l)
   uint32_t tmem;
   int abort;
+  uint32_t again[kTlAgainItems / 32];  // items of this CTA with a row to compute again, by number
 };
 constexpr size_t kTlSmemBytes = sizeof(TlSmem) + 1024;  // the tiles start on 1 KB
 
@@ -396,31 +398,6 @@ __device__ __forceinline__ uint32_t tl_vpos(const TlArgs& a, const TlItem& x, in
 }
 __device__ __forceinline__ uint32_t tl_loads(const TlArgs& a, const TlItem& x) {
   return 2u * (a.dual ? x.t[0] + x.t[1] : x.t[0]);
-}
-
-// A row's own (m, l, O) from the cache, its warp together: the tokens of the part's tiles
-// that it sees.  For rows whose O is not finite.
-__device__ __noinline__ DnRow tl_row_again(const TlArgs& a, TlItem x, int64_t row, int lane) {
-  DnRow r;
-  const int64_t t = row >> a.lg;
-  const int g = (int)(row & (a.G - 1));
-  dn_row_begin(r, a.q + x.b * a.qs.seq + (int64_t)(x.h * a.G + g) * a.qs.head + t * a.qs.token,
-               a.sl2, lane);
-  const int64_t base = x.bh * a.ncap * kD, p = x.p0 + t;
-  for (int i = x.ta; i < x.tb; ++i) {
-    int64_t c0, end;
-    tl_tile(x, i, c0, end);
-    end = imin64(end, c0 + kDtKeys);
-    if (a.causal) {
-      end = imin64(end, p + 1);
-      const int64_t w = imax64(c0, p - a.w.window + 1);
-      const int64_t s = imin64(imin64(end, a.w.sink), w);  // first tokens before the window
-      dn_row_over(r, a.K + base, a.V + base, c0, s, lane);
-      c0 = imax64(c0, w);
-    }
-    dn_row_over(r, a.K + base, a.V + base, c0, end, lane);
-  }
-  return r;
 }
 
 // Bits [0, n) of a word.
@@ -747,23 +724,13 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
         a.lse[((int64_t)x.b * a.Hkv * a.G + head) * a.w.m + t] =
             l == 0.0f ? -INFINITY : (m + log2f(l)) * kDnLn2;
     }
-    // a row whose O is not finite may owe that to tokens that it does not see: again by itself
+    // a row whose O is not finite may owe that to tokens that it does not see (tl_again)
     float odd0, odd1;
     tl_of(odd, odd0, odd1);
-    for (uint32_t rows = __ballot_sync(0xFFFFFFFFu, mine && !(odd0 == 0.0f && odd1 == 0.0f)); rows;
-         rows &= rows - 1) {
-      const int64_t rw = x.r0 + (local - lane) + __ffs((int)rows) - 1;
-      const DnRow r = tl_row_again(a, x, rw, lane);
-      const int hd = x.h * a.G + (int)(rw & (a.G - 1));
-      const int64_t tt = rw >> a.lg;
-      if (final) {
-        dn_row_end(r, a.out + x.b * a.os.seq + hd * a.os.head + tt * a.os.token,
-                   a.lse ? a.lse + ((int64_t)x.b * a.Hkv * a.G + hd) * a.w.m + tt : nullptr, lane);
-      } else {
-        const int64_t pr = (x.bh * a.w.m * a.G + rw) * a.splits + x.split;
-        reinterpret_cast<float4*>(a.part_o + pr * kD)[lane] = r.o;
-        if (lane == 0) a.part_ml[pr] = make_float2(r.m, r.l);
-      }
+    if (__builtin_expect(__any_sync(0xFFFFFFFFu, mine && !(odd0 == 0.0f && odd1 == 0.0f)), 0) &&
+        lane == 0) {
+      const uint32_t nth = id / gridDim.x;
+      atomicOr(&sm.again[nth % kTlAgainItems / 32], 1u << (nth % 32));
     }
     tl_fence_before();
     __syncwarp();
@@ -963,6 +930,188 @@ __device__ __forceinline__ void tl_queries(TlSmem& sm, const TlArgs& a) {
   }
 }
 
+// ---- rows that are not finite ------------------------------------------------------------
+// Such rows of the CTA's items once more, when all of its items are done: nothing waits for
+// this but the end of the kernel, so that no bounded wait can run out over it.  A warp takes
+// eight rows: groups of 16 tokens that all of them see by tensor-core products, where no
+// weight of 0 meets a value that its row does not see; then, row by row, what is left (the
+// edges of the mask), token by token.  All rows of 32 heads x 32,768 tokens, causal: 86 ms
+// (6.0 where they are finite), under a window of 4,096 and 128 first tokens 28 ms (1.55).
+// Not inlined: in the kernel's own code it cost the rows that are finite 1 to 7 %.
+constexpr int kTlCuts = 16, kTlEight = 8, kTlAgainStages = 3;
+struct TlAgain {  // a warp's place, 28 KB of the tiles'
+  uint8_t ring[kTlAgainStages][kDnStage];
+  union {
+    uint32_t q[16][32];       // the rows' queries as the products take them
+    float o[kTlEight][kD];
+  };
+};
+static_assert(8 * sizeof(TlAgain) <= (2 + kTlStages) * kTlTile, "eight warps share the tiles");
+
+struct TlWalk {  // the item's tiles, and what eight rows see of them (tokens are below 2^31)
+  int s1, w0, w1, na, tb;
+  int causal, sink;
+  int hi0, hi1;    // no row sees a token behind hi1, all see those up to hi0 by their position
+  int lo0, lo1;    // ... the window: no row up to lo0, all behind lo1
+  int i, g;        // the walk's place: group g of tile i
+  int t0, end;     // tile i
+  bool whole;      // all rows see all of it
+  int cuts;        // tiles passed that some rows see some of
+
+  __device__ __forceinline__ void tile(int at, int& c0, int& c1) const {
+    c0 = at < na ? at * kDtKeys : w0 + (at - na) * kDtKeys;
+    c1 = min(at < na ? s1 : w1, c0 + kDtKeys);
+  }
+  // all rows see all of [c0, c1)
+  __device__ __forceinline__ bool all(int c0, int c1) const {
+    return !causal || (c1 - 1 <= hi0 && (c1 <= sink || c0 > lo1));
+  }
+  __device__ __forceinline__ bool none(int c0, int c1) const {
+    return causal && (c0 > hi1 || (c1 - 1 <= lo0 && c0 >= sink));
+  }
+  // The next group that all see; false behind the last.
+  __device__ __forceinline__ bool next(int& c0, int* cut) {
+    for (; i < tb; ++i, g = 0) {
+      if (g == 0) {
+        tile(i, t0, end);
+        whole = end - t0 == kDtKeys && all(t0, end);
+        // (at most six: what eight rows see of the first tokens and of the window ends in two
+        // tiles each, and the two ranges of the item end in one)
+        if (!whole && !none(t0, end) && cuts < kTlCuts) cut[cuts++] = i;
+      }
+      for (; g < kDtKeys / kSwGroup; ++g) {
+        c0 = t0 + g * kSwGroup;
+        if (whole || (c0 + kSwGroup <= end && all(c0, c0 + kSwGroup))) {
+          ++g;
+          return true;
+        }
+      }
+    }
+    return false;
+  }
+  // What the row at p sees of the rest of tile `at`.
+  __device__ __forceinline__ void rest(DnRow& r, int at, int64_t p, int64_t window,
+                                       const uint16_t* K, const uint16_t* V, int lane) const {
+    int c0, t1;
+    tile(at, c0, t1);
+#pragma unroll 1
+    for (; c0 < t1; c0 += kSwGroup) {
+      const int c1 = min(t1, c0 + kSwGroup);
+      if (c1 - c0 == kSwGroup && all(c0, c1)) continue;
+#pragma unroll 1
+      for (int c = c0; c < c1; ++c)
+        if (!causal || (c <= p && (c < sink || c > p - window)))
+          dn_row_over(r, K, V, c, c + 1, lane);
+    }
+  }
+};
+
+__device__ __noinline__ void tl_again(TlSmem* sm, const TlArgs* args) {
+  const TlArgs& a = *args;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  TlAgain& at = reinterpret_cast<TlAgain*>(sm->q[0])[warp];
+  const uint32_t ring = dn_su32(at.ring);
+  const bool final = a.splits == 1 && !a.parts_only;
+  int cut[kTlCuts];
+  uint32_t nth = 0;
+  for (uint32_t id = blockIdx.x; id < a.items; id += gridDim.x, ++nth) {
+    if (!(sm->again[nth % kTlAgainItems / 32] >> (nth % 32) & 1u)) continue;
+    const TlItem x = tl_item(a, id);
+    const uint16_t* K = a.K + x.bh * a.ncap * kD;
+    const uint16_t* V = a.V + x.bh * a.ncap * kD;
+    auto head = [&](int64_t row) { return x.h * a.G + (int)(row & (a.G - 1)); };
+    auto part = [&](int64_t row) { return (x.bh * a.w.m * a.G + row) * a.splits + x.split; };
+    auto result = [&](int64_t row) {
+      return a.out + x.b * a.os.seq + head(row) * a.os.head + (row >> a.lg) * a.os.token;
+    };
+    auto query = [&](int64_t row) {
+      return a.q + x.b * a.qs.seq + (int64_t)head(row) * a.qs.head + (row >> a.lg) * a.qs.token;
+    };
+#pragma unroll 1
+    for (int r0 = kTlEight * warp; r0 < x.rows; r0 += kTlEight * 8) {
+      const int rows = min(kTlEight, x.rows - r0);
+      const int64_t row0 = x.r0 + r0;
+      uint32_t odd = 0;  // rows whose result is not finite
+#pragma unroll 1
+      for (int r = 0; r < rows; ++r) {
+        const float4 y =
+            final ? dn_ld4(result(row0 + r) + 4 * lane)
+                  : reinterpret_cast<const float4*>(a.part_o + part(row0 + r) * kD)[lane];
+        if (__any_sync(0xFFFFFFFFu,
+                       !(isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w))))
+          odd |= 1u << r;
+      }
+      if (!odd) continue;
+      const bool real = (lane >> 2) < rows;
+      {
+        const uint32_t* q =
+            reinterpret_cast<const uint32_t*>(query(row0 + (real ? lane >> 2 : 0)));
+        __syncwarp();  // the rows before are written
+        for (int k = 0; k < 16; ++k) at.q[k][lane] = real ? q[4 * k + (lane & 3)] : 0u;
+      }
+      auto token = [&](int64_t i) { return (int)imax64(-1, imin64(a.w.n, i)); };
+      const int64_t pa = x.p0 + (row0 >> a.lg), pb = x.p0 + ((row0 + rows - 1) >> a.lg);
+      TlWalk walk;
+      walk.s1 = (int)x.r.s1, walk.w0 = (int)x.r.w0, walk.w1 = (int)x.r.w1;
+      walk.na = x.na, walk.tb = x.tb, walk.causal = a.causal;
+      walk.sink = token(a.w.sink), walk.hi0 = token(pa), walk.hi1 = token(pb);
+      walk.lo0 = token(pa - a.w.window), walk.lo1 = token(pb - a.w.window);
+      walk.i = x.ta, walk.g = walk.cuts = 0;
+      DnEight y;
+      dn_eight_begin(y);
+      const float sl2 = a.sl2;
+      int ahead = 0, slot = 0, c0;
+#pragma unroll 1
+      for (int k = 0;; ++k) {  // group k copied, group k - 2 worked on
+        __syncwarp();          // what the slot held is read by all
+        if (walk.next(c0, cut)) {
+          dn_fetch(ring + slot * kDnStage, K, V, (int64_t)c0 * kD, kSwGroup, lane);
+          ++ahead;
+        }
+        dn_cp_commit();
+        slot = slot == kTlAgainStages - 1 ? 0 : slot + 1;
+        if (k < kTlAgainStages - 1) continue;
+        if (!ahead) break;
+        dn_cp_wait<kTlAgainStages - 1>();
+        __syncwarp();
+        uint32_t qa[8][2];
+#pragma unroll
+        for (int kk = 0; kk < 16; ++kk) qa[kk >> 1][kk & 1] = at.q[kk][lane];
+        dn_eight_step(y, qa, ring + slot * kDnStage, kSwGroup, real, sl2, 0.0f, lane);
+        --ahead;
+      }
+      dn_cp_wait<0>();
+      dn_eight_end(y, at.o[0], rows, lane);
+      __syncwarp();
+#pragma unroll 1
+      for (int r = 0; r < rows; ++r) {
+        const int64_t row = row0 + r, t = row >> a.lg;
+        DnRow z;
+        z.m = __shfl_sync(0xFFFFFFFFu, y.m, 4 * r);
+        z.l = __shfl_sync(0xFFFFFFFFu, y.l, 4 * r);
+        if (!(odd >> r & 1u)) continue;
+        z.o = reinterpret_cast<const float4*>(at.o[r])[lane];
+        dn_row_begin(z, query(row), sl2, lane);
+        for (int c = 0; c < walk.cuts; ++c)
+          walk.rest(z, cut[c], x.p0 + t, a.w.window, K, V, lane);
+        if (final) {
+          float* lse =
+              a.lse ? a.lse + ((int64_t)x.b * a.Hkv * a.G + head(row)) * a.w.m + t : nullptr;
+          dn_row_end(z, result(row), lse, lane);
+        } else {
+          reinterpret_cast<float4*>(a.part_o + part(row) * kD)[lane] = z.o;
+          if (lane == 0) a.part_ml[part(row)] = make_float2(z.m, z.l);
+        }
+      }
+    }
+  }
+}
+
+// All warps of the CTA, from either side.
+__device__ __forceinline__ void tl_meet() {
+  asm volatile("barrier.sync 1, %0;\n" ::"n"(kTlThreads) : "memory");
+}
+
 __global__ void __launch_bounds__(kTlThreads, 1)
     dense_tile_kernel(const __grid_constant__ TlMaps maps, const __grid_constant__ TlArgs a) {
   extern __shared__ uint8_t raw[];
@@ -991,6 +1140,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     tl_init(&sm.mlfull, 4);
     tl_init(&sm.drain, 1);
     sm.abort = 0;
+    for (int i = 0; i < (int)kTlAgainItems / 32; ++i) sm.again[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     const TlItem x = tl_item(a, blockIdx.x);
     tl_load_steps(sm, ld, a, maps, x, 0, tl_early(a, x));
@@ -1011,6 +1161,12 @@ __global__ void __launch_bounds__(kTlThreads, 1)
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
     tl_softmax(sm, a, warp >> 2, tmem);
+    tl_fence_before();
+    tl_meet();
+    static_assert(kTlAgainItems == 32 * 32, "a word a lane");
+    const uint32_t some = sm.again[threadIdx.x & 31];
+    if (__builtin_expect(!sm.abort && __any_sync(0xFFFFFFFFu, some != 0), 0))
+      tl_again(&sm, &a);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
     if (warp == 8) {
@@ -1025,12 +1181,12 @@ __global__ void __launch_bounds__(kTlThreads, 1)
       tl_queries(sm, a);
     }
     __syncwarp();
+    tl_fence_before();
+    tl_meet();
+    tl_fence_after();
+    if (warp == 8)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
   }
-  tl_fence_before();
-  __syncthreads();
-  tl_fence_after();
-  if (warp == 8)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
 }
 
 // ---- joining parts -----------------------------------------------------------------------
