@@ -434,6 +434,39 @@ def test_window_scales(sd, scale):
     check_window(case, run_window(sd, *case, scale=scale), scale=scale)
 
 
+@pytest.mark.parametrize("scale", [1e3, 1e6, 3e8, 1e30])
+@pytest.mark.parametrize("low", [-100, -300, 40])
+def test_window_wide_scores(sd, scale, low):
+    """Whole numbers as scores, times a scale that sets them far apart: a row's result is the
+    mean of the values of its largest score, however far that is from 0.  (The scores are
+    exact; the scale, log2 e, ln 2 and the products with them are rounded, 2^-24 each.
+    Weights of equal scores are equal, of others below 2^-126 from a scale of 1e3 on.)"""
+    for m, n, window in ((1, 900, 900), (20, 900, 700), (150, 400, 400), (500, 500, 130)):
+        case = (1, 2, 4, n, n, m, n - m, None, None, window, 3)
+
+        def spoil(q, K, V):
+            g = torch.Generator(device="cuda").manual_seed(m)
+            q[..., 1:] = 0.0
+            q[..., 0] = 1.0
+            K[..., 0] = torch.randint(low, low + 201, K.shape[:3], device="cuda", generator=g,
+                                      dtype=torch.int32).bfloat16()
+            K[:, :, n // 2, 0] = K[:, :, n // 2 - 1, 0]
+        q, K, V, out, lse = run_window(sd, *case, scale=scale, prep=spoil)
+        see = visible(torch.arange(n - m, n, device="cuda"), n, window, 3, "cuda")
+        for h in range(2):
+            z = K[0, h, :, 0].double().expand(m, -1).masked_fill(~see, -math.inf)
+            top = z.amax(-1, keepdim=True)
+            w = (z == top).double()
+            count = w.sum(-1, keepdim=True)
+            ref, size = w @ V[0, h].double() / count, w @ V[0, h].double().abs() / count
+            check(out[0, 4 * h:4 * h + 4], ref.expand(4, -1, -1),
+                  (2.0 ** -8 * (ref.abs() + size) + 2.0 ** -20 * size + 1e-30).expand(4, -1, -1),
+                  "out")
+            want = (top * scale + torch.log(count))[:, 0]
+            check(lse[0, 4 * h:4 * h + 4], want.expand(4, -1),
+                  (8 * 2.0 ** -24 * want.abs() + 2.0 ** -18).expand(4, -1), "lse")
+
+
 def test_window_repeats_and_graph(sd):
     """The same bits again, from another workspace's contents and from a replayed graph."""
     for case in ((2, 2, 4, 3000, 3000, 1, 2999, None, None, 2900, 0),

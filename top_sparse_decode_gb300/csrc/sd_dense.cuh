@@ -68,7 +68,7 @@ __device__ __forceinline__ DnRanges dn_ranges(const DnWindow& w, int64_t p0, int
 }
 
 // One query row's softmax, a warp over a range of tokens: lane l holds channels 4l .. 4l + 3
-// of q (times scale log2 e) and of the sum.  m in log2 units.
+// of q and of the sum.  m in log2 units.
 struct DnRow {
   float4 q, o;
   float m, l;
@@ -77,17 +77,14 @@ __device__ __forceinline__ float4 dn_ld4(const uint16_t* p) {
   const uint2 x = *reinterpret_cast<const uint2*>(p);
   return make_float4(bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y));
 }
-__device__ __forceinline__ void dn_row_begin(DnRow& r, const uint16_t* q, float sl2, int lane) {
-  const float4 x = dn_ld4(q + 4 * lane);
-  r.q = make_float4(x.x * sl2, x.y * sl2, x.z * sl2, x.w * sl2);
-}
 __device__ __forceinline__ void dn_row_over(DnRow& r, const uint16_t* K, const uint16_t* V,
-                                            int64_t i0, int64_t i1, int lane) {
+                                            int64_t i0, int64_t i1, float sl2, int lane) {
   for (int64_t i = i0; i < i1; ++i) {
     const float4 k = dn_ld4(K + i * kD + 4 * lane), v = dn_ld4(V + i * kD + 4 * lane);
     float z = fmaf(r.q.x, k.x, fmaf(r.q.y, k.y, fmaf(r.q.z, k.z, r.q.w * k.w)));
 #pragma unroll
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+    z *= sl2;
     const float top = fmaxf(r.m, z), mu = top == -INFINITY ? 0.0f : top;
     const float f = exp2f(r.m - mu), p = exp2f(z - mu);
     r.m = top;

@@ -74,6 +74,7 @@ constexpr uint32_t kTlHalf = kTlTile / 2;       // 64 channels of it
 constexpr uint32_t kTlSpin = 1u << 22;          // try_wait rounds before a wait gives up
 constexpr float kTlMost = 16384.0f;             // half a tile's weights sum up to this at most,
 constexpr float kTlLeast = 0x1p-40f;            // and a row's so far to this at least, or m moves
+constexpr float kTlWide = 0x1p26f;
 constexpr uint32_t kTlAgainItems = 1024;        // items with a bit of their own in `again`
 
 struct TlSmem {
@@ -441,7 +442,10 @@ __device__ __forceinline__ bool tl_off(float sum, float l) {
 // The weights of half a tile for a warp whose rows see a part of it, or with a row whose m
 // does not fit: where the half's largest score is over 8 above m, or 30 below while the row
 // has no weight yet, m becomes the whole number above it, and l and O move by a power of two,
-// exactly.  with_o: O holds products, done when `b` completes its phase.
+// exactly.  From 2^26 on a score's product with the scale, which the weights take before it is
+// rounded, may be far from such an m: the row becomes NaN, and is computed again with scores
+// that are rounded first (tl_again).  with_o: O holds products, done when `b` completes its
+// phase.
 struct TlFit {
   float m, l;
   bool ok;
@@ -488,7 +492,7 @@ __device__ __noinline__ TlFit tl_fit(int* abort, unsigned long long* b, uint32_t
   float f = 1.0f;
   if (top > m + 8.0f || (l == 0.0f && top < m - 30.0f && top != -INFINITY)) {
     f = l == 0.0f || m - top < -126.0f ? 0.0f : exp2f(m - top);
-    m = top;
+    m = fabsf(top) < kTlWide ? top : NAN;
     l *= f;
   }
   if (with_o && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
@@ -991,7 +995,8 @@ struct TlWalk {  // the item's tiles, and what eight rows see of them (tokens ar
   }
   // What the row at p sees of the rest of tile `at`.
   __device__ __forceinline__ void rest(DnRow& r, int at, int64_t p, int64_t window,
-                                       const uint16_t* K, const uint16_t* V, int lane) const {
+                                       const uint16_t* K, const uint16_t* V, float sl2,
+                                       int lane) const {
     int c0, t1;
     tile(at, c0, t1);
 #pragma unroll 1
@@ -1001,7 +1006,7 @@ struct TlWalk {  // the item's tiles, and what eight rows see of them (tokens ar
 #pragma unroll 1
       for (int c = c0; c < c1; ++c)
         if (!causal || (c <= p && (c < sink || c > p - window)))
-          dn_row_over(r, K, V, c, c + 1, lane);
+          dn_row_over(r, K, V, c, c + 1, sl2, lane);
     }
   }
 };
@@ -1091,9 +1096,9 @@ __device__ __noinline__ void tl_again(TlSmem* sm, const TlArgs* args) {
         z.l = __shfl_sync(0xFFFFFFFFu, y.l, 4 * r);
         if (!(odd >> r & 1u)) continue;
         z.o = reinterpret_cast<const float4*>(at.o[r])[lane];
-        dn_row_begin(z, query(row), sl2, lane);
+        z.q = dn_ld4(query(row) + 4 * lane);
         for (int c = 0; c < walk.cuts; ++c)
-          walk.rest(z, cut[c], x.p0 + t, a.w.window, K, V, lane);
+          walk.rest(z, cut[c], x.p0 + t, a.w.window, K, V, sl2, lane);
         if (final) {
           float* lse =
               a.lse ? a.lse + ((int64_t)x.b * a.Hkv * a.G + head(row)) * a.w.m + t : nullptr;
