@@ -434,6 +434,18 @@ def test_window_scales(sd, scale):
     check_window(case, run_window(sd, *case, scale=scale), scale=scale)
 
 
+@pytest.mark.parametrize("scale", [0.0, 2e-38, 1e-30])
+def test_window_small_scales(sd, scale):
+    """Scales far below 1 with products as far above it (0: every visible token counts alike)."""
+    for m in (1, 20, 300):
+        case = (1, 1, 4, 600, 600, m, 600 - m, None, None, 500, 9)
+
+        def spoil(q, K, V):
+            q[..., 0] = 3e18
+            K[..., 0] *= 1.5e19 if scale < 1e-35 else 3e11
+        check_window(case, run_window(sd, *case, scale=scale, prep=spoil), scale=scale)
+
+
 @pytest.mark.parametrize("scale", [1e3, 1e6, 3e8, 1e30])
 @pytest.mark.parametrize("low", [-100, -300, 40])
 def test_window_wide_scores(sd, scale, low):

@@ -1305,9 +1305,9 @@ int tl_launch(TlArgs& a, int64_t rows_bh, const DtPlan& p, cudaStream_t st) {
   if (firsts % kDtKeys)
     if (int rc = tl_map(&maps.vs, a.V, firsts, a.ncap, rows_bh)) return rc;
   a.lg = a.G == 8 ? 3 : a.G == 4 ? 2 : a.G - 1;
-  // scale 0: every score 0, as a product with a factor this small gives (0 would turn the
+  // scale 0: every score 0, as near as a product with the least factor comes (0 would turn the
   // -inf of unseen tokens into NaN)
-  a.sl2 = fmaxf(a.sl2, 1e-36f);
+  if (a.sl2 == 0.0f) a.sl2 = 1e-45f;
   a.dual = p.dual;
   a.splits = p.splits;
   a.per = p.per;
