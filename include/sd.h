@@ -565,8 +565,9 @@ int sd_qk_norm_rope(const sd_shape* shape, const sd_rope* rope, const void* q,
  *   overlap.
  *   Errors: SD_ERR_INVALID_ARG for a NULL or misaligned pointer (16 bytes; 4 for lse, pos,
  *   length), bad strides, m outside [0, 2^31), first outside [0, n], window < 1, sink < 0,
- *   a scale that is negative or not finite; SD_ERR_UNSUPPORTED for n >= 2^31 or m * hq *
- *   B >= 2^31 (shape); SD_ERR_WORKSPACE; SD_ERR_CUDA.  m = 0 does nothing.
+ *   a scale outside [0, 2.3e38] (scale log2 e is finite, too); SD_ERR_UNSUPPORTED for
+ *   n >= 2^31 or m * hq * B >= 2^31 (shape); SD_ERR_WORKSPACE; SD_ERR_CUDA.  m = 0 does
+ *   nothing.
  */
 size_t sd_window_attend_workspace_size(const sd_shape* shape, int64_t m, int64_t window,
                                        int64_t sink);

@@ -95,6 +95,16 @@ def test_window_sizes(sd):
     assert sd.sd_window_attend_workspace_size(big, 1, 0) == 0
 
 
+@pytest.mark.parametrize("scale", [2.4e38, 3.3e38])
+def test_scales_without_a_finite_log2_factor(sd, scale):
+    # (a workspace of 0 bytes: a call that passed the scale would be refused for that)
+    big = dict(shp=sd.make_shape(1, 4, 1, 100000), m=100, window=100000, ws_bytes=0)
+    assert window_call(sd, scale=2.2e38, **big) == sd.SD_ERR_WORKSPACE
+    assert window_call(sd, scale=scale, **big) == sd.SD_ERR_INVALID_ARG
+    assert prefix_call(sd, scale=scale, ws_bytes=0) == sd.SD_ERR_INVALID_ARG
+    assert prefix_call(sd, scale=2.2e38, ws_bytes=0) == sd.SD_ERR_WORKSPACE
+
+
 def prefix_call(sd, shp=None, q=P, Kp=P, Vp=P, p=50, pcap=0, K=P, V=P, end=P, scale=0.1, out=P,
                 lse=P, ws=P, ws_bytes=1 << 40):
     shp = shp or shape(sd)

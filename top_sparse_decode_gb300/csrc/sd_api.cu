@@ -708,8 +708,9 @@ int sd_qk_norm_rope(const sd_shape* shape, const sd_rope* rope, const void* q,
 // What the window and prefix calls share: scale, workspace.
 static int check_dense(const char* fn, float scale, const float* lse, void* ws, size_t ws_bytes,
                        size_t need) {
-  if (!(scale >= 0.0f) || scale > 3.4e38f)
-    return fail(SD_ERR_INVALID_ARG, "%s: scale must be finite and not negative", fn);
+  // (the kernels work in log2 units: scale log2 e has to be finite, too)
+  if (!(scale >= 0.0f) || scale > 2.3e38f)
+    return fail(SD_ERR_INVALID_ARG, "%s: scale must be in [0, 2.3e38]", fn);
   if (!aligned4(lse)) return fail(SD_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", fn);
   if (need && (!ws || ws_bytes < need))
     return fail(SD_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
