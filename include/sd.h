@@ -775,12 +775,14 @@ int sd_device_status(void* stream);
 int sd_set_fallback_paths(int on);
 
 /*
- * sd_debug_set_device_error -- testing: sets this GPU's libsd error word as a
- * kernel whose bounded wait ran out would (ordered on `stream`, then waits for
- * it), so that sd_device_status's report can be tested without making a wait
- * run out.
+ * sd_debug_set_device_error, sd_debug_set_tile_error -- testing: set this GPU's
+ * libsd error words, of the bit-plane scans and of sd_window_attend and
+ * sd_prefix_attend, as a kernel whose bounded wait ran out would (ordered on
+ * `stream`, then wait for it), so that sd_device_status's report can be tested
+ * without making a wait run out.
  */
 int sd_debug_set_device_error(void* stream);
+int sd_debug_set_tile_error(void* stream);
 
 /*
  * sd_copy -- copy `bytes` bytes from src to dst with a kernel on `stream`, where
@@ -809,8 +811,8 @@ const char* sd_last_error(void);
  * sd_device_status, sd_set_fallback_paths and sd_debug_set_device_error; 103 adds
  * SD_PLAN_SPLIT, sd_shard_candidates, sd_topk_merge, sd_shard_select and
  * sd_attend_combine; 104 adds sd_copy.  The sd_kv4_* entry points came later under
- * the same number, and so did sd_qk_norm_rope, sd_window_attend and sd_prefix_attend
- * (nothing else changed): look them up by name. */
+ * the same number, and so did sd_qk_norm_rope, sd_window_attend, sd_prefix_attend and
+ * sd_debug_set_tile_error (nothing else changed): look them up by name. */
 int sd_version(void);
 
 /*

@@ -33,6 +33,28 @@ def test_status_reports_once_and_clears(sd):
     sd.sd_device_status()  # cleared by the report
 
 
+@pytest.mark.parametrize("scan", [False, True])
+def test_status_of_the_tile_attention(sd, scan):
+    """The window and prefix attention's word: reported by its own message, alone or with the
+    scans', and cleared with it; the calls behind it run."""
+    sd.sd_device_status()
+    stream = torch.cuda.Stream()
+    sd.sd_debug_set_tile_error(stream)
+    if scan:
+        sd.sd_debug_set_device_error()
+    with pytest.raises(sd.SdError) as e:
+        sd.sd_device_status()
+    assert e.value.code == sd.SD_ERR_TIMEOUT
+    assert "window or prefix attention" in str(e.value) and "incomplete" in str(e.value)
+    assert ("so did a bit-plane scan" in str(e.value)) == scan
+    sd.sd_device_status()  # both cleared
+    q, K, V = (torch.ones((1, 2, 70, 128), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    out = torch.zeros_like(q)
+    sd.sd_window_attend(sd.make_shape(1, 2, 2, 70), q, K, V, 70, 70, 0, 0.0, out)
+    sd.sd_device_status()
+    assert (out == 1).all()
+
+
 def test_status_clean_after_scans(sd):
     cfg = synth.config(2, B=1, n=8192)
     inp = synth.make_inputs(cfg, with_v=False)

@@ -32,7 +32,8 @@ __all__ = [
     "sd_gather_attend_noalloc", "sd_offload_gather", "Resident", "sd_delta_select",
     "sd_resident_gather",
     "sd_event_wait", "sd_last_error", "sd_version", "sd_launch_count", "sd_device_status",
-    "sd_set_fallback_paths", "sd_debug_set_device_error", "sd_shard_candidates",
+    "sd_set_fallback_paths", "sd_debug_set_device_error", "sd_debug_set_tile_error",
+    "sd_shard_candidates",
     "sd_topk_merge", "sd_shard_select", "sd_attend_combine",
     "sd_score_topk_workspace_size", "sd_score_topk", "sd_plan_score", "sd_topk_wmax", "sd_copy",
     "sd_select_attend_workspace_size", "sd_select_attend", "sd_hamming_topk_workspace_size",
@@ -564,8 +565,13 @@ def sd_set_fallback_paths(on: bool) -> bool:
 
 
 def sd_debug_set_device_error(stream=None) -> None:
-    """Testing: raise the device error word that sd_device_status reports."""
+    """Testing: raise the scans' device error word, which sd_device_status reports."""
     _check(lib().sd_debug_set_device_error(_stream(stream)), "sd_debug_set_device_error")
+
+
+def sd_debug_set_tile_error(stream=None) -> None:
+    """Testing: raise the window and prefix attention's device error word."""
+    _check(lib().sd_debug_set_tile_error(_stream(stream)), "sd_debug_set_tile_error")
 
 
 def sd_copy(dst, src, nbytes: Optional[int] = None, stream=None) -> None:

@@ -110,6 +110,7 @@ SIGNATURES = {
     "sd_device_status": (_i, [_p]),
     "sd_set_fallback_paths": (_i, [_i]),
     "sd_debug_set_device_error": (_i, [_p]),
+    "sd_debug_set_tile_error": (_i, [_p]),
     "sd_event_wait": (_i, [_p, _i64]),
     "sd_copy": (_i, [_p, _p, _sz, _p]),
     "sd_last_error": (ctypes.c_char_p, []),

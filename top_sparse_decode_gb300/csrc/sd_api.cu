@@ -975,6 +975,8 @@ int sd_debug_set_device_error(void* stream) {
   return scan_error_set(1u, (cudaStream_t)stream);
 }
 
+int sd_debug_set_tile_error(void* stream) { return tile_error_set(1u, (cudaStream_t)stream); }
+
 namespace {
 // 16-byte words, grid-strided; several loads in flight per thread.
 __global__ void __launch_bounds__(256) copy16_kernel(uint4* __restrict__ dst,

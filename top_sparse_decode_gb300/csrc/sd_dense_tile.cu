@@ -1335,7 +1335,8 @@ constexpr size_t kTlPart = kD * sizeof(float) + sizeof(float2);
 
 }  // namespace
 
-// Sets the word as a kernel whose bounded wait ran out would have, reads and clears it.
+// Reads this GPU's word after the work on `st`, then clears it (both ordered on `st`; the host
+// waits for the stream).
 int tile_error_take(cudaStream_t st, unsigned* word) {
   *word = 0;
   unsigned zero = 0;
@@ -1348,6 +1349,15 @@ int tile_error_take(cudaStream_t st, unsigned* word) {
                                st) != cudaSuccess ||
        cudaStreamSynchronize(st) != cudaSuccess))
     return check_launch("device status: clear");
+  return SD_OK;
+}
+
+// Sets the word as a kernel whose bounded wait ran out would (for testing the report).
+int tile_error_set(unsigned word, cudaStream_t st) {
+  if (cudaMemcpyToSymbolAsync(g_tile_timeout, &word, sizeof(unsigned), 0, cudaMemcpyHostToDevice,
+                              st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return check_launch("device status: set");
   return SD_OK;
 }
 

@@ -62,6 +62,7 @@ int scan_error_take(cudaStream_t st, unsigned* word);
 int scan_error_set(unsigned word, cudaStream_t st);
 // The tile attention's (sd_dense_tile.cu).
 int tile_error_take(cudaStream_t st, unsigned* word);
+int tile_error_set(unsigned word, cudaStream_t st);
 // The current device's SM count (cached per device; 152 if it cannot be read).
 int device_sm_count();
 
