@@ -555,14 +555,15 @@ int sd_qk_norm_rope(const sd_shape* shape, const sd_rope* rope, const void* q,
  *   with strides of its own, rows apart; lse: fp32 [B][hq][m] or NULL.  pos, length: int32
  *   [B] (device), NULL meaning 0 and m.  Rows of tokens t >= length[b] are not written.
  *   scale >= 0.  Scores, sums and the softmax are fp32.  For the product with V the weights
- *   e^{z - m'} (m' from 14 log 2 below the row's largest score so far to 40 log 2 above it)
+ *   e^{z - m'} (m' from 14 log 2 below the row's largest score so far to 46 log 2 above it)
  *   are rounded to bf16, with m = 1 to two bf16 parts (16 bits); lse comes from the sums
  *   before that.
  *   A token that a query does not see reaches nothing of it, whatever its K and V hold
  *   (infinities and NaN included).
  *   Workspace: sd_window_attend_workspace_size() bytes (device, 16-byte aligned; 0 where
  *   none is needed), contents need not be initialised; calls sharing a workspace must not
- *   overlap.
+ *   overlap.  The size does not grow with m: a short chunk whose rows are cut over the
+ *   tokens may need more than a long prompt, so take the largest of the calls in use.
  *   Errors: SD_ERR_INVALID_ARG for a NULL or misaligned pointer (16 bytes; 4 for lse, pos,
  *   length), bad strides, m outside [0, 2^31), first outside [0, n], window < 1, sink < 0,
  *   a scale outside [0, 2.3e38] (scale log2 e is finite, too); SD_ERR_UNSUPPORTED for
