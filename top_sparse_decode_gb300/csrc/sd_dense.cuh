@@ -11,11 +11,8 @@ namespace sd {
 constexpr float kDnLog2e = 1.4426950408889634f;
 constexpr float kDnLn2 = 0.6931471805599453f;
 
-// A kernel launched while the one before it in the stream ends waits here for it.
-__device__ __forceinline__ void dn_wait_prior() {
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-}
-// Launches a kernel that way (it makes no read-only loads), in clusters where cluster > 0.
+// Launches a kernel while the one before it ends (it calls wait_prior and makes no read-only
+// loads), in clusters where cluster > 0.
 template <class P>
 int dn_launch_early(const char* what, void (*kern)(P), unsigned grid, int threads, size_t smem,
                     int cluster, cudaStream_t st, const P& a, bool early = true) {
@@ -95,15 +92,10 @@ __device__ __forceinline__ void dn_row_over(DnRow& r, const uint16_t* K, const u
     r.o.w = fmaf(r.o.w, f, p * v.w);
   }
 }
-__device__ __forceinline__ uint32_t dn_pack(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 __device__ __forceinline__ void dn_row_end(const DnRow& r, uint16_t* out, float* lse, int lane) {
   const float inv = r.l == 0.0f ? 0.0f : 1.0f / r.l;  // a row that sees nothing: 0
   *reinterpret_cast<uint2*>(out + 4 * lane) =
-      make_uint2(dn_pack(r.o.x * inv, r.o.y * inv), dn_pack(r.o.z * inv, r.o.w * inv));
+      make_uint2(bf16_pack(r.o.x * inv, r.o.y * inv), bf16_pack(r.o.z * inv, r.o.w * inv));
   if (lse && lane == 0) *lse = r.l == 0.0f ? -INFINITY : (r.m + log2f(r.l)) * kDnLn2;
 }
 
@@ -221,7 +213,7 @@ __device__ __forceinline__ void dn_eight_step(DnEight& x, const uint32_t (&qa)[8
     const float u = exp2f(z[n][0] - mu), v = exp2f(z[n][1] - mu);
     x.l += u + v;
     p[n] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x7632);
-    rest[n] = dn_pack(fmaxf(u - bf16_lo(p[n]), 0x1p-126f), fmaxf(v - bf16_hi(p[n]), 0x1p-126f));
+    rest[n] = bf16_pack(fmaxf(u - bf16_lo(p[n]), 0x1p-126f), fmaxf(v - bf16_hi(p[n]), 0x1p-126f));
   }
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) {

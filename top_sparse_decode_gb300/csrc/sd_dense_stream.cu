@@ -122,7 +122,7 @@ __device__ __forceinline__ void sw_finish(const SwArgs& a, SwHead x, int b, int 
   const int head = h * G + g;
   const float inv = x.sum == 0.0f ? 0.0f : 1.0f / x.sum;
   *reinterpret_cast<uint2*>(a.out + b * a.oseq + head * a.ohead + 4 * lane) =
-      make_uint2(dn_pack(x.o.x * inv, x.o.y * inv), dn_pack(x.o.z * inv, x.o.w * inv));
+      make_uint2(bf16_pack(x.o.x * inv, x.o.y * inv), bf16_pack(x.o.z * inv, x.o.w * inv));
   if (a.lse && lane == 0)
     a.lse[(int64_t)b * a.Hkv * G + head] =
         x.sum == 0.0f ? -INFINITY : (x.top + log2f(x.sum)) * kDnLn2;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(SwArgs a) {
   dn_cp_wait<0>();
   // behind a prefix's kernel every CTA waits for it, also where a later kernel joins the
   // parts: that one waits for this kernel only
-  if (a.pre) dn_wait_prior();
+  if (a.pre) wait_prior();
 
   // the warp's (m, l, O) into its own part of the ring
   dn_eight_end(x, reinterpret_cast<float*>(ring + warp * kSwStages * kDnStage), G, lane);

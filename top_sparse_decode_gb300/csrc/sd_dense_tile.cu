@@ -424,7 +424,7 @@ __device__ __forceinline__ float tl_weights(uint32_t* pk, const uint32_t* s, flo
     u = tl_exp2(u);
     v = tl_exp2(v);
     sum[i & 1] = tl_add2(sum[i & 1], tl_two(u, v));
-    pk[i] = dn_pack(u, v);
+    pk[i] = bf16_pack(u, v);
   }
   float u, v;
   tl_of(tl_add2(sum[0], sum[1]), u, v);
@@ -696,7 +696,7 @@ __device__ __forceinline__ void tl_softmax(TlSmem& sm, const TlArgs& a, int g, u
           uint32_t y[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            y[i] = dn_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            y[i] = bf16_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
           uint16_t* dst = a.out + orow + 32 * c;
           if (a.wide) {  // whole 32-byte sectors
 #pragma unroll
@@ -1214,7 +1214,7 @@ struct TlJoin {
 __global__ void __launch_bounds__(128) dense_join_kernel(TlJoin a) {
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  dn_wait_prior();
+  wait_prior();
   if (i >= a.rows) return;
   const int64_t m = a.w.m, bhq = i / m, t = i - bhq * m;
   const int64_t b = bhq / a.Hq;

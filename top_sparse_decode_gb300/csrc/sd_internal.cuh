@@ -76,6 +76,16 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
 // low / high bf16 of a packed pair
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// A kernel launched while the one before it in the stream ends waits here for it.
+__device__ __forceinline__ void wait_prior() {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
 
 // order-preserving 32-bit keys: larger score -> larger key
 __device__ __forceinline__ uint32_t key_of_f32(float f) {

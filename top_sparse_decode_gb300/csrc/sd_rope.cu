@@ -8,15 +8,20 @@
 //
 // Bound by HBM: every row is read and written once (512 bytes).  Sixteen lanes take a token
 // and walk heads, 16 bytes of a row a lane, kRpRows rows in flight.  What depends on the
-// token alone is formed once: its angles, since position * inv_freq reaches 10^6 radians as
-// the fraction of a turn, a whole number of 2^-64 per position times the position in 64-bit
+// token alone is formed once.  Its angles, since position * inv_freq reaches 10^6 radians as
+// the fraction of a turn: a whole number of 2^-64 per position, times the position in 64-bit
 // integers, which drop the whole turns by themselves (64-bit floats run at 2 a cycle and SM
-// here); a thread forms a few of the CTA's, through shared memory; and per channel the factors A = w cos t and B = -+ w' sin t, w' the pair's other
-// weight, so that a row's channel is r (x A + x' B) with r the row's norm: the other channel
-// x' comes as it was loaded, from the lane rot / 16 away or (`pairs`) from the same word.
+// here); a thread forms a few of the CTA's, through shared memory.  And per channel the
+// factors A = w cos t and B = -+ w' sin t, w' the pair's other weight, so that a row's channel
+// is r (x A + x' B) with r the row's norm: the other channel x' comes as it was loaded, from
+// the lane rot / 16 away or (`pairs`) from the same word.
+//
 // 4 x 32,768 tokens of 48 heads: 536 us, 6.0 TB/s, 89 % of the measured copy rate.  (With the
-// angles read again and applied after the norm for every row the arithmetic was the bound:
-// 1,064 us.  With angles in 64-bit floats 545, and 64 tokens 7.0 us, 5.8 now.)
+// angles in 64-bit floats 545.  With the angles read again and applied after the norm for
+// every row the arithmetic was the bound: 1,064 us.)  Few tokens pay for it: their first rows
+// are loaded behind the angles and two barriers, and queries, keys and values one after the
+// other.  64 tokens of 48 heads take 5.9 us, 3 x 1,021 of 12 heads 10.8; the kernel of 1,064 us,
+// whose first rows were in flight beside the angles, took 4.8 and 6.0.
 #include "sd_internal.cuh"
 
 namespace sd {
@@ -50,11 +55,6 @@ struct RpArgs {
   int heads_per;     // heads per CTA (of queries, then keys, then values)
 };
 
-__device__ __forceinline__ uint32_t rp_pack(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 __device__ __forceinline__ uint32_t rp_word(const uint4& x, int i) {
   return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
 }
@@ -113,7 +113,7 @@ __device__ __forceinline__ void rp_heads(const uint16_t* src, int64_t sstep, uin
             lo = fmaf(bf16_lo(o), B[2 * i], lo);
             hi = fmaf(bf16_hi(o), B[2 * i + 1], hi);
           }
-          w[i] = rp_pack(lo * r, hi * r);
+          w[i] = bf16_pack(lo * r, hi * r);
         }
         y = make_uint4(w[0], w[1], w[2], w[3]);
       }
