@@ -553,7 +553,8 @@ int sd_qk_norm_rope(const sd_shape* shape, const sd_rope* rope, const void* q,
  *   gives out = 0, lse = -inf.
  *   q: bf16, strides as sd_qk_norm_rope's q; K, V: bf16 [B][hkv][n_cap][d]; out: bf16
  *   with strides of its own, rows apart and apart from q, K and V; lse: fp32 [B][hq][m] or
- *   NULL.  pos, length: int32 [B] (device), NULL meaning 0 and m.  Rows of tokens t >= length[b] are not written.
+ *   NULL.  pos, length: int32 [B] (device), NULL meaning 0 and m.  Rows of tokens
+ *   t >= length[b] are not written.
  *   scale >= 0.  Scores, sums and the softmax are fp32.  For the product with V the weights
  *   e^{z - m'} (m' from 14 log 2 below the row's largest score so far to 46 log 2 above it)
  *   are rounded to bf16, with m = 1 to two bf16 parts (16 bits); lse comes from the sums

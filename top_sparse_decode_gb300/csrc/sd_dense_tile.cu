@@ -42,14 +42,15 @@
 // What bounds it: the chain of a row tile, whose scores' product, two halves of softmax and
 // product with V follow each other; two row tiles in flight keep the tensor pipe busy for some
 // 60 % of the cycles.  32,768 tokens of 32 heads, window 4,096: 1,549 us, 1.37 PFLOP/s, 72 %
-// of the measured bf16 rate; 4 x 4,096 tokens causal: 448 us, 64 %.  What its steps measured
-// on the first of these: products issued by one diverged thread 2,479 us, by a warp 1,934; no
-// maximum before the weights, products back to back 1,857; rows that are not finite found in
-// O, not by a search of V, 1,777; halves 1,757; the masked softmax out of line 1,603 (before
-// that the code did not fit the instruction cache: its misses ran at 67 % of what the cache
-// behind it gives, now 18 %); the products unrolled again 1,549.  Slower: the maximum and the
-// weights by 32 columns with a vote each (2,125), the weights again by a loop around the same
-// code (2,179), the softmax groups looking for landed tiles in the issuing warp's place
+// of the measured bf16 rate; 4 x 4,096 tokens causal: 447 us, 64 % (items go to CTAs by a fixed
+// stride from the largest down: the busiest has 1.07 times the mean's work).  What its steps
+// measured on the first of these: products issued by one diverged thread 2,479 us, by a warp
+// 1,934; no maximum before the weights, products back to back 1,857; rows that are not finite
+// found in O, not by a search of V, 1,777; halves 1,757; the masked softmax out of line 1,603
+// (before that the code did not fit the instruction cache: its misses ran at 67 % of what the
+// cache behind it gives, now 18 %); the products unrolled again 1,549.  Slower: the maximum and
+// the weights by 32 columns with a vote each (2,125), the weights again by a loop around the
+// same code (2,179), the softmax groups looking for landed tiles in the issuing warp's place
 // (1,637), a barrier for PV at an item's end only and stages released behind QK (1,602).
 //
 // Every wait is bounded: one that runs out sets the library's error word (sd_device_status)
