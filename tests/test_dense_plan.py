@@ -3,6 +3,7 @@ for the host: every cut covers its work, fits its workspace, and leaves no SM wi
 where there is work for it."""
 import ctypes
 import os
+import re
 import shutil
 import subprocess
 
@@ -38,6 +39,19 @@ def plan(tmp_path_factory):
         fn(*args, out)
         return list(out)
     return (lambda *a: call(dll.tile, 4, *a)), (lambda *a: call(dll.stream, 3, *a))
+
+
+def test_early_kernels_use_ordinary_loads():
+    """Kernels that are launched while their producer runs (dn_wait_prior) make no read-only
+    loads: those are not ordered by the wait."""
+    early = []
+    for name in sorted(os.listdir(CSRC)):
+        with open(os.path.join(CSRC, name)) as f:
+            code = re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+        if "dn_wait_prior" in code:
+            early.append(name)
+            assert not re.search(r"__ldg\b|ld\.global\.nc|__restrict__", code), name
+    assert {"sd_dense.cuh", "sd_dense_stream.cu", "sd_dense_tile.cu"} <= set(early)
 
 
 @pytest.mark.parametrize("sms", [1, 20, 152])

@@ -11,8 +11,12 @@ namespace sd {
 constexpr float kDnLog2e = 1.4426950408889634f;
 constexpr float kDnLn2 = 0.6931471805599453f;
 
-// Launches a kernel while the one before it ends (it calls wait_prior and makes no read-only
-// loads), in clusters where cluster > 0.
+// A kernel launched while the one before it in the stream ends waits here for it.  (In a place
+// and under a name of its own: the kernels that use it are held to ordinary loads by name.)
+__device__ __forceinline__ void dn_wait_prior() {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+// Launches a kernel that way (it makes no read-only loads), in clusters where cluster > 0.
 template <class P>
 int dn_launch_early(const char* what, void (*kern)(P), unsigned grid, int threads, size_t smem,
                     int cluster, cudaStream_t st, const P& a, bool early = true) {

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kSwThreads, 2) dense_stream_kernel(SwArgs a) {
   dn_cp_wait<0>();
   // behind a prefix's kernel every CTA waits for it, also where a later kernel joins the
   // parts: that one waits for this kernel only
-  if (a.pre) wait_prior();
+  if (a.pre) dn_wait_prior();
 
   // the warp's (m, l, O) into its own part of the ring
   dn_eight_end(x, reinterpret_cast<float*>(ring + warp * kSwStages * kDnStage), G, lane);

@@ -1215,7 +1215,7 @@ struct TlJoin {
 __global__ void __launch_bounds__(128) dense_join_kernel(TlJoin a) {
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  wait_prior();
+  dn_wait_prior();
   if (i >= a.rows) return;
   const int64_t m = a.w.m, bhq = i / m, t = i - bhq * m;
   const int64_t b = bhq / a.Hq;

@@ -82,11 +82,6 @@ __device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
   return d;
 }
 
-// A kernel launched while the one before it in the stream ends waits here for it.
-__device__ __forceinline__ void wait_prior() {
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-}
-
 // order-preserving 32-bit keys: larger score -> larger key
 __device__ __forceinline__ uint32_t key_of_f32(float f) {
   uint32_t u = __float_as_uint(f);

@@ -82,7 +82,7 @@ struct KvLane {
 };
 
 __global__ void __launch_bounds__(32 * kKvWarps) kv4_write_kernel(const KvMoveArgs a) {
-  wait_prior();
+  kv4_wait_prior();
   const KvLane L(a);
   const bool asked = a.x[L.half] != nullptr;
   const int64_t st = a.st[L.half];
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv4_write_kernel(const KvMoveAr
 }
 
 __global__ void __launch_bounds__(32 * kKvWarps) kv4_read_kernel(const KvMoveArgs a) {
-  wait_prior();
+  kv4_wait_prior();
   const KvLane L(a);
   const int64_t st = a.st[L.half];
   uint16_t* dst = a.x[L.half] + L.x + L.t * st;

@@ -793,7 +793,7 @@ __device__ __forceinline__ void ka_write(const KaArgs& a, int64_t bq, int j, flo
 template <int G, bool GATHER>
 __global__ void __launch_bounds__(kKaThreads, 2) kv4_cluster_kernel(const KaArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  wait_prior();
+  kv4_wait_prior();
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), CS = (int)cl.num_blocks();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1085,7 +1085,7 @@ __global__ void __launch_bounds__(32 * kKaJoinWarps) kv4_join_kernel(const KaArg
   __shared__ float4 so[kKaJoinWarps][32];
   __shared__ float2 sml[kKaJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  wait_prior();  // the streaming kernel
+  kv4_wait_prior();  // the streaming kernel
   const int64_t pairs = a.rows * G;
   for (int64_t base = (int64_t)blockIdx.x * run; base < pairs; base += (int64_t)gridDim.x * run) {
     const int64_t mine = base + warp;
