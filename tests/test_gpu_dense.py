@@ -370,6 +370,22 @@ def test_prefix_bad_value(sd, bad):
     assert int((~torch.isfinite(got[5].float())).sum()) == 17 * 8 + 8
 
 
+@pytest.mark.parametrize("m", [1, 20, 200])
+def test_window_largest_values_without_weight(sd, m):
+    """The largest values of V, at tokens whose weights are 0 in fp32, are not seen in out."""
+    n = 600
+    case = (1, 2, 4, n, n, m, n - m, None, None, n, 0)
+
+    def spoil(q, K, V):
+        q[..., 0] = 8.0
+        K[..., 0] = 0.0
+        K[:, :, 5:n - m:40, 0] = -400.0  # scores some 280 below the others'
+        V[:, :, 5:n - m:40] = 3.3e38
+    got = run_window(sd, *case, prep=spoil)
+    assert got[3].float().abs().max() < 10
+    check_window(case, got)
+
+
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 @pytest.mark.parametrize("n", [1, 40, 600, 9000])
 def test_single_token_bad_value(sd, n, bad):

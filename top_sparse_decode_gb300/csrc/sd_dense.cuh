@@ -210,14 +210,16 @@ __device__ __forceinline__ void dn_eight_step(DnEight& x, const uint32_t (&qa)[8
   }
   const float mu = x.m == -INFINITY ? 0.0f : x.m;
   // a weight as two bf16, its upper half and what that leaves: 16 bits of it.  Neither part is
-  // negative, and the second not 0 either, so that an infinity in V stays what it is.
+  // negative, and the second is a 2^17th of the weight at least (0 only below 2^-116), so that
+  // an infinity in V stays what it is and a weight of 0 stays 0.
   uint32_t p[2], rest[2];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const float u = exp2f(z[n][0] - mu), v = exp2f(z[n][1] - mu);
     x.l += u + v;
     p[n] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x7632);
-    rest[n] = bf16_pack(fmaxf(u - bf16_lo(p[n]), 0x1p-126f), fmaxf(v - bf16_hi(p[n]), 0x1p-126f));
+    rest[n] = bf16_pack(fmaxf(u - bf16_lo(p[n]), u * 0x1p-17f),
+                        fmaxf(v - bf16_hi(p[n]), v * 0x1p-17f));
   }
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) {
