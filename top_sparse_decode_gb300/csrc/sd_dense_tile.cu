@@ -16,7 +16,10 @@
 // rounded to bf16 into the columns that S held, O += P V (P from tensor memory, V as it
 // lies), by halves of 64 tokens: the first half's product runs beside the second half's
 // weights.  The rounding of p costs as much as that of the bf16 result (out is 1.4 times as
-// far from 64 bits); l and lse are of the sums before it.
+// far from 64 bits, up to 1.6); l and lse are of the sums before it.  A second product with
+// what it cut off (both parts in the columns of S) took that error away and cost every prompt:
+// 32,768 tokens under a window of 4,096 2,117 us (1,546 without), 4 x 4,096 causal 588 (447),
+// 3 x 257 21.5 (18.5), a prefix of 131,072 for 128 294 (229).
 //
 // The reference m begins at 0 and stands as long as half a tile's weights sum up to 2^14 at
 // most and a row's so far to 2^-40 at least: a weight's rounding is relative to itself, so any
